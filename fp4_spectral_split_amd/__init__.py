@@ -15,6 +15,12 @@ Calls (same names as the C ABI in include/metis_fp4.h):
   spectral_fp4_linear_bwd(dY, X, W)            -> (dX = dY W, dW = dY^T X)
   metis_spectral_lr_rescale(G, rec, r, gmax)   -> G rescaled in place
   metis_dual_range_reg(W, ...)                 -> (loss, grad)
+  act8_block_quant(x, fmt)                     -> Act8Tensor (8-bit storage)
+  act8_block_dequant(q, dtype)                 -> fp32 or bf16 tensor
+  metis_norm_fwd(x, weight, bias, kind)        -> (y, mean, rstd, stored x)
+  metis_norm_bwd(dy, x, weight, mean, rstd)    -> (dx, dweight, dbias)
+  metis_swiglu_fwd(a, b)                       -> (silu(a) b, stored a, stored b)
+  metis_swiglu_bwd(dh, a, b)                   -> (da, db, silu(a) b)
 """
 import ctypes
 import os
@@ -32,6 +38,12 @@ OMEGA_GAUSSIAN, OMEGA_COLUMNS = 0, 1
 _FMT = {"mxfp4": MXFP4, "nvfp4": NVFP4, MXFP4: MXFP4, NVFP4: NVFP4}
 _FMT_NAME = {MXFP4: "mxfp4", NVFP4: "nvfp4"}
 BLOCK = {MXFP4: 32, NVFP4: 16}
+MXFP8, MXINT8 = 2, 3
+BLOCK8 = 32
+NORM_LAYER, NORM_RMS = 0, 1
+_FMT8 = {"mxfp8": MXFP8, "mxint8": MXINT8, MXFP8: MXFP8, MXINT8: MXINT8}
+_FMT8_NAME = {MXFP8: "mxfp8", MXINT8: "mxint8"}
+_KIND = {"layer": NORM_LAYER, "rms": NORM_RMS, NORM_LAYER: NORM_LAYER, NORM_RMS: NORM_RMS}
 
 
 class MetisError(RuntimeError):
@@ -48,6 +60,11 @@ class _Split(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("U", ctypes.c_void_p), ("S", ctypes.c_void_p), ("V", ctypes.c_void_p),
                 ("Ut_q", _Fp4), ("Vt_q", _Fp4), ("R_q", _Fp4), ("Rt_q", _Fp4)]
+
+
+class _Act8(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -106,6 +123,23 @@ def load():
     L.metis_gemm_nt_prepare.argtypes = [sp, i32, sp, i32, vp, sz, vp]
     L.metis_gemm_nt_main.restype = i32
     L.metis_gemm_nt_main.argtypes = [sp, i32, sp, i32, vp, i64, vp, sz, vp]
+    q8, f32 = ctypes.POINTER(_Act8), ctypes.c_float
+    L.act8_block_quant.restype = i32
+    L.act8_block_quant.argtypes = [vp, i32, i64, i64, i64, q8, vp]
+    L.act8_block_dequant.restype = i32
+    L.act8_block_dequant.argtypes = [q8, vp, i32, i64, vp]
+    L.metis_norm_fwd.restype = i32
+    L.metis_norm_fwd.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i32, f32, vp, i32, i64, vp, vp, q8, vp]
+    L.metis_norm_bwd_workspace_bytes.restype = sz
+    L.metis_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    L.metis_norm_bwd.restype = i32
+    L.metis_norm_bwd.argtypes = [vp, i32, i64, vp, i32, i64, q8, vp, i32, i32, vp, vp, i64, i64, vp, i32, i64, vp, vp,
+                                 i32, vp, sz, vp]
+    L.metis_swiglu_fwd.restype = i32
+    L.metis_swiglu_fwd.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, q8, q8, vp]
+    L.metis_swiglu_bwd.restype = i32
+    L.metis_swiglu_bwd.argtypes = [vp, i32, i64, vp, i64, vp, i64, i32, q8, q8, i64, i64, vp, i64, vp, i64, vp, i64,
+                                   i32, vp]
     _lib = L
     return L
 
@@ -116,7 +150,9 @@ EXPORTS = ["metis_status_str", "metis_abi_version", "fp4_block_quant_workspace_b
            "metis_mean_split", "metis_linear_workspace_bytes",
            "spectral_fp4_linear_fwd", "spectral_fp4_linear_fwd_noalloc", "spectral_fp4_linear_bwd", "metis_gemm_nt_workspace_bytes",
            "metis_gemm_nt_prepare", "metis_gemm_nt_main", "metis_spectral_lr_rescale",
-           "metis_dual_range_workspace_bytes", "metis_dual_range_reg"]
+           "metis_dual_range_workspace_bytes", "metis_dual_range_reg", "act8_block_quant", "act8_block_dequant",
+           "metis_norm_fwd", "metis_norm_bwd_workspace_bytes", "metis_norm_bwd", "metis_swiglu_fwd",
+           "metis_swiglu_bwd"]
 
 
 def _check(status):
@@ -437,3 +473,286 @@ def metis_dual_range_reg(W, tau_lo, tau_hi, lam_lo, lam_hi, grad=None, accumulat
                                   grad.stride(0) if want_grad else 0, int(bool(accumulate)), _ptr(loss), _ptr(ws), nws,
                                   _stream(W.device)))
     return loss, grad
+
+
+# ------------------------------------- norm, gate and 8-bit activation storage
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _code(dtype):
+    c = _DTYPE.get(dtype)
+    if c is None:
+        raise MetisError("tensors must be float32 or bfloat16, got %s" % dtype)
+    return c
+
+
+def _matrix(t, name, shape=None, device=None):
+    """Checks a 2-D CUDA tensor with contiguous rows; returns its leading
+    dimension in elements."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+        raise MetisError("%s must be a 2-D CUDA tensor" % name)
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise MetisError("%s must be %d x %d, got %d x %d" % (name, shape[0], shape[1], rows, cols))
+    if device is not None and t.device != device:
+        raise MetisError("%s is on %s, the other operands on %s" % (name, t.device, device))
+    if cols > 1 and t.stride(1) != 1:
+        raise MetisError("the rows of %s must be contiguous" % name)
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, name, n, device, dtype=None):
+    """Checks an optional contiguous CUDA vector of n elements."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise MetisError("%s must be a contiguous vector of %d elements" % (name, n))
+    if t.device != device:
+        raise MetisError("%s is on %s, the other operands on %s" % (name, t.device, device))
+    if dtype is not None and t.dtype != dtype:
+        raise MetisError("%s must be %s" % (name, dtype))
+
+
+def _on(device, call):
+    """call(stream) with the tensors' device as the current one (a launch goes
+    to the current device, whatever device its operands are on)."""
+    if torch.cuda.current_device() == device.index:
+        _check(call(_stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(device)))
+
+
+@dataclass
+class Act8Tensor:
+    """rows x cols matrix in 8 bits, blocks of 32 along cols (see metis_act8_t)."""
+    fmt: int
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def empty(fmt, rows, cols, device):
+        return Act8Tensor(_fmt8(fmt), rows, cols, torch.empty(rows, cols, dtype=torch.uint8, device=device),
+                          torch.empty(rows, -(-cols // BLOCK8), dtype=torch.uint8, device=device))
+
+    @staticmethod
+    def from_codes(fmt, codes, scales):
+        """The record of given codes (rows x cols) and scale bytes (rows x
+        ceil(cols / 32))."""
+        q = Act8Tensor(_fmt8(fmt), codes.shape[0], codes.shape[1], codes, scales)
+        _stored(q, "codes", tuple(codes.shape), codes.device)
+        return q
+
+    def c(self):
+        return _Act8(self.fmt, 0, self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr())
+
+    @property
+    def fmt_name(self):
+        return _FMT8_NAME[self.fmt]
+
+
+def _fmt8(fmt):
+    f = _FMT8.get(fmt)
+    if f is None:
+        raise MetisError("8-bit format must be mxfp8 or mxint8, got %r" % (fmt,))
+    return f
+
+
+def _stored(q, name, shape, device):
+    """Checks an Act8Tensor: its buffers hold the matrix it says, on the device."""
+    rows, cols = shape
+    if (q.rows, q.cols) != (rows, cols):
+        raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
+    for buf, n in ((q.codes, rows * cols), (q.scales, rows * -(-cols // BLOCK8))):
+        if buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() != n or not buf.is_cuda:
+            raise MetisError("%s needs contiguous uint8 CUDA codes and scales of its size" % name)
+        if buf.device != device:
+            raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))
+    return q
+
+
+def _save(save, shape, device):
+    """The Act8Tensor to store into: a new one of a named format, the one
+    given, or None."""
+    if save is None:
+        return None
+    if isinstance(save, Act8Tensor):
+        return _stored(save, "save", shape, device)
+    return Act8Tensor.empty(save, shape[0], shape[1], device)
+
+
+def _out(out, name, shape, dtype, device):
+    """An output tensor (new where none is given) and its leading dimension."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    if out.dtype != dtype:
+        raise MetisError("%s must be %s" % (name, dtype))
+    return out, _matrix(out, name, shape, device)
+
+
+def act8_block_quant(x, fmt="mxfp8", out=None):
+    """Store a 2-D fp32/bf16 CUDA tensor (any width, rows contiguous) in 8
+    bits: MXFP8 (E4M3) or MXINT8 codes with one scale per 32 elements."""
+    ld = _matrix(x, "x")
+    if out is None:
+        out = Act8Tensor.empty(fmt, x.shape[0], x.shape[1], x.device)
+    else:
+        _stored(out, "out", tuple(x.shape), x.device)
+        if out.fmt != _fmt8(fmt):
+            raise MetisError("out is of another format")
+    c = out.c()
+    L, dt = load(), _code(x.dtype)
+    _on(x.device, lambda s: L.act8_block_quant(x.data_ptr(), dt, x.shape[0], x.shape[1], ld, c, s))
+    return out
+
+
+def act8_block_dequant(q, dtype=torch.float32, out=None):
+    """The values of an Act8Tensor as fp32 or bf16 (both hold them exactly)."""
+    dev = q.codes.device
+    _stored(q, "q", (q.rows, q.cols), dev)
+    dt = _code(dtype)
+    out, ld = _out(out, "out", (q.rows, q.cols), dtype, dev)
+    c, L = q.c(), load()
+    _on(dev, lambda s: L.act8_block_dequant(c, out.data_ptr(), dt, ld, s))
+    return out
+
+
+def _norm_kind(kind):
+    k = _KIND.get(kind)
+    if k is None:
+        raise MetisError("norm kind must be layer or rms, got %r" % (kind,))
+    return k
+
+
+def metis_norm_fwd(x, weight=None, bias=None, kind="layer", eps=1e-5, dtype=None, save=None, out=None):
+    """Layer ("layer") or RMS ("rms") norm of the rows of a 2-D fp32/bf16 CUDA
+    tensor: (y, mean, rstd, stored). y is of type `dtype` (default: x's); mean
+    (None for RMS) and rstd are fp32, one per row. save: "mxfp8" / "mxint8" or
+    an Act8Tensor to write into: x in 8 bits for the backward pass, as stored."""
+    ldx = _matrix(x, "x")
+    dev, shape = x.device, tuple(x.shape)
+    k, dt = _norm_kind(kind), _code(x.dtype)
+    _vector(weight, "weight", shape[1], dev)
+    _vector(bias, "bias", shape[1], dev, weight.dtype if weight is not None else None)
+    wt = weight if weight is not None else bias
+    wdt = _code(wt.dtype) if wt is not None else F32
+    dtype = x.dtype if dtype is None else dtype
+    ydt = _code(dtype)
+    y, ldy = _out(out, "out", shape, dtype, dev)
+    mean = torch.empty(shape[0], dtype=torch.float32, device=dev) if k == NORM_LAYER else None
+    rstd = torch.empty(shape[0], dtype=torch.float32, device=dev)
+    stored = _save(save, shape, dev)
+    c = stored.c() if stored is not None else None
+    L = load()
+    _on(dev, lambda s: L.metis_norm_fwd(x.data_ptr(), dt, shape[0], shape[1], ldx, _ptr(weight), _ptr(bias), wdt, k,
+                                        eps, y.data_ptr(), ydt, ldy, _ptr(mean), rstd.data_ptr(), c, s))
+    return y, mean, rstd, stored
+
+
+def metis_norm_bwd(dy, x, weight, mean, rstd, kind="layer", dtype=None, need_dweight=True, need_dbias=None,
+                   dweight=None, dbias=None, accumulate=False, out=None):
+    """Gradients of metis_norm_fwd: (dx, dweight, dbias). x: the forward's
+    input, dense or as the Act8Tensor it stored; mean and rstd: as it returned
+    them. dx is of type `dtype` (default: dy's); dweight and dbias are fp32
+    (need_dbias defaults to the layer norm), added to the tensors given with
+    accumulate=True."""
+    lddy = _matrix(dy, "dy")
+    dev, shape = dy.device, tuple(dy.shape)
+    k, dydt = _norm_kind(kind), _code(dy.dtype)
+    if isinstance(x, Act8Tensor):
+        q, xp, xdt, ldx = _stored(x, "x", shape, dev).c(), None, F32, 0
+    else:
+        ldx = _matrix(x, "x", shape, dev)
+        q, xp, xdt = None, x.data_ptr(), _code(x.dtype)
+    _vector(weight, "weight", shape[1], dev)
+    if rstd is None or (k == NORM_LAYER and mean is None):
+        raise MetisError("the backward pass needs the forward's rstd, and for a layer norm its mean")
+    _vector(rstd, "rstd", shape[0], dev, torch.float32)
+    if k == NORM_RMS:
+        mean = None
+    _vector(mean, "mean", shape[0], dev, torch.float32)
+    dtype = dy.dtype if dtype is None else dtype
+    dxdt = _code(dtype)
+    if need_dbias is None:
+        need_dbias = k == NORM_LAYER
+    if accumulate and ((need_dweight and dweight is None) or (need_dbias and dbias is None)):
+        raise MetisError("accumulate needs the gradients to add to")
+    dx, lddx = _out(out, "out", shape, dtype, dev)
+    grads = []
+    for need, g, name in ((need_dweight, dweight, "dweight"), (need_dbias, dbias, "dbias")):
+        if need and g is None:
+            g = torch.empty(shape[1], dtype=torch.float32, device=dev)
+        _vector(g, name, shape[1], dev, torch.float32)
+        grads.append(g if need else None)
+    dw, db = grads
+    L = load()
+    # the partial sums live in a buffer of their own per call: a captured call
+    # keeps it in its graph's memory, so two graphs never share one
+    nws = L.metis_norm_bwd_workspace_bytes(shape[0], shape[1]) if need_dweight or need_dbias else 0
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    wdt = _code(weight.dtype) if weight is not None else F32
+    _on(dev, lambda s: L.metis_norm_bwd(dy.data_ptr(), dydt, lddy, xp, xdt, ldx, q, _ptr(weight), wdt, k, _ptr(mean),
+                                        rstd.data_ptr(), shape[0], shape[1], dx.data_ptr(), dxdt, lddx, _ptr(dw),
+                                        _ptr(db), int(bool(accumulate)), _ptr(ws), nws, s))
+    return dx, dw, db
+
+
+def metis_swiglu_fwd(a, b, dtype=None, save=None, out=None):
+    """h = silu(a) b of two 2-D fp32/bf16 CUDA tensors of one type (also the
+    two halves of one matrix): (h, stored a, stored b). h is of type `dtype`
+    (default: a's). save: "mxfp8" / "mxint8" or a pair of Act8Tensors: a and b
+    in 8 bits for the backward pass."""
+    lda = _matrix(a, "a")
+    dev, shape = a.device, tuple(a.shape)
+    ldb = _matrix(b, "b", shape, dev)
+    if a.dtype != b.dtype:
+        raise MetisError("a and b must be of one type")
+    dt = _code(a.dtype)
+    dtype = a.dtype if dtype is None else dtype
+    hdt = _code(dtype)
+    h, ldh = _out(out, "out", shape, dtype, dev)
+    if isinstance(save, (tuple, list)):
+        if len(save) != 2 or not all(isinstance(q, Act8Tensor) for q in save):
+            raise MetisError("save must be a format or a pair of Act8Tensors")
+        qa, qb = (_save(q, shape, dev) for q in save)
+    elif isinstance(save, Act8Tensor):
+        raise MetisError("save must be a format or a pair of Act8Tensors")
+    else:
+        qa, qb = _save(save, shape, dev), _save(save, shape, dev)
+    ca, cb = (qa.c(), qb.c()) if qa is not None else (None, None)
+    L = load()
+    _on(dev, lambda s: L.metis_swiglu_fwd(a.data_ptr(), lda, b.data_ptr(), ldb, dt, shape[0], shape[1], h.data_ptr(),
+                                          hdt, ldh, ca, cb, s))
+    return h, qa, qb
+
+
+def metis_swiglu_bwd(dh, a, b, dtype=None, need_h=False, da=None, db=None, h=None):
+    """Gradients of metis_swiglu_fwd: (da, db, h). a and b: its inputs, dense or
+    as the Act8Tensors it stored. da and db are of type `dtype` (default:
+    dh's), as is h = silu(a) b, rebuilt where need_h is set (else None)."""
+    lddh = _matrix(dh, "dh")
+    dev, shape = dh.device, tuple(dh.shape)
+    dhdt = _code(dh.dtype)
+    if isinstance(a, Act8Tensor) != isinstance(b, Act8Tensor):
+        raise MetisError("a and b must both be dense or both stored")
+    if isinstance(a, Act8Tensor):
+        qa, qb = _stored(a, "a", shape, dev).c(), _stored(b, "b", shape, dev).c()
+        ap = bp = None
+        lda, ldb, dt = shape[1], shape[1], F32
+    else:
+        lda, ldb = _matrix(a, "a", shape, dev), _matrix(b, "b", shape, dev)
+        if a.dtype != b.dtype:
+            raise MetisError("a and b must be of one type")
+        qa = qb = None
+        ap, bp, dt = a.data_ptr(), b.data_ptr(), _code(a.dtype)
+    dtype = dh.dtype if dtype is None else dtype
+    odt = _code(dtype)
+    da, ldda = _out(da, "da", shape, dtype, dev)
+    db, lddb = _out(db, "db", shape, dtype, dev)
+    h, ldh = _out(h, "h", shape, dtype, dev) if need_h else (None, shape[1])
+    L = load()
+    _on(dev, lambda s: L.metis_swiglu_bwd(dh.data_ptr(), dhdt, lddh, ap, lda, bp, ldb, dt, qa, qb, shape[0], shape[1],
+                                          da.data_ptr(), ldda, db.data_ptr(), lddb, _ptr(h), ldh, odt, s))
+    return da, db, h

@@ -1,0 +1,327 @@
+// 8-bit block storage of activations: device codec and chunked row access.
+//
+// Number formats: the MX forms with 8-bit elements and one E8M0 scale per 32
+// (OCP Microscaling Formats v1.0 §5.3): MXFP8 with E4M3 elements, MXINT8 with
+// two's complement elements in units of 1/64.
+//
+// Scale rule: the smallest exponent e >= -127 for which the block's largest
+// magnitude does not exceed the largest element times 2^e (448, 127/64). The
+// floor rule of §6.3 that the FP4 blocks use would clip magnitudes between
+// 448 and 512 (127/64 and 2) units of the scale, an error of up to 1/8 of the
+// largest values; with this rule every element is off by half a step at most.
+//
+// A row is worked on in chunks of eight elements, one per lane: a 16-byte
+// load of bf16, two of fp32, eight bytes of codes. Four neighbouring lanes
+// hold one block, so its maximum takes two DPP steps and no LDS.
+#pragma once
+#include "common.hpp"
+
+namespace metis {
+
+// What a kernel reads: a dense matrix or the 8-bit form.
+enum : int { kDense = 0, kFp8 = METIS_MXFP8, kInt8 = METIS_MXINT8 };
+
+constexpr int kBlock8 = 32;  // elements under one scale
+constexpr int kChunk = 8;    // elements a lane holds of a row
+
+// Rows need not be aligned beyond their element type: the hardware takes
+// 16-byte accesses at any address, and these types make the compiler use them.
+typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef short shortx2 __attribute__((ext_vector_type(2)));
+
+// ------------------------------------------------------- chunks of a row
+template <typename T> struct Raw;  // a chunk as loaded
+template <> struct Raw<float> { uint32_t w[8]; };
+template <> struct Raw<unsigned short> { uint32_t w[4]; };
+template <> struct Raw<uint8_t> { uint32_t w[2]; };
+
+// The chunk at p; of a row's last chunk only n elements exist (zeros follow).
+__device__ __forceinline__ void load_raw(const float *p, int n, Raw<float> &r) {
+  if (n >= kChunk) {
+    const u32x4_a1 a = *(const u32x4_a1 *)p, b = *(const u32x4_a1 *)(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.w[i] = a[i];
+      r.w[4 + i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+  }
+}
+__device__ __forceinline__ void load_raw(const unsigned short *p, int n, Raw<unsigned short> &r) {
+  if (n >= kChunk) {
+    const u32x4_a1 a = *(const u32x4_a1 *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = a[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+  }
+}
+__device__ __forceinline__ void load_raw(const uint8_t *p, int n, Raw<uint8_t> &r) {
+  if (n >= kChunk) {
+    const u32x2_a1 a = *(const u32x2_a1 *)p;
+    r.w[0] = a[0];
+    r.w[1] = a[1];
+  } else {
+    r.w[0] = r.w[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) r.w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+  }
+}
+
+__device__ __forceinline__ void to_f32(const Raw<float> &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void to_f32(const Raw<unsigned short> &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+  }
+}
+
+// n of the eight values to p, bf16 rounded to nearest even (NaN stays NaN).
+__device__ __forceinline__ void store_chunk(float *p, const float (&v)[8], int n) {
+  if (n >= kChunk) {
+    u32x4_a1 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = __float_as_uint(v[i]);
+      b[i] = __float_as_uint(v[4 + i]);
+    }
+    *(u32x4_a1 *)p = a;
+    *(u32x4_a1 *)(p + 4) = b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  bf16x2 b;
+  b[0] = (__bf16)lo;
+  b[1] = (__bf16)hi;
+  return __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ void store_chunk(unsigned short *p, const float (&v)[8], int n) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if (n >= kChunk) {
+    u32x4_a1 a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = w[i];
+    *(u32x4_a1 *)p = a;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (unsigned short)(w[i / 2] >> (16 * (i % 2)));
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, uint32_t lo, uint32_t hi, int n) {
+  if (n >= kChunk) {
+    u32x2_a1 a;
+    a[0] = lo;
+    a[1] = hi;
+    *(u32x2_a1 *)p = a;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4)));
+  }
+}
+
+// ------------------------------------------------------------------ codec
+// The bits of the largest magnitude of a chunk. Magnitudes order like their
+// bits; a NaN orders above infinity and so is not lost, as it would be in a
+// floating-point maximum.
+__device__ __forceinline__ uint32_t amax_bits(const Raw<float> &r) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, r.w[i] & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ uint32_t amax_bits(const Raw<unsigned short> &r) {
+  typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+  ushortx2 m = __builtin_bit_cast(ushortx2, r.w[0] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(ushortx2, r.w[i] & 0x7FFF7FFFu));
+  return (uint32_t)max(m[0], m[1]) << 16;
+}
+
+// The maximum over the four lanes of a quad (all of them active).
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+}
+
+// E8M0 byte (e + 127) of a block from the bits of its largest magnitude; 255
+// (NaN) for a block that holds an infinity or a NaN. Adding the distance from
+// the largest element's mantissa to the next power of two carries into the
+// exponent field exactly where e has to be one larger.
+template <int FMT> __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  uint32_t byte;
+  if (FMT == kFp8) {
+    byte = max((amax + 0x1FFFFFu) >> 23, 8u) - 8u;  // 448 = 1.75 * 2^8
+  } else {
+    // 127/64 = 1.984375; a subnormal amax has no leading one, its limit
+    // 127/64 * 2^-127 is 0x7F0000 units
+    byte = min((amax + (amax < 0x800000u ? 0xFFFFu : 0x1FFFFu)) >> 23, 254u);
+  }
+  return amax >= 0x7F800000u ? 255u : byte;
+}
+
+// 2^(byte - 127); 255 gives NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  const uint32_t b = byte << 23;
+  return __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7FC00000u : b));
+}
+
+// Codes of a chunk under its block's scale.
+template <int FMT>
+__device__ __forceinline__ void encode(const float (&v)[8], uint32_t byte, uint32_t &lo, uint32_t &hi) {
+  if (FMT == kFp8) {
+    // the conversion divides by its scale operand before it rounds to nearest
+    // even, which is exact for a power of two; the scale rule leaves nothing
+    // to saturate
+    const float s = scale_value(byte);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      shortx2 r = {0, 0};
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * h], v[4 * h + 1], s, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * h + 2], v[4 * h + 3], s, true);
+      w[h] = byte == 255u ? 0x7F7F7F7Fu : __builtin_bit_cast(uint32_t, r);
+    }
+    lo = w[0];
+    hi = w[1];
+  } else {
+    // x / 2^e is exact; the fused multiply-add rounds its product with 64
+    // once, at the unit of the added 1.5 * 2^23, to nearest even, and leaves
+    // the two's complement integer in the low bits. A magnitude at the top of
+    // fp32's range, for which e would be 128, is held at 127.
+    const float inv = __uint_as_float(byte >= 254u ? 0x00400000u : (254u - byte) << 23);
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = __builtin_amdgcn_fmed3f(v[i] * inv, -1.984375f, 1.984375f);
+      b[i] = __float_as_uint(fmaf(q, 64.0f, 12582912.0f));
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t p = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u);
+      const uint32_t q = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000C0Cu);
+      w[h] = byte == 255u ? 0u : (p | q);
+    }
+    lo = w[0];
+    hi = w[1];
+  }
+}
+
+// Values of a chunk of codes; exact in fp32.
+template <int FMT>
+__device__ __forceinline__ void decode(const Raw<uint8_t> &r, uint32_t byte, float (&v)[8]) {
+  const float s = scale_value(byte);
+  if (FMT == kFp8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const floatx2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r.w[h], s, false);
+      const floatx2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r.w[h], s, true);
+      v[4 * h] = a[0];
+      v[4 * h + 1] = a[1];
+      v[4 * h + 2] = b[0];
+      v[4 * h + 3] = b[1];
+    }
+  } else {
+    const float u = s * 0.015625f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = (float)(int)(int8_t)(r.w[h] >> (8 * i)) * u;
+  }
+}
+
+// ----------------------------------------------------------- row sources
+// A chunk of a matrix that is dense (SRC = kDense, elements of type T) or in
+// the 8-bit form (codes with their scales, tightly packed rows).
+template <int SRC, typename T> struct Chunk {
+  Raw<T> raw;
+  __device__ __forceinline__ void load(const void *p, const uint8_t *, int64_t r, int64_t ld, int, int c, int n) {
+    load_raw((const T *)p + r * ld + c, n, raw);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { to_f32(raw, v); }
+};
+template <typename T> struct Chunk<kFp8, T> {
+  Raw<uint8_t> raw;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int c,
+                                       int n) {
+    load_raw((const uint8_t *)p + r * ld + c, n, raw);
+    byte = n > 0 ? scales[r * nblk + c / kBlock8] : 0u;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { decode<kFp8>(raw, byte, v); }
+};
+template <typename T> struct Chunk<kInt8, T> {
+  Raw<uint8_t> raw;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int c,
+                                       int n) {
+    load_raw((const uint8_t *)p + r * ld + c, n, raw);
+    byte = n > 0 ? scales[r * nblk + c / kBlock8] : 0u;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { decode<kInt8>(raw, byte, v); }
+};
+
+// ------------------------------------------------------------- positions
+// n / d for n < 2^29 by a multiply-high: m = ceil(2^(29 + l) / d) with
+// l = ceil(log2 d), whose excess over the exact quotient stays below 1 / d for
+// every n < 2^29.
+struct FastDiv {
+  uint32_t d, m, sh;
+  __host__ void set(uint32_t div) {
+    d = div;
+    uint32_t l = 0;
+    while ((1ull << l) < div) ++l;
+    const uint32_t up = l < 3u ? 3u - l : 0u;  // at least 32 bits to shift by
+    m = div == 1u ? 0u : (uint32_t)((((1ull << (29 + l)) + div - 1) / div) << up);
+    sh = l + up - 3u;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d == 1u ? n : __umulhi(n, m) >> sh; }
+};
+
+}  // namespace metis
+
+// ------------------------------------------------------------------ host
+namespace metis_host {
+
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1, kMaxCols = (int64_t)1 << 30;
+
+inline bool dtype_ok(int dt) { return dt == METIS_F32 || dt == METIS_BF16; }
+inline int elem_bytes(int dt) { return dt == METIS_F32 ? 4 : 2; }
+
+// A dense rows x cols operand (not empty): present, and aligned to its type.
+inline bool dense_ok(const void *p, int dt, int64_t cols, int64_t ld) {
+  return p && dtype_ok(dt) && ld >= cols && ((uintptr_t)p & (uintptr_t)(elem_bytes(dt) - 1)) == 0;
+}
+
+inline bool act8_fmt_ok(const metis_act8_t *q) {
+  return q && (q->fmt == METIS_MXFP8 || q->fmt == METIS_MXINT8);
+}
+
+// A launch numbers at most 2^31 chunks; taller matrices take several.
+inline int64_t slab_rows(int64_t blocks_per_row) {
+  const int64_t r = (((int64_t)1 << 29) - 1) / blocks_per_row;
+  return r < 1 ? 1 : r;
+}
+
+}  // namespace metis_host

@@ -1,0 +1,647 @@
+// Layer norm and RMS norm of the rows of a matrix, and their gradients.
+//
+//   mean = sum(x) / n (0 for RMS),  rstd = (sum((x - mean)^2) / n + eps)^(-1/2)
+//   xh = (x - mean) rstd,           y = xh w + b
+//   g = dy w,  dx = rstd (g - [sum(g) / n, layer only] - xh sum(g xh) / n)
+//   dw = sum over rows of dy xh,    db = sum over rows of dy
+//
+// HBM bound. A row is held in registers between its reduction and its use,
+// by one wave or one workgroup, so that x (and dy) are read once; rows beyond
+// what a workgroup holds are read again, out of the L2. All sums are fp32.
+// The gradients of w and b are summed over rows in two steps of fixed order
+// (a workgroup's rows in its registers, then the workgroups), without atomics:
+// results are bitwise reproducible.
+#include <algorithm>
+#include <type_traits>
+
+#include "act8.hpp"
+
+using namespace metis;
+using namespace metis_host;
+
+namespace {
+
+constexpr int kWide = 1024;         // threads on a row that does not fit registers
+constexpr int kHeldCols = 16384;    // widest row held in registers
+constexpr int kMaxParts = 512;      // partial sums of dw and db
+constexpr int kFinishThreads = 256;
+
+// ------------------------------------------------------------ reductions
+template <int CTRL> __device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float readlane_f32(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+// Sum over the wave, the same bits in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v += dpp_f32<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v += dpp_f32<0x141>(v);  // row_half_mirror: lane i with lane 7 - i
+  v += dpp_f32<0x140>(v);  // row_mirror: lane i with lane 15 - i
+  return (readlane_f32(v, 0) + readlane_f32(v, 16)) + (readlane_f32(v, 32) + readlane_f32(v, 48));
+}
+
+// Sums of two values over the LANES threads of a row (a wave, or the whole
+// workgroup through LDS). `slot` alternates between calls, so that one barrier
+// per call is enough: a wave writes a slot again only after the barrier of the
+// call in between, which every wave reaches after it has read that slot.
+template <int LANES> __device__ __forceinline__ void row_sum2(float &a, float &b, float (*red)[2][LANES / 64], int slot) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      red[slot][0][threadIdx.x >> 6] = a;
+      red[slot][1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < LANES / 64; ++w) {
+      s += red[slot][0][w];
+      t += red[slot][1][w];
+    }
+    a = s;
+    b = t;
+  }
+}
+template <int LANES> __device__ __forceinline__ float row_sum(float a, float (*red)[2][LANES / 64], int slot) {
+  a = wave_sum(a);
+  if (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) red[slot][0][threadIdx.x >> 6] = a;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < LANES / 64; ++w) s += red[slot][0][w];
+    a = s;
+  }
+  return a;
+}
+
+// Chunk c of w or b, which may be absent (`fill`) and of either type.
+__device__ __forceinline__ void load_vec(const void *p, int bf16, int c, int n, float fill, float (&v)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fill;
+  } else if (bf16) {
+    Raw<unsigned short> r;
+    load_raw((const unsigned short *)p + c, n, r);
+    to_f32(r, v);
+  } else {
+    Raw<float> r;
+    load_raw((const float *)p + c, n, r);
+    to_f32(r, v);
+  }
+}
+
+// --------------------------------------------------------------- forward
+struct FwdArgs {
+  const void *x;
+  int64_t ldx;
+  const void *w, *b;
+  int w_bf16;
+  void *y;
+  int64_t ldy;
+  float *mean, *rstd;
+  uint8_t *codes, *scales;
+  int64_t rows;
+  int cols, nblk;
+  float n, eps;  // n = cols; divided by, not multiplied with its reciprocal: a row of one value is its own mean
+};
+
+// LANES threads hold a row as V chunks each; a workgroup of 256 threads or
+// more takes the rows of its groups, then those a grid further on.
+template <typename T, typename TY, int LANES, int V, bool LAYER, int STORE>
+__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_fwd_kernel(FwdArgs g) {
+  constexpr int GROUPS = LANES < 256 ? 256 / LANES : 1;
+  __shared__ float red[2][2][LANES / 64];
+  const int t = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  float w[V][8], b[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * LANES + t) * kChunk;
+    load_vec(g.w, g.w_bf16, c, g.cols - c, 1.0f, w[v]);
+    load_vec(g.b, g.w_bf16, c, g.cols - c, 0.0f, b[v]);
+  }
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + grp; r < g.rows; r += (int64_t)gridDim.x * GROUPS) {
+    Raw<T> raw[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk;
+      load_raw((const T *)g.x + r * g.ldx + c, g.cols - c, raw[v]);
+    }
+    float mean = 0.0f;
+    if (LAYER) {
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float x[8];
+        to_f32(raw[v], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[i];
+      }
+      mean = row_sum<LANES>(s, red, 0) / g.n;
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int n = g.cols - (v * LANES + t) * kChunk;
+      float x[8];
+      to_f32(raw[v], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // elements past the row's end are zeros, which only the mean would turn into a term
+        const float d = (!LAYER || i < n) ? x[i] - mean : 0.0f;
+        ss = fmaf(d, d, ss);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<LANES>(ss, red, 1) / g.n + g.eps);
+    if (t == 0) {
+      if (LAYER && g.mean) g.mean[r] = mean;
+      if (g.rstd) g.rstd[r] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      float x[8], y[8];
+      to_f32(raw[v], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf((x[i] - mean) * rstd, w[v][i], b[v][i]);
+      store_chunk((TY *)g.y + r * g.ldy + c, y, n);
+      if (STORE != kDense) {
+        const uint32_t byte = scale_byte<STORE>(quad_max(amax_bits(raw[v])));
+        uint32_t lo, hi;
+        encode<STORE>(x, byte, lo, hi);
+        store_codes(g.codes + r * g.cols + c, lo, hi, n);
+        if ((t & 3) == 0 && n > 0) g.scales[r * g.nblk + c / kBlock8] = (uint8_t)byte;
+      }
+    }
+    if (LANES > 64 && !LAYER) __syncthreads();  // RMS uses one slot: it is read before the next row writes it
+  }
+}
+
+// Rows wider than kHeldCols: read once for the mean, once for the deviation,
+// once for the result.
+template <typename T, typename TY, bool LAYER, int STORE>
+__global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
+  __shared__ float red[2][2][kWide / 64];
+  const int t = threadIdx.x, step = kWide * kChunk, end = g.nblk * kBlock8;
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
+    const T *row = (const T *)g.x + r * g.ldx;
+    Raw<T> raw;
+    float x[8], mean = 0.0f;
+    if (LAYER) {
+      float s = 0.0f;
+      for (int c = t * kChunk; c < g.cols; c += step) {
+        load_raw(row + c, g.cols - c, raw);
+        to_f32(raw, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[i];
+      }
+      mean = row_sum<kWide>(s, red, 0) / g.n;
+    }
+    float ss = 0.0f;
+    for (int c = t * kChunk; c < g.cols; c += step) {
+      const int n = g.cols - c;
+      load_raw(row + c, n, raw);
+      to_f32(raw, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = (!LAYER || i < n) ? x[i] - mean : 0.0f;
+        ss = fmaf(d, d, ss);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<kWide>(ss, red, 1) / g.n + g.eps);
+    if (t == 0) {
+      if (LAYER && g.mean) g.mean[r] = mean;
+      if (g.rstd) g.rstd[r] = rstd;
+    }
+    for (int c = t * kChunk; c < end; c += step) {  // whole blocks: the lanes of a quad stay together
+      const int n = g.cols - c;
+      float w[8], b[8], y[8];
+      load_raw(row + c, n, raw);
+      to_f32(raw, x);
+      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
+      load_vec(g.b, g.w_bf16, c, n, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf((x[i] - mean) * rstd, w[i], b[i]);
+      store_chunk((TY *)g.y + r * g.ldy + c, y, n);
+      if (STORE != kDense) {
+        const uint32_t byte = scale_byte<STORE>(quad_max(amax_bits(raw)));
+        uint32_t lo, hi;
+        encode<STORE>(x, byte, lo, hi);
+        store_codes(g.codes + r * g.cols + c, lo, hi, n);
+        if ((t & 3) == 0) g.scales[r * g.nblk + c / kBlock8] = (uint8_t)byte;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------- backward
+struct BwdArgs {
+  const void *dy;
+  int64_t lddy;
+  const void *x;  // dense matrix or codes
+  const uint8_t *scales;
+  int64_t ldx;
+  const void *w;
+  int w_bf16;
+  const float *mean, *rstd;
+  void *dx;
+  int64_t lddx;
+  float *pw, *pb;  // partial sums, one row of cols per workgroup; NULL: not wanted
+  int64_t rows;
+  int cols, nblk;
+  float inv_n;
+};
+
+template <typename TD, int SRC, typename T, typename TO, int LANES, int V, bool LAYER>
+__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_bwd_kernel(BwdArgs g) {
+  constexpr int GROUPS = LANES < 256 ? 256 / LANES : 1;
+  __shared__ float red[2][2][LANES / 64];
+  const int t = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  float w[V][8], aw[V][8], ab[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * LANES + t) * kChunk;
+    load_vec(g.w, g.w_bf16, c, g.cols - c, 1.0f, w[v]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.0f;
+  }
+  int slot = 0;
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + grp; r < g.rows; r += (int64_t)gridDim.x * GROUPS) {
+    Raw<TD> rd[V];
+    Chunk<SRC, T> rx[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd[v]);
+      rx[v].load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+    }
+    const float rstd = g.rstd[r], mean = LAYER ? g.mean[r] : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float d[8], x[8];
+      to_f32(rd[v], d);
+      rx[v].get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // past the row's end dy is zero: no term of any sum
+        const float xh = (x[i] - mean) * rstd, gi = d[i] * w[v][i];
+        s1 += gi;
+        s2 = fmaf(gi, xh, s2);
+        aw[v][i] = fmaf(d[i], xh, aw[v][i]);
+        ab[v][i] += d[i];
+      }
+    }
+    row_sum2<LANES>(s1, s2, red, slot);
+    slot ^= 1;
+    s1 = LAYER ? s1 * g.inv_n : 0.0f;
+    s2 *= g.inv_n;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      float d[8], x[8], o[8];
+      to_f32(rd[v], d);
+      rx[v].get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = (x[i] - mean) * rstd;
+        o[i] = rstd * (fmaf(d[i], w[v][i], -s1) - xh * s2);
+      }
+      store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
+    }
+  }
+  if (!g.pw && !g.pb) return;
+  // the groups of a workgroup join through LDS, in order
+  if (GROUPS > 1) {
+    __shared__ float join[GROUPS > 1 ? V * LANES * kChunk : 1];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      for (int k = 1; k < GROUPS; ++k) {
+        __syncthreads();
+        if (grp == k) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) join[(v * 8 + i) * LANES + t] = which ? ab[v][i] : aw[v][i];
+        }
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float &a = which ? ab[v][i] : aw[v][i];
+              a += join[(v * 8 + i) * LANES + t];
+            }
+        }
+      }
+    }
+  }
+  if (grp == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      if (g.pw) store_chunk(g.pw + (int64_t)blockIdx.x * g.cols + c, aw[v], n);
+      if (g.pb) store_chunk(g.pb + (int64_t)blockIdx.x * g.cols + c, ab[v], n);
+    }
+  }
+}
+
+// Rows wider than kHeldCols: dx with dy and x read twice, dw and db in a pass
+// of their own.
+template <typename TD, int SRC, typename T, typename TO, bool LAYER>
+__global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
+  __shared__ float red[2][2][kWide / 64];
+  const int t = threadIdx.x, step = kWide * kChunk;
+  int slot = 0;
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
+    const float rstd = g.rstd[r], mean = LAYER ? g.mean[r] : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f, d[8], x[8], w[8];
+    Raw<TD> rd;
+    Chunk<SRC, T> rx;
+    for (int c = t * kChunk; c < g.cols; c += step) {
+      const int n = g.cols - c;
+      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
+      rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
+      to_f32(rd, d);
+      rx.get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float gi = d[i] * w[i];
+        s1 += gi;
+        s2 = fmaf(gi, (x[i] - mean) * rstd, s2);
+      }
+    }
+    row_sum2<kWide>(s1, s2, red, slot);
+    slot ^= 1;
+    s1 = LAYER ? s1 * g.inv_n : 0.0f;
+    s2 *= g.inv_n;
+    for (int c = t * kChunk; c < g.cols; c += step) {
+      const int n = g.cols - c;
+      float o[8];
+      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
+      rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
+      to_f32(rd, d);
+      rx.get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = rstd * (fmaf(d[i], w[i], -s1) - (x[i] - mean) * rstd * s2);
+      store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
+    }
+  }
+}
+
+// A workgroup's 256 chunks of columns over the rows blockIdx.y, + gridDim.y, ...
+template <typename TD, int SRC, typename T, bool LAYER>
+__global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(BwdArgs g) {
+  const int c = (int)(blockIdx.x * 256 + threadIdx.x) * kChunk, n = g.cols - c;
+  if (n <= 0) return;
+  float aw[8], ab[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) aw[i] = ab[i] = 0.0f;
+  for (int64_t r = blockIdx.y; r < g.rows; r += gridDim.y) {
+    const float rstd = g.rstd[r], mean = LAYER ? g.mean[r] : 0.0f;
+    Raw<TD> rd;
+    Chunk<SRC, T> rx;
+    float d[8], x[8];
+    load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
+    rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+    to_f32(rd, d);
+    rx.get(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      aw[i] = fmaf(d[i], (x[i] - mean) * rstd, aw[i]);
+      ab[i] += d[i];
+    }
+  }
+  if (g.pw) store_chunk(g.pw + (int64_t)blockIdx.y * g.cols + c, aw, n);
+  if (g.pb) store_chunk(g.pb + (int64_t)blockIdx.y * g.cols + c, ab, n);
+}
+
+// dw and db from the partial sums: 64 columns per workgroup, each wave a
+// quarter of the partials, then the waves in order. With parts = 0 (no rows)
+// the sums are zero.
+__global__ void __launch_bounds__(kFinishThreads)
+    norm_finish_kernel(const float *__restrict__ pw, const float *__restrict__ pb, int parts, int cols,
+                       float *__restrict__ dw, float *__restrict__ db, int accumulate) {
+  __shared__ float red[kFinishThreads / 64][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  const float *src = blockIdx.y ? pb : pw;
+  float *dst = blockIdx.y ? db : dw;
+  if (!dst) return;  // the whole workgroup
+  float s = 0.0f;
+  if (c < cols)
+    for (int p = wave; p < parts; p += kFinishThreads / 64) s += src[(int64_t)p * cols + c];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    for (int i = 1; i < kFinishThreads / 64; ++i) s += red[i][lane];
+    dst[c] = accumulate ? dst[c] + s : s;
+  }
+}
+
+// -------------------------------------------------------------- launches
+int lanes_of(int64_t cols) { return cols <= 2048 ? 64 : (cols <= 8192 ? 256 : 1024); }
+
+template <typename T, typename TY, bool LAYER, int STORE> void fwd_launch(const FwdArgs &g, hipStream_t stream) {
+  const int lanes = lanes_of(g.cols);
+  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(g.rows, lanes == 64 ? 4 : 1), 65536);
+  const int per = (int)cdiv(g.cols, (int64_t)lanes * kChunk);
+  if (g.cols > kHeldCols) norm_fwd_wide_kernel<T, TY, LAYER, STORE><<<grid, kWide, 0, stream>>>(g);
+  else if (lanes == 64 && per <= 1) norm_fwd_kernel<T, TY, 64, 1, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+  else if (lanes == 64 && per <= 2) norm_fwd_kernel<T, TY, 64, 2, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+  else if (lanes == 64) norm_fwd_kernel<T, TY, 64, 4, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+  else if (lanes == 256 && per <= 2) norm_fwd_kernel<T, TY, 256, 2, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+  else if (lanes == 256) norm_fwd_kernel<T, TY, 256, 4, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+  else norm_fwd_kernel<T, TY, 1024, 2, LAYER, STORE><<<grid, 1024, 0, stream>>>(g);
+}
+
+template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer, int store, hipStream_t stream) {
+  if (layer) {
+    if (store == kDense) fwd_launch<T, TY, true, kDense>(g, stream);
+    else if (store == kFp8) fwd_launch<T, TY, true, kFp8>(g, stream);
+    else fwd_launch<T, TY, true, kInt8>(g, stream);
+  } else {
+    if (store == kDense) fwd_launch<T, TY, false, kDense>(g, stream);
+    else if (store == kFp8) fwd_launch<T, TY, false, kFp8>(g, stream);
+    else fwd_launch<T, TY, false, kInt8>(g, stream);
+  }
+}
+
+// Workgroups of the backward pass, each leaving one partial sum of dw and db
+// (of a row beyond kHeldCols: row groups, fewer of them the wider the row is).
+int bwd_parts(int64_t rows, int64_t cols) {
+  if (cols > kHeldCols) return (int)std::min<int64_t>(rows, std::max<int64_t>(1, kMaxParts * (int64_t)kHeldCols / cols));
+  return (int)std::min<int64_t>(lanes_of(cols) == 64 ? cdiv(rows, 4) : rows, kMaxParts);
+}
+
+template <typename TD, int SRC, typename T, typename TO, bool LAYER>
+void bwd_launch(const BwdArgs &g, int parts, hipStream_t stream) {
+  const int lanes = lanes_of(g.cols);
+  const int per = (int)cdiv(g.cols, (int64_t)lanes * kChunk);
+  if (g.cols > kHeldCols) {
+    const unsigned grid = (unsigned)std::min<int64_t>(g.rows, 65536);
+    norm_bwd_wide_kernel<TD, SRC, T, TO, LAYER><<<grid, kWide, 0, stream>>>(g);
+    if (g.pw || g.pb)
+      norm_bwd_wide_cols_kernel<TD, SRC, T, LAYER>
+          <<<dim3((unsigned)cdiv(g.cols, 256 * kChunk), (unsigned)parts), 256, 0, stream>>>(g);
+  } else if (lanes == 64 && per <= 1) {
+    norm_bwd_kernel<TD, SRC, T, TO, 64, 1, LAYER><<<parts, 256, 0, stream>>>(g);
+  } else if (lanes == 64 && per <= 2) {
+    norm_bwd_kernel<TD, SRC, T, TO, 64, 2, LAYER><<<parts, 256, 0, stream>>>(g);
+  } else if (lanes == 64) {
+    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, LAYER><<<parts, 256, 0, stream>>>(g);
+  } else if (lanes == 256 && per <= 2) {
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 2, LAYER><<<parts, 256, 0, stream>>>(g);
+  } else if (lanes == 256) {
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, LAYER><<<parts, 256, 0, stream>>>(g);
+  } else {
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 2, LAYER><<<parts, 1024, 0, stream>>>(g);
+  }
+}
+
+template <typename TD, typename TO, bool LAYER>
+void bwd_by_source(const BwdArgs &g, int src, int xdt, int parts, hipStream_t stream) {
+  if (src == kFp8) bwd_launch<TD, kFp8, float, TO, LAYER>(g, parts, stream);
+  else if (src == kInt8) bwd_launch<TD, kInt8, float, TO, LAYER>(g, parts, stream);
+  else if (xdt == METIS_F32) bwd_launch<TD, kDense, float, TO, LAYER>(g, parts, stream);
+  else bwd_launch<TD, kDense, unsigned short, TO, LAYER>(g, parts, stream);
+}
+
+template <bool LAYER>
+void bwd_by_type(const BwdArgs &g, int dydt, int dxdt, int src, int xdt, int parts, hipStream_t stream) {
+  if (dydt == METIS_F32) {
+    if (dxdt == METIS_F32) bwd_by_source<float, float, LAYER>(g, src, xdt, parts, stream);
+    else bwd_by_source<float, unsigned short, LAYER>(g, src, xdt, parts, stream);
+  } else {
+    if (dxdt == METIS_F32) bwd_by_source<unsigned short, float, LAYER>(g, src, xdt, parts, stream);
+    else bwd_by_source<unsigned short, unsigned short, LAYER>(g, src, xdt, parts, stream);
+  }
+}
+
+bool vec_ok(const void *p, int dt) { return ((uintptr_t)p & (uintptr_t)(elem_bytes(dt) - 1)) == 0; }
+
+}  // namespace
+
+extern "C" metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx,
+                                         const void *w, const void *b, metis_dtype_t wdt, metis_norm_t kind, float eps,
+                                         void *y, metis_dtype_t ydt, int64_t ldy, float *mean, float *rstd,
+                                         metis_act8_t *stored, hipStream_t stream) {
+  if (!dtype_ok(dt) || !dtype_ok(ydt) || rows < 0 || cols < 0 || ldx < cols || ldy < cols) return METIS_ERR_INVALID;
+  if (kind != METIS_NORM_LAYER && kind != METIS_NORM_RMS) return METIS_ERR_INVALID;
+  if ((w || b) && (!dtype_ok(wdt) || !vec_ok(w, wdt) || !vec_ok(b, wdt))) return METIS_ERR_INVALID;
+  if (!(eps >= 0.0f) || (stored && !act8_fmt_ok(stored))) return METIS_ERR_INVALID;
+  if (rows > kMaxRows || cols > kMaxCols) return METIS_ERR_UNSUPPORTED;
+  if (stored) {
+    stored->rows = rows;
+    stored->cols = cols;
+  }
+  if (rows == 0 || cols == 0) return METIS_OK;
+  if (!dense_ok(x, dt, cols, ldx) || !dense_ok(y, ydt, cols, ldy)) return METIS_ERR_INVALID;
+  if (((uintptr_t)mean & 3) || ((uintptr_t)rstd & 3)) return METIS_ERR_INVALID;
+  if (stored && (!stored->codes || !stored->scales)) return METIS_ERR_INVALID;
+  FwdArgs g = {};
+  g.x = x;
+  g.ldx = ldx;
+  g.w = w;
+  g.b = b;
+  g.w_bf16 = wdt == METIS_BF16;
+  g.y = y;
+  g.ldy = ldy;
+  g.mean = mean;
+  g.rstd = rstd;
+  g.codes = stored ? stored->codes : nullptr;
+  g.scales = stored ? stored->scales : nullptr;
+  g.rows = rows;
+  g.cols = (int)cols;
+  g.nblk = (int)cdiv(cols, kBlock8);
+  g.n = (float)cols;
+  g.eps = eps;
+  const bool layer = kind == METIS_NORM_LAYER;
+  const int store = stored ? stored->fmt : kDense;
+  if (dt == METIS_F32) {
+    if (ydt == METIS_F32) fwd_by_kind<float, float>(g, layer, store, stream);
+    else fwd_by_kind<float, unsigned short>(g, layer, store, stream);
+  } else {
+    if (ydt == METIS_F32) fwd_by_kind<unsigned short, float>(g, layer, store, stream);
+    else fwd_by_kind<unsigned short, unsigned short>(g, layer, store, stream);
+  }
+  METIS_LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+extern "C" size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || rows > kMaxRows || cols > kMaxCols) return 0;
+  Carver ws(nullptr);
+  const size_t n = (size_t)bwd_parts(rows, cols) * (size_t)cols;
+  ws.take<float>(n);
+  ws.take<float>(n);
+  return ws.bytes();
+}
+
+extern "C" metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, const void *x,
+                                         metis_dtype_t xdt, int64_t ldx, const metis_act8_t *stored, const void *w,
+                                         metis_dtype_t wdt, metis_norm_t kind, const float *mean, const float *rstd,
+                                         int64_t rows, int64_t cols, void *dx, metis_dtype_t dxdt, int64_t lddx,
+                                         float *dw, float *db, int32_t accumulate, void *ws, size_t ws_bytes,
+                                         hipStream_t stream) {
+  if (!dtype_ok(dydt) || !dtype_ok(dxdt) || rows < 0 || cols < 0 || lddy < cols || lddx < cols)
+    return METIS_ERR_INVALID;
+  if (kind != METIS_NORM_LAYER && kind != METIS_NORM_RMS) return METIS_ERR_INVALID;
+  if (w && (!dtype_ok(wdt) || !vec_ok(w, wdt))) return METIS_ERR_INVALID;
+  if (((uintptr_t)dw & 3) || ((uintptr_t)db & 3)) return METIS_ERR_INVALID;
+  if (stored) {
+    if (x || !act8_fmt_ok(stored) || stored->rows != rows || stored->cols != cols) return METIS_ERR_INVALID;
+  } else if (!dtype_ok(xdt) || ldx < cols) {
+    return METIS_ERR_INVALID;
+  }
+  if (rows > kMaxRows || cols > kMaxCols) return METIS_ERR_UNSUPPORTED;
+  if (cols == 0) return METIS_OK;
+  const bool layer = kind == METIS_NORM_LAYER, sums = dw || db;
+  const dim3 finish((unsigned)cdiv(cols, 64), 2);
+  if (rows == 0) {  // dw and db are empty sums
+    if (sums && !accumulate) {
+      norm_finish_kernel<<<finish, kFinishThreads, 0, stream>>>(nullptr, nullptr, 0, (int)cols, dw, db, 0);
+      METIS_LAUNCH_CHECK();
+    }
+    return METIS_OK;
+  }
+  if (!dense_ok(dy, dydt, cols, lddy) || !dense_ok(dx, dxdt, cols, lddx)) return METIS_ERR_INVALID;
+  if (stored ? (!stored->codes || !stored->scales) : !dense_ok(x, xdt, cols, ldx)) return METIS_ERR_INVALID;
+  if (!rstd || ((uintptr_t)rstd & 3) || (layer && (!mean || ((uintptr_t)mean & 3)))) return METIS_ERR_INVALID;
+  if (sums && (!ws || ws_bytes < metis_norm_bwd_workspace_bytes(rows, cols))) return METIS_ERR_WORKSPACE;
+  if (sums && ((uintptr_t)ws & 255)) return METIS_ERR_INVALID;
+  const int parts = bwd_parts(rows, cols);
+  Carver carve(ws);
+  float *pw = carve.take<float>((size_t)parts * (size_t)cols), *pb = carve.take<float>((size_t)parts * (size_t)cols);
+  BwdArgs g = {};
+  g.dy = dy;
+  g.lddy = lddy;
+  g.x = stored ? stored->codes : x;
+  g.scales = stored ? stored->scales : nullptr;
+  g.ldx = stored ? cols : ldx;
+  g.w = w;
+  g.w_bf16 = wdt == METIS_BF16;
+  g.mean = mean;
+  g.rstd = rstd;
+  g.dx = dx;
+  g.lddx = lddx;
+  g.pw = dw ? pw : nullptr;
+  g.pb = db ? pb : nullptr;
+  g.rows = rows;
+  g.cols = (int)cols;
+  g.nblk = (int)cdiv(cols, kBlock8);
+  g.inv_n = 1.0f / (float)cols;
+  const int src = stored ? stored->fmt : kDense;
+  if (layer) bwd_by_type<true>(g, dydt, dxdt, src, xdt, parts, stream);
+  else bwd_by_type<false>(g, dydt, dxdt, src, xdt, parts, stream);
+  if (sums) norm_finish_kernel<<<finish, kFinishThreads, 0, stream>>>(pw, pb, parts, (int)cols, dw, db, accumulate);
+  METIS_LAUNCH_CHECK();
+  return METIS_OK;
+}

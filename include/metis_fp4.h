@@ -24,8 +24,10 @@
  *  - Matrices are row-major with an explicit leading dimension (elements).
  *  - FP4 blocks always run along the last (contiguous) axis of the stored
  *    matrix; for a GEMM operand that is the contraction axis.
- *  - Inputs containing NaN or Inf give undefined (but memory-safe) results.
- *  - Empty matrices (a zero dimension) are valid and enqueue nothing.
+ *  - Inputs containing NaN or Inf give undefined (but memory-safe) results,
+ *    where a call does not say otherwise.
+ *  - Empty matrices (a zero dimension) are valid and enqueue nothing, where a
+ *    call does not say otherwise.
  */
 #ifndef METIS_FP4_H
 #define METIS_FP4_H
@@ -306,6 +308,112 @@ size_t metis_dual_range_workspace_bytes(void);
 metis_status_t metis_dual_range_reg(const void *W, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldw,
                                     float tau_lo, float tau_hi, float lam_lo, float lam_hi, float *grad, int64_t ldg,
                                     int32_t accumulate, double *loss, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit storage of activations between the forward and the backward pass
+ * (what the backward pass reads again beside the FP4 operands: norm inputs,
+ * gate inputs). Formats: OCP Microscaling v1.0 §5.3, one E8M0 scale per 32
+ * elements along a row, the last block of a row possibly shorter.
+ *  METIS_MXFP8:  E4M3 elements (at most 448; relative half step 2^-4 down to
+ *                2^-6 of the scale, spacing 2^-9 below).
+ *  METIS_MXINT8: two's complement elements in units of 1/64 (at most 127/64;
+ *                half step 2^-7 of the scale everywhere).
+ * Scale 2^e: the smallest e >= -127 with which no element of the block exceeds
+ * the largest representable one (so nothing is clipped; only an MXINT8 block
+ * above 127/64 * 2^127 is held at that value). Elements x / 2^e round to
+ * nearest even; an MXFP8 zero keeps its sign. A block that holds an infinity
+ * or a NaN is stored with scale byte 255 and reads back as NaN throughout; an
+ * all-zero block has scale byte 0. */
+typedef enum { METIS_MXFP8 = 2, METIS_MXINT8 = 3 } metis_fmt8_t;
+
+/* One matrix (rows x cols) in 8 bits, blocks along cols.
+ *  codes:  rows * cols bytes, row-major, rows tightly packed.
+ *  scales: rows * ceil(cols / 32) bytes, row-major; byte e means 2^(e-127). */
+typedef struct {
+  int32_t fmt; /* metis_fmt8_t */
+  int32_t reserved;
+  int64_t rows, cols;
+  uint8_t *codes;
+  uint8_t *scales;
+} metis_act8_t;
+
+/* x (rows x cols of type dt, ldx >= cols, aligned to its element type; any
+ * width) into out, whose fmt, codes and scales the caller sets; the library
+ * writes out->rows and out->cols. Beyond 2^31 - 1 rows or 2^30 columns:
+ * METIS_ERR_UNSUPPORTED, here and in the calls below. In these calls no output
+ * may overlap an input or another output. */
+metis_status_t act8_block_quant(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx,
+                                metis_act8_t *out, hipStream_t stream);
+/* The stored values as type dt, exact in both types (no element has more than
+ * 8 significant bits), but for subnormals in bf16 and for 2^128, which MXFP8
+ * rounds magnitudes from 1.9375 * 2^127 on to: it reads back as infinity. */
+metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, metis_dtype_t dt, int64_t ldy, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm and RMS norm of the rows of x (n = cols), the input of an FP4
+ * projection:
+ *   LAYER: mean = sum(x) / n,  rstd = (sum((x - mean)^2) / n + eps)^(-1/2)
+ *   RMS:   mean = 0,           rstd = (sum(x^2) / n + eps)^(-1/2)
+ *   y = (x - mean) rstd w + b.
+ *  x:      rows x cols of type dt, ldx >= cols, aligned to its element type.
+ *  w, b:   cols elements of type wdt; either may be NULL (w = 1, b = 0).
+ *  y:      rows x cols of type ydt, rounded once from fp32.
+ *  mean, rstd: optional fp32 outputs, one per row (mean: LAYER only, not
+ *          written for RMS); the backward pass needs them.
+ *  stored: optional: x in 8 bits as act8_block_quant writes it (fmt, codes and
+ *          scales set by the caller), from the same read of x.
+ *  eps >= 0 (else METIS_ERR_INVALID). Sums in fp32; the deviation is summed
+ * around the mean, in a second pass over the row on chip. */
+typedef enum { METIS_NORM_LAYER = 0, METIS_NORM_RMS = 1 } metis_norm_t;
+metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx, const void *w,
+                              const void *b, metis_dtype_t wdt, metis_norm_t kind, float eps, void *y,
+                              metis_dtype_t ydt, int64_t ldy, float *mean, float *rstd, metis_act8_t *stored,
+                              hipStream_t stream);
+
+/* Its gradients. With xh = (x - mean) rstd and g = dy w:
+ *   dx = rstd (g - [LAYER: sum(g) / n] - xh sum(g xh) / n),
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy.
+ *  dy:     rows x cols of type dydt. x: dense, type xdt; or NULL with `stored`
+ *          the 8-bit form of x (its rows and cols set): then xh is formed from
+ *          the stored values with the mean and rstd given.
+ *  mean, rstd: as written by metis_norm_fwd (mean may be NULL for RMS).
+ *  dx:     rows x cols of type dxdt, rounded once from fp32.
+ *  dw, db: optional fp32 of cols elements, stored (accumulate == 0) or added
+ *          to what is there (accumulate != 0). With no rows they are zero
+ *          (stored) or kept (added).
+ *  ws:     metis_norm_bwd_workspace_bytes() bytes, 256-byte aligned; may be
+ *          NULL without dw and db. Sums over rows run in a fixed order (no
+ *          atomics): bitwise reproducible. */
+size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, const void *x, metis_dtype_t xdt,
+                              int64_t ldx, const metis_act8_t *stored, const void *w, metis_dtype_t wdt,
+                              metis_norm_t kind, const float *mean, const float *rstd, int64_t rows, int64_t cols,
+                              void *dx, metis_dtype_t dxdt, int64_t lddx, float *dw, float *db, int32_t accumulate,
+                              void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * SwiGLU gate between an FFN's up and down projections:
+ *   h = silu(a) b,  silu(a) = a / (1 + exp(-a)).
+ *  a, b:   rows x cols of type dt, leading dimensions lda, ldb >= cols (the
+ *          two halves of one fused projection's output, or two matrices).
+ *  h:      rows x cols of type hdt, rounded once from fp32.
+ *  qa, qb: optional, both or neither and of one format: a and b in 8 bits as
+ *          act8_block_quant writes them, from the same read. */
+metis_status_t metis_swiglu_fwd(const void *a, int64_t lda, const void *b, int64_t ldb, metis_dtype_t dt, int64_t rows,
+                                int64_t cols, void *h, metis_dtype_t hdt, int64_t ldh, metis_act8_t *qa,
+                                metis_act8_t *qb, hipStream_t stream);
+
+/* Its gradients. With s = 1 / (1 + exp(-a)):
+ *   da = dh b s (1 + a (1 - s)),  db = dh a s.
+ *  dh:     rows x cols of type dhdt.
+ *  a, b:   dense, type dt; or both NULL with qa and qb their 8-bit forms.
+ *  da, db: rows x cols of type odt, rounded once from fp32.
+ *  h:      optional, type odt: silu(a) b again, from the a and b given (the
+ *          weight gradient of the down projection reads it). */
+metis_status_t metis_swiglu_bwd(const void *dh, metis_dtype_t dhdt, int64_t lddh, const void *a, int64_t lda,
+                                const void *b, int64_t ldb, metis_dtype_t dt, const metis_act8_t *qa,
+                                const metis_act8_t *qb, int64_t rows, int64_t cols, void *da, int64_t ldda, void *db,
+                                int64_t lddb, void *h, int64_t ldh, metis_dtype_t odt, hipStream_t stream);
 
 #ifdef __cplusplus
 }

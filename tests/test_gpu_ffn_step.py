@@ -1,0 +1,157 @@
+"""Norm, gate and 8-bit storage as a training step uses them around the FP4
+linear layer: forward and backward of an FFN, every stage against the oracle
+on the stage's own input, and the same calls captured into HIP graphs."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import act8 as A
+from oracle import ffn as O
+from oracle import linear as OL
+from tests import _ffn as H
+from tests import _glue as G
+from tests import test_gpu_norm as TN
+from tests import test_gpu_swiglu as TS
+
+pytestmark = pytest.mark.gpu
+
+import fp4_spectral_split_amd as M
+
+TOK, DIM, FFN = 96, 256, 352  # tokens, model width, FFN width (a multiple of 32, not of 64)
+EPS = float(np.float32(1e-5))
+
+
+def _weights(g):
+    w = lambda *s: torch.from_numpy(g.standard_normal(s) / np.sqrt(s[1])).to(torch.bfloat16).cuda()
+    both = ("n", "t")
+    return M.plain_operand(w(2 * FFN, DIM), "mxfp4", both), M.plain_operand(w(DIM, FFN), "mxfp4", both)
+
+
+def _step(x, nw, wu, wd, dout, fmt, kind):
+    """One FFN training step; returns every intermediate value."""
+    s = {}
+    s["y"], s["mean"], s["rstd"], s["x8"] = M.metis_norm_fwd(x, nw, None, kind=kind, save=fmt)
+    s["yq"] = M.plain_operand(s["y"], "mxfp4", ("n", "t"))
+    s["up"] = M.spectral_fp4_linear_fwd(s["yq"], wu)
+    a, b = s["up"][:, :FFN], s["up"][:, FFN:]
+    s["h"], s["a8"], s["b8"] = M.metis_swiglu_fwd(a, b, dtype=torch.bfloat16, save=fmt)
+    s["out"] = M.spectral_fp4_linear_fwd(M.plain_operand(s["h"], "mxfp4"), wd)
+    # backward: h is not kept but rebuilt from the 8-bit a and b
+    dq = M.plain_operand(dout, "mxfp4", ("n", "t"))
+    s["dq"] = dq
+    s["dh"] = torch.empty(TOK, FFN, device="cuda")
+    hq = M.SplitRecord(TOK, FFN, 0, M.MXFP4, R_q=M.plain_operand(s["h"], "mxfp4").R_q)
+    M.spectral_fp4_linear_bwd(dq, hq, wd, need_dw=False, dx=s["dh"])
+    dup = torch.empty(TOK, 2 * FFN, dtype=torch.bfloat16, device="cuda")
+    s["da"], s["db"], s["h2"] = M.metis_swiglu_bwd(s["dh"], s["a8"], s["b8"], dtype=torch.bfloat16, need_h=True,
+                                                   da=dup[:, :FFN], db=dup[:, FFN:])
+    _, s["dwd"] = M.spectral_fp4_linear_bwd(dq, M.plain_operand(s["h2"], "mxfp4", ("n", "t")), wd, need_dx=False)
+    s["dupq"] = M.plain_operand(dup, "mxfp4", ("n", "t"))
+    s["dy"], s["dwu"] = M.spectral_fp4_linear_bwd(s["dupq"], s["yq"], wu)
+    s["dx"], s["dnw"], _ = M.metis_norm_bwd(s["dy"], s["x8"], nw, s["mean"], s["rstd"], kind=kind, dtype=x.dtype)
+    return s
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+def test_ffn_training_step(fmt, kind):
+    g = H.rng(41)
+    x = H.to_dev(TN._stream(g, (TOK, DIM)), torch.bfloat16)
+    nw = torch.from_numpy(1 + 0.1 * g.standard_normal(DIM)).float().cuda()
+    wu, wd = _weights(g)
+    dout = H.to_dev(1e-2 * g.standard_normal((TOK, DIM)), torch.bfloat16)
+    print("case ffn step", fmt, kind, flush=True)
+    s = _step(x, nw, wu, wd, dout, fmt, kind)
+    torch.cuda.synchronize()
+    n = H.np64
+    TN._check_fwd(s["y"], s["mean"], s["rstd"], n(x), n(nw), None, kind, EPS, torch.bfloat16)
+    up = n(s["up"])
+    TS._check_fwd(s["h"], up[:, :FFN], up[:, FFN:], torch.bfloat16)
+    a8, b8 = A.restored(up[:, :FFN], fmt), A.restored(up[:, FFN:], fmt)
+    TS._check_bwd((s["da"], s["db"], s["h2"]), n(s["dh"]), a8, b8, torch.bfloat16)
+    TN._check_bwd((s["dx"], s["dnw"], None), n(s["dy"]), A.restored(n(x), fmt), n(nw),
+                  n(s["mean"]) if kind == "layer" else None, n(s["rstd"]), kind, torch.bfloat16)
+    # the GEMMs between them, on the records they were given (1e-3, the framework's bound)
+    for got, want in ((s["up"], OL.linear_fwd(G.record_to_dict(s["yq"]), G.record_to_dict(wu))),
+                      (s["dy"], OL.linear_bwd_dx(G.record_to_dict(s["dupq"]), G.record_to_dict(wu)))):
+        assert np.linalg.norm(n(got) - want) <= 1e-3 * np.linalg.norm(want)
+
+
+def test_stored_inputs_change_the_gradients_by_their_rounding_only():
+    """The gate's gradient from stored inputs against that from the dense ones:
+    it moves by no more than its derivatives times the storage's half steps."""
+    g = H.rng(42)
+    a, b, dh = (H.to_dev(g.standard_normal((64, 320)), torch.float32) for _ in range(3))
+    a64, b64, d64 = H.np64(a), H.np64(b), H.np64(dh)
+    dense = M.metis_swiglu_bwd(dh, a, b, need_h=True)
+    for fmt in ("mxfp8", "mxint8"):
+        _, qa, qb = M.metis_swiglu_fwd(a, b, save=fmt)
+        got = M.metis_swiglu_bwd(dh, qa, qb, need_h=True)
+        ea, eb = np.abs(A.restored(a64, fmt) - a64), np.abs(A.restored(b64, fmt) - b64)
+        # |silu| <= |a|, |silu'| <= 1.1, |silu''| <= 0.5
+        at = np.abs(a64) + ea
+        bound = (np.abs(d64) * (0.5 * ea * (np.abs(b64) + eb) + 1.1 * eb), np.abs(d64) * 1.1 * ea,
+                 1.1 * ea * (np.abs(b64) + eb) + at * eb)
+        for p, q, m in zip(got, dense, bound):
+            assert np.all(np.abs(H.np64(p) - H.np64(q)) <= m + 1e-5 * (1 + np.abs(H.np64(q))))
+
+
+def test_two_captured_steps_replayed_together():
+    """Two graphs of the same calls on different inputs, captured on one stream
+    and replayed on two at once, again and again with eager work between: each
+    equals its eager result bit for bit (their workspaces are their own)."""
+    shapes = [(257, 1365), (130, 2056)]
+    g = H.rng(43)
+    sets = []
+    for rows, cols in shapes:
+        x = H.to_dev(TN._stream(g, (rows, cols)), torch.bfloat16)
+        dy = H.to_dev(g.standard_normal((rows, cols)), torch.float32)
+        a, b = H.to_dev(g.standard_normal((rows, cols)), torch.float32), H.to_dev(g.standard_normal((rows, cols)),
+                                                                                 torch.float32)
+        w = torch.from_numpy(g.standard_normal(cols)).float().cuda()
+        sets.append((x, dy, a, b, w))
+
+    def work(x, dy, a, b, w):
+        y, mean, rstd, x8 = M.metis_norm_fwd(x, w, w, save="mxfp8")
+        dx, dw, db = M.metis_norm_bwd(dy, x8, w, mean, rstd)
+        h, a8, b8 = M.metis_swiglu_fwd(a, b, save="mxint8")
+        da, dbb, h2 = M.metis_swiglu_bwd(dy, a8, b8, need_h=True)
+        return [y, rstd, dx, dw, db, h, da, dbb, h2, M.act8_block_dequant(x8)]
+
+    for s in sets:
+        work(*s)
+    torch.cuda.synchronize()
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    for s in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=side):
+            outs.append(work(*s))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(4):
+        print("replay", rep, flush=True)
+        for s in sets:
+            s[0].mul_(1.0 + 0.25 * rep)
+            s[2].mul_(0.9)
+        want = [[t.clone() for t in work(*s)] for s in sets]
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+def test_calls_on_another_stream_than_the_default():
+    g = H.rng(44)
+    x, dy = H.to_dev(g.standard_normal((300, 700)), torch.bfloat16), H.to_dev(g.standard_normal((300, 700)), torch.bfloat16)
+    y, mean, rstd, _ = M.metis_norm_fwd(x)
+    want = M.metis_norm_bwd(dy, x, None, mean, rstd)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        y2, mean2, rstd2, _ = M.metis_norm_fwd(x)
+        got = M.metis_norm_bwd(dy, x, None, mean2, rstd2)
+    st.synchronize()
+    assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(got, want))
