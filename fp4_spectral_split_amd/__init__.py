@@ -476,6 +476,8 @@ def metis_dual_range_reg(W, tau_lo, tau_hi, lam_lo, lam_hi, grad=None, accumulat
 
 
 # ------------------------------------- norm, gate and 8-bit activation storage
+# A call on few rows lasts as long as its way through this binding, so the
+# checks below read each attribute once and addresses go to C as plain ints.
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -491,36 +493,43 @@ def _matrix(t, name, shape=None, device=None):
     dimension in elements."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
         raise MetisError("%s must be a 2-D CUDA tensor" % name)
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise MetisError("%s must be %d x %d, got %d x %d" % (name, shape[0], shape[1], rows, cols))
+    s = t.shape
+    if shape is not None and s != shape:
+        raise MetisError("%s must be %d x %d, got %d x %d" % (name, shape[0], shape[1], s[0], s[1]))
     if device is not None and t.device != device:
         raise MetisError("%s is on %s, the other operands on %s" % (name, t.device, device))
-    if cols > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and s[1] > 1:
         raise MetisError("the rows of %s must be contiguous" % name)
-    return t.stride(0) if rows > 1 else cols
+    return ld if s[0] > 1 else s[1]
 
 
 def _vector(t, name, n, device, dtype=None):
-    """Checks an optional contiguous CUDA vector of n elements."""
+    """Checks an optional contiguous CUDA vector of n elements; returns its
+    address (None where it is absent)."""
     if t is None:
-        return
+        return None
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise MetisError("%s must be a contiguous vector of %d elements" % (name, n))
     if t.device != device:
         raise MetisError("%s is on %s, the other operands on %s" % (name, t.device, device))
     if dtype is not None and t.dtype != dtype:
         raise MetisError("%s must be %s" % (name, dtype))
+    return t.data_ptr()
 
 
-def _on(device, call):
-    """call(stream) with the tensors' device as the current one (a launch goes
-    to the current device, whatever device its operands are on)."""
-    if torch.cuda.current_device() == device.index:
-        _check(call(_stream(device)))
+def _run(device, fn, *args):
+    """fn(*args, stream) on the current stream of the tensors' device, with that
+    device as the current one (a launch goes to the current device, whatever
+    device its operands are on)."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(call(_stream(device)))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
 
 
 @dataclass
@@ -534,15 +543,15 @@ class Act8Tensor:
 
     @staticmethod
     def empty(fmt, rows, cols, device):
-        return Act8Tensor(_fmt8(fmt), rows, cols, torch.empty(rows, cols, dtype=torch.uint8, device=device),
-                          torch.empty(rows, -(-cols // BLOCK8), dtype=torch.uint8, device=device))
+        return Act8Tensor(_fmt8(fmt), rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                          torch.empty((rows, -(-cols // BLOCK8)), dtype=torch.uint8, device=device))
 
     @staticmethod
     def from_codes(fmt, codes, scales):
         """The record of given codes (rows x cols) and scale bytes (rows x
         ceil(cols / 32))."""
         q = Act8Tensor(_fmt8(fmt), codes.shape[0], codes.shape[1], codes, scales)
-        _stored(q, "codes", tuple(codes.shape), codes.device)
+        _stored(q, "codes", codes.shape, codes.device)
         return q
 
     def c(self):
@@ -563,59 +572,73 @@ def _fmt8(fmt):
 def _stored(q, name, shape, device):
     """Checks an Act8Tensor: its buffers hold the matrix it says, on the device."""
     rows, cols = shape
-    if (q.rows, q.cols) != (rows, cols):
+    if q.rows != rows or q.cols != cols:
         raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
     for buf, n in ((q.codes, rows * cols), (q.scales, rows * -(-cols // BLOCK8))):
-        if buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() != n or not buf.is_cuda:
+        if buf.dtype != torch.uint8 or buf.numel() != n or not buf.is_contiguous() or not buf.is_cuda:
             raise MetisError("%s needs contiguous uint8 CUDA codes and scales of its size" % name)
         if buf.device != device:
             raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))
     return q
 
 
-def _save(save, shape, device):
-    """The Act8Tensor to store into: a new one of a named format, the one
+def _act8_like(fmt, x):
+    """A new Act8Tensor for x."""
+    rows, cols = x.shape
+    codes = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+    return Act8Tensor(_fmt8(fmt), rows, cols, codes, codes.new_empty((rows, -(-cols // BLOCK8))))
+
+
+def _save(save, x):
+    """The Act8Tensor to store x into: a new one of a named format, the one
     given, or None."""
     if save is None:
         return None
     if isinstance(save, Act8Tensor):
-        return _stored(save, "save", shape, device)
-    return Act8Tensor.empty(save, shape[0], shape[1], device)
+        return _stored(save, "save", x.shape, x.device)
+    return _act8_like(save, x)
 
 
-def _out(out, name, shape, dtype, device):
-    """An output tensor (new where none is given) and its leading dimension."""
+def _out(out, name, like, dtype, device):
+    """An output of the shape of `like` (new where none is given) and its
+    leading dimension."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format), like.shape[1]
+    ld = _matrix(out, name, like.shape, device)
     if out.dtype != dtype:
         raise MetisError("%s must be %s" % (name, dtype))
-    return out, _matrix(out, name, shape, device)
+    return out, ld
+
+
+def _sum_out(t, name, n, device):
+    """A per-column fp32 sum (new where none is given) and its address."""
+    if t is None:
+        t = torch.empty(n, dtype=torch.float32, device=device)
+        return t, t.data_ptr()
+    return t, _vector(t, name, n, device, torch.float32)
 
 
 def act8_block_quant(x, fmt="mxfp8", out=None):
     """Store a 2-D fp32/bf16 CUDA tensor (any width, rows contiguous) in 8
     bits: MXFP8 (E4M3) or MXINT8 codes with one scale per 32 elements."""
     ld = _matrix(x, "x")
+    shape, dev, dt = x.shape, x.device, _code(x.dtype)
     if out is None:
-        out = Act8Tensor.empty(fmt, x.shape[0], x.shape[1], x.device)
+        out = _act8_like(fmt, x)
     else:
-        _stored(out, "out", tuple(x.shape), x.device)
+        _stored(out, "out", shape, dev)
         if out.fmt != _fmt8(fmt):
             raise MetisError("out is of another format")
-    c = out.c()
-    L, dt = load(), _code(x.dtype)
-    _on(x.device, lambda s: L.act8_block_quant(x.data_ptr(), dt, x.shape[0], x.shape[1], ld, c, s))
+    _run(dev, load().act8_block_quant, x.data_ptr(), dt, shape[0], shape[1], ld, out.c())
     return out
 
 
 def act8_block_dequant(q, dtype=torch.float32, out=None):
     """The values of an Act8Tensor as fp32 or bf16 (both hold them exactly)."""
-    dev = q.codes.device
-    _stored(q, "q", (q.rows, q.cols), dev)
-    dt = _code(dtype)
-    out, ld = _out(out, "out", (q.rows, q.cols), dtype, dev)
-    c, L = q.c(), load()
-    _on(dev, lambda s: L.act8_block_dequant(c, out.data_ptr(), dt, ld, s))
+    dev, shape, dt = q.codes.device, (q.rows, q.cols), _code(dtype)
+    _stored(q, "q", shape, dev)
+    out, ld = _out(out, "out", q.codes.view(shape), dtype, dev)
+    _run(dev, load().act8_block_dequant, q.c(), out.data_ptr(), dt, ld)
     return out
 
 
@@ -632,22 +655,21 @@ def metis_norm_fwd(x, weight=None, bias=None, kind="layer", eps=1e-5, dtype=None
     (None for RMS) and rstd are fp32, one per row. save: "mxfp8" / "mxint8" or
     an Act8Tensor to write into: x in 8 bits for the backward pass, as stored."""
     ldx = _matrix(x, "x")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
+    rows, cols = shape
     k, dt = _norm_kind(kind), _code(x.dtype)
-    _vector(weight, "weight", shape[1], dev)
-    _vector(bias, "bias", shape[1], dev, weight.dtype if weight is not None else None)
+    wp = _vector(weight, "weight", cols, dev)
+    bp = _vector(bias, "bias", cols, dev, weight.dtype if weight is not None else None)
     wt = weight if weight is not None else bias
     wdt = _code(wt.dtype) if wt is not None else F32
     dtype = x.dtype if dtype is None else dtype
     ydt = _code(dtype)
-    y, ldy = _out(out, "out", shape, dtype, dev)
-    mean = torch.empty(shape[0], dtype=torch.float32, device=dev) if k == NORM_LAYER else None
-    rstd = torch.empty(shape[0], dtype=torch.float32, device=dev)
-    stored = _save(save, shape, dev)
-    c = stored.c() if stored is not None else None
-    L = load()
-    _on(dev, lambda s: L.metis_norm_fwd(x.data_ptr(), dt, shape[0], shape[1], ldx, _ptr(weight), _ptr(bias), wdt, k,
-                                        eps, y.data_ptr(), ydt, ldy, _ptr(mean), rstd.data_ptr(), c, s))
+    y, ldy = _out(out, "out", x, dtype, dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if k == NORM_LAYER else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    stored = _save(save, x)
+    _run(dev, load().metis_norm_fwd, x.data_ptr(), dt, rows, cols, ldx, wp, bp, wdt, k, eps, y.data_ptr(), ydt, ldy,
+         None if mean is None else mean.data_ptr(), rstd.data_ptr(), None if stored is None else stored.c())
     return y, mean, rstd, stored
 
 
@@ -659,44 +681,42 @@ def metis_norm_bwd(dy, x, weight, mean, rstd, kind="layer", dtype=None, need_dwe
     (need_dbias defaults to the layer norm), added to the tensors given with
     accumulate=True."""
     lddy = _matrix(dy, "dy")
-    dev, shape = dy.device, tuple(dy.shape)
+    dev, shape = dy.device, dy.shape
+    rows, cols = shape
     k, dydt = _norm_kind(kind), _code(dy.dtype)
     if isinstance(x, Act8Tensor):
         q, xp, xdt, ldx = _stored(x, "x", shape, dev).c(), None, F32, 0
     else:
         ldx = _matrix(x, "x", shape, dev)
         q, xp, xdt = None, x.data_ptr(), _code(x.dtype)
-    _vector(weight, "weight", shape[1], dev)
+    wp = _vector(weight, "weight", cols, dev)
+    wdt = _code(weight.dtype) if weight is not None else F32
     if rstd is None or (k == NORM_LAYER and mean is None):
         raise MetisError("the backward pass needs the forward's rstd, and for a layer norm its mean")
-    _vector(rstd, "rstd", shape[0], dev, torch.float32)
-    if k == NORM_RMS:
-        mean = None
-    _vector(mean, "mean", shape[0], dev, torch.float32)
+    rp = _vector(rstd, "rstd", rows, dev, torch.float32)
+    mp = _vector(mean, "mean", rows, dev, torch.float32) if k == NORM_LAYER else None
     dtype = dy.dtype if dtype is None else dtype
     dxdt = _code(dtype)
     if need_dbias is None:
         need_dbias = k == NORM_LAYER
     if accumulate and ((need_dweight and dweight is None) or (need_dbias and dbias is None)):
         raise MetisError("accumulate needs the gradients to add to")
-    dx, lddx = _out(out, "out", shape, dtype, dev)
-    grads = []
-    for need, g, name in ((need_dweight, dweight, "dweight"), (need_dbias, dbias, "dbias")):
-        if need and g is None:
-            g = torch.empty(shape[1], dtype=torch.float32, device=dev)
-        _vector(g, name, shape[1], dev, torch.float32)
-        grads.append(g if need else None)
-    dw, db = grads
+    dx, lddx = _out(out, "out", dy, dtype, dev)
+    wgp = bgp = ws = None
+    nws = 0
+    if need_dweight:
+        dweight, wgp = _sum_out(dweight, "dweight", cols, dev)
+    if need_dbias:
+        dbias, bgp = _sum_out(dbias, "dbias", cols, dev)
     L = load()
-    # the partial sums live in a buffer of their own per call: a captured call
-    # keeps it in its graph's memory, so two graphs never share one
-    nws = L.metis_norm_bwd_workspace_bytes(shape[0], shape[1]) if need_dweight or need_dbias else 0
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    wdt = _code(weight.dtype) if weight is not None else F32
-    _on(dev, lambda s: L.metis_norm_bwd(dy.data_ptr(), dydt, lddy, xp, xdt, ldx, q, _ptr(weight), wdt, k, _ptr(mean),
-                                        rstd.data_ptr(), shape[0], shape[1], dx.data_ptr(), dxdt, lddx, _ptr(dw),
-                                        _ptr(db), int(bool(accumulate)), _ptr(ws), nws, s))
-    return dx, dw, db
+    if need_dweight or need_dbias:
+        # the partial sums live in a buffer of their own per call: a captured
+        # call keeps it in its graph's memory, so two graphs never share one
+        nws = L.metis_norm_bwd_workspace_bytes(rows, cols)
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _run(dev, L.metis_norm_bwd, dy.data_ptr(), dydt, lddy, xp, xdt, ldx, q, wp, wdt, k, mp, rp, rows, cols,
+         dx.data_ptr(), dxdt, lddx, wgp, bgp, 1 if accumulate else 0, ws.data_ptr() if nws else None, nws)
+    return dx, dweight if need_dweight else None, dbias if need_dbias else None
 
 
 def metis_swiglu_fwd(a, b, dtype=None, save=None, out=None):
@@ -705,26 +725,26 @@ def metis_swiglu_fwd(a, b, dtype=None, save=None, out=None):
     (default: a's). save: "mxfp8" / "mxint8" or a pair of Act8Tensors: a and b
     in 8 bits for the backward pass."""
     lda = _matrix(a, "a")
-    dev, shape = a.device, tuple(a.shape)
+    dev, shape, dt = a.device, a.shape, a.dtype
     ldb = _matrix(b, "b", shape, dev)
-    if a.dtype != b.dtype:
+    if b.dtype != dt:
         raise MetisError("a and b must be of one type")
-    dt = _code(a.dtype)
-    dtype = a.dtype if dtype is None else dtype
-    hdt = _code(dtype)
-    h, ldh = _out(out, "out", shape, dtype, dev)
-    if isinstance(save, (tuple, list)):
-        if len(save) != 2 or not all(isinstance(q, Act8Tensor) for q in save):
+    dtype = dt if dtype is None else dtype
+    dt, hdt = _code(dt), _code(dtype)
+    h, ldh = _out(out, "out", a, dtype, dev)
+    qa = qb = ca = cb = None
+    if save is not None:
+        if isinstance(save, (tuple, list)):
+            if len(save) != 2 or not all(isinstance(q, Act8Tensor) for q in save):
+                raise MetisError("save must be a format or a pair of Act8Tensors")
+            qa, qb = _save(save[0], a), _save(save[1], b)
+        elif isinstance(save, Act8Tensor):
             raise MetisError("save must be a format or a pair of Act8Tensors")
-        qa, qb = (_save(q, shape, dev) for q in save)
-    elif isinstance(save, Act8Tensor):
-        raise MetisError("save must be a format or a pair of Act8Tensors")
-    else:
-        qa, qb = _save(save, shape, dev), _save(save, shape, dev)
-    ca, cb = (qa.c(), qb.c()) if qa is not None else (None, None)
-    L = load()
-    _on(dev, lambda s: L.metis_swiglu_fwd(a.data_ptr(), lda, b.data_ptr(), ldb, dt, shape[0], shape[1], h.data_ptr(),
-                                          hdt, ldh, ca, cb, s))
+        else:
+            qa, qb = _save(save, a), _save(save, b)
+        ca, cb = qa.c(), qb.c()
+    _run(dev, load().metis_swiglu_fwd, a.data_ptr(), lda, b.data_ptr(), ldb, dt, shape[0], shape[1], h.data_ptr(), hdt,
+         ldh, ca, cb)
     return h, qa, qb
 
 
@@ -733,14 +753,13 @@ def metis_swiglu_bwd(dh, a, b, dtype=None, need_h=False, da=None, db=None, h=Non
     as the Act8Tensors it stored. da and db are of type `dtype` (default:
     dh's), as is h = silu(a) b, rebuilt where need_h is set (else None)."""
     lddh = _matrix(dh, "dh")
-    dev, shape = dh.device, tuple(dh.shape)
-    dhdt = _code(dh.dtype)
-    if isinstance(a, Act8Tensor) != isinstance(b, Act8Tensor):
-        raise MetisError("a and b must both be dense or both stored")
+    dev, shape, dhdt = dh.device, dh.shape, _code(dh.dtype)
     if isinstance(a, Act8Tensor):
+        if not isinstance(b, Act8Tensor):
+            raise MetisError("a and b must both be dense or both stored")
         qa, qb = _stored(a, "a", shape, dev).c(), _stored(b, "b", shape, dev).c()
         ap = bp = None
-        lda, ldb, dt = shape[1], shape[1], F32
+        lda = ldb = dt = 0
     else:
         lda, ldb = _matrix(a, "a", shape, dev), _matrix(b, "b", shape, dev)
         if a.dtype != b.dtype:
@@ -749,10 +768,14 @@ def metis_swiglu_bwd(dh, a, b, dtype=None, need_h=False, da=None, db=None, h=Non
         ap, bp, dt = a.data_ptr(), b.data_ptr(), _code(a.dtype)
     dtype = dh.dtype if dtype is None else dtype
     odt = _code(dtype)
-    da, ldda = _out(da, "da", shape, dtype, dev)
-    db, lddb = _out(db, "db", shape, dtype, dev)
-    h, ldh = _out(h, "h", shape, dtype, dev) if need_h else (None, shape[1])
-    L = load()
-    _on(dev, lambda s: L.metis_swiglu_bwd(dh.data_ptr(), dhdt, lddh, ap, lda, bp, ldb, dt, qa, qb, shape[0], shape[1],
-                                          da.data_ptr(), ldda, db.data_ptr(), lddb, _ptr(h), ldh, odt, s))
+    da, ldda = _out(da, "da", dh, dtype, dev)
+    db, lddb = _out(db, "db", dh, dtype, dev)
+    hp, ldh = None, 0
+    if need_h:
+        h, ldh = _out(h, "h", dh, dtype, dev)
+        hp = h.data_ptr()
+    else:
+        h = None
+    _run(dev, load().metis_swiglu_bwd, dh.data_ptr(), dhdt, lddh, ap, lda, bp, ldb, dt, qa, qb, shape[0], shape[1],
+         da.data_ptr(), ldda, db.data_ptr(), lddb, hp, ldh, odt)
     return da, db, h

@@ -383,7 +383,8 @@ metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int
  *          (stored) or kept (added).
  *  ws:     metis_norm_bwd_workspace_bytes() bytes, 256-byte aligned; may be
  *          NULL without dw and db. Sums over rows run in a fixed order (no
- *          atomics): bitwise reproducible. */
+ *          atomics): bitwise reproducible. A row with a NaN or an infinity
+ *          makes its own row of dx and dw NaN (its columns of db by dy). */
 size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, const void *x, metis_dtype_t xdt,
                               int64_t ldx, const metis_act8_t *stored, const void *w, metis_dtype_t wdt,
@@ -398,7 +399,10 @@ metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, 
  *          two halves of one fused projection's output, or two matrices).
  *  h:      rows x cols of type hdt, rounded once from fp32.
  *  qa, qb: optional, both or neither and of one format: a and b in 8 bits as
- *          act8_block_quant writes them, from the same read. */
+ *          act8_block_quant writes them, from the same read.
+ * A NaN or an infinity reaches the outputs of its own element only. Below
+ * a = -86.6 the sigmoid is held at 2^-125, so that |h| is up to 2^-118 |b|
+ * where it should be smaller still. */
 metis_status_t metis_swiglu_fwd(const void *a, int64_t lda, const void *b, int64_t ldb, metis_dtype_t dt, int64_t rows,
                                 int64_t cols, void *h, metis_dtype_t hdt, int64_t ldh, metis_act8_t *qa,
                                 metis_act8_t *qb, hipStream_t stream);
