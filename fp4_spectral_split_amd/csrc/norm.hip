@@ -277,15 +277,45 @@ struct BwdArgs {
   float inv_n;
 };
 
+// A row's dy and x as loaded, with its statistics.
+template <typename TD, int SRC, typename T, int V> struct BwdRow {
+  Raw<TD> d[V];
+  Chunk<SRC, T> x[V];
+  float mean, rstd;
+};
+
 // LANES threads hold a row, GROUPS rows are worked on at once, and every
 // thread keeps the sums of dw and db of its columns in registers over all rows
 // of its group. With dr = dy rstd and xc = x - mean held from the reductions
 // (S1 = sum(dy w), S2 = sum(dy w xc)) the result is
 //   dx = dr w - rstd S1 / n - xc rstd^3 S2 / n.
-template <typename TD, int SRC, typename T, typename TO, int LANES, int GROUPS, int V, bool LAYER>
+// DEPTH sets of rows are in registers: one worked on, the others on their way
+// (8192 x 4096, bf16 dy and MXFP8 x: one set 42.0 us with the join of the sums,
+// two 39.7, three 40.7).
+template <typename TD, int SRC, typename T, typename TO, int LANES, int GROUPS, int V, int DEPTH, bool LAYER>
 __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
   __shared__ float red[2][GROUPS][2][LANES / 64];
   const int t = threadIdx.x % LANES, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  typedef BwdRow<TD, SRC, T, V> Row;
+  // every group runs the same steps (they meet at barriers); past the last row
+  // it works on zeros
+  auto load = [&](int64_t r, Row &row) {
+    const bool live = r < g.rows;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * LANES + t) * kChunk, n = live ? g.cols - c : 0;
+      load_raw((const TD *)g.dy + r * g.lddy + c, n, row.d[v]);
+      row.x[v].load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+    }
+    row.rstd = live ? g.rstd[r] : 0.0f;
+    row.mean = LAYER && live ? g.mean[r] : 0.0f;
+  };
+  int64_t r0 = (int64_t)blockIdx.x * GROUPS + grp;
+  const int64_t end = g.rows + grp;  // of r0: the same step for every group
+  Row rows[DEPTH];
+#pragma unroll
+  for (int k = 0; k < DEPTH - 1; ++k) load(r0 + k * step, rows[k]);
   float w[V][8], aw[V][8], ab[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -295,26 +325,14 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.0f;
   }
   int slot = 0;
-  // every group runs the same steps (they meet at barriers); past the last row
-  // it works on zeros
-  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < g.rows; r0 += (int64_t)gridDim.x * GROUPS) {
-    const int64_t r = r0 + grp;
-    const bool live = GROUPS == 1 || r < g.rows;
-    Raw<TD> rd[V];
-    Chunk<SRC, T> rx[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = live ? g.cols - c : 0;
-      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd[v]);
-      rx[v].load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
-    }
-    const float rstd = live ? g.rstd[r] : 0.0f, mean = LAYER && live ? g.mean[r] : 0.0f;
+  auto work = [&](int64_t r, const Row &row) {
+    const float rstd = row.rstd, mean = row.mean;
     float dr[V][8], xc[V][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float d[8];
-      to_f32(rd[v], d);
-      rx[v].get(xc[v]);
+      to_f32(row.d[v], d);
+      row.x[v].get(xc[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // past the row's end dy is zero: no term of any sum
@@ -332,11 +350,20 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
     const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = live ? g.cols - c : 0;
+      const int c = (v * LANES + t) * kChunk, n = r < g.rows ? g.cols - c : 0;
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = fmaf(dr[v][i], w[v][i], fmaf(-k2, xc[v][i], -k1));
       store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
+    }
+  };
+  for (; r0 < end; r0 += DEPTH * step) {
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= end) break;
+      load(r + (DEPTH - 1) * step, rows[(k + DEPTH - 1) % DEPTH]);
+      work(r, rows[k]);
     }
   }
   if (!g.pw && !g.pb) return;
@@ -517,13 +544,15 @@ template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer
 // workgroups as the sums of dw and db allow (next), this is what fills a CU.
 // 517 x 1365 fp32 in one, two, four rows at once: 10.8, 9.1, 8.5 us; 4096 x
 // 2048 bf16: 17.4, 16.6, 15.8; 8192 x 4096 bf16: 42.5, 42.3, 49.6, the four
-// waiting for each other at every row's barrier.
-int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 8192 ? 2 : 1); }
+// waiting for each other at every row's barrier. 8192 x 8192 bf16 with four
+// chunks of a row per thread, two rows at once: 84 us; one chunk and one row:
+// 81.
+int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 4096 ? 2 : 1); }
 
 // Workgroups of the backward pass, each leaving one partial sum of dw and db
 // (of a row beyond kHeldCols: row groups, fewer of them the wider the row is).
 // 256 partial sums instead of 512: 2048 x 14336 49 us instead of 59, 8192 x
-// 8192 84 instead of 89; up to 1024 columns they cost little and 512 fill the
+// 8192 81 instead of 86; up to 1024 columns they cost little and 512 fill the
 // CUs better.
 int bwd_parts(int64_t rows, int64_t cols) {
   if (cols > kHeldCols) return (int)std::min<int64_t>(rows, std::max<int64_t>(1, kMaxParts * (int64_t)kHeldCols / cols));
@@ -539,17 +568,17 @@ void bwd_launch(const BwdArgs &g, int parts, hipStream_t stream) {
       norm_bwd_wide_cols_kernel<TD, SRC, T, LAYER>
           <<<dim3((unsigned)cdiv(g.cols, 256 * kChunk), (unsigned)parts), 256, 0, stream>>>(g);
   } else if (g.cols <= 512) {
-    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 1, LAYER><<<parts, 256, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 1, 1, LAYER><<<parts, 256, 0, stream>>>(g);
   } else if (g.cols <= 1024) {
-    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 2, LAYER><<<parts, 256, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 2, 1, LAYER><<<parts, 256, 0, stream>>>(g);
   } else if (g.cols <= 2048) {
-    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 1, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
   } else if (g.cols <= 4096) {
-    norm_bwd_kernel<TD, SRC, T, TO, 256, 2, 2, LAYER><<<parts, 512, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 2, 2, 2, LAYER><<<parts, 512, 0, stream>>>(g);
   } else if (g.cols <= 8192) {
-    norm_bwd_kernel<TD, SRC, T, TO, 256, 2, 4, LAYER><<<parts, 512, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 1, 2, LAYER><<<parts, 1024, 0, stream>>>(g);
   } else {
-    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 2, LAYER><<<parts, 1024, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 2, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
   }
 }
 
