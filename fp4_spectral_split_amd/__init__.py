@@ -735,7 +735,7 @@ def metis_swiglu_fwd(a, b, dtype=None, save=None, out=None):
     qa = qb = ca = cb = None
     if save is not None:
         if isinstance(save, (tuple, list)):
-            if len(save) != 2 or not all(isinstance(q, Act8Tensor) for q in save):
+            if len(save) != 2 or not all(isinstance(q, Act8Tensor) for q in save) or save[0] is save[1]:
                 raise MetisError("save must be a format or a pair of Act8Tensors")
             qa, qb = _save(save[0], a), _save(save[1], b)
         elif isinstance(save, Act8Tensor):

@@ -170,6 +170,7 @@ def test_empty_and_refused():
            lambda: M.metis_swiglu_fwd(x.t(), y.t()), lambda: M.metis_swiglu_fwd(x, y.cpu()),
            lambda: M.metis_swiglu_fwd(x, y, dtype=torch.float16), lambda: M.metis_swiglu_fwd(x, y, save="nvfp4"),
            lambda: M.metis_swiglu_fwd(x, y, save=q), lambda: M.metis_swiglu_fwd(x, y, save=(q, q2)),
+           lambda: M.metis_swiglu_fwd(x, y, save=(q, q)), lambda: M.metis_swiglu_fwd(x, y, save=(q,)),
            lambda: M.metis_swiglu_fwd(x, y, out=torch.empty(8, 63, device="cuda")),
            lambda: M.metis_swiglu_bwd(x, q, y), lambda: M.metis_swiglu_bwd(x, q, q2),
            lambda: M.metis_swiglu_bwd(x[:, :32], q, q), lambda: M.metis_swiglu_bwd(x, x, y.bfloat16()),
