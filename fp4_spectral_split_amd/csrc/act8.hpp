@@ -38,41 +38,88 @@ template <> struct Raw<float> { uint32_t w[8]; };
 template <> struct Raw<unsigned short> { uint32_t w[4]; };
 template <> struct Raw<uint8_t> { uint32_t w[2]; };
 
-// The chunk at p; of a row's last chunk only n elements exist (zeros follow).
-__device__ __forceinline__ void load_raw(const float *p, int n, Raw<float> &r) {
-  if (n >= kChunk) {
-    const u32x4_a1 a = *(const u32x4_a1 *)p, b = *(const u32x4_a1 *)(p + 4);
+// Eight elements at p, at once.
+__device__ __forceinline__ void load_all(const float *p, Raw<float> &r) {
+  const u32x4_a1 a = *(const u32x4_a1 *)p, b = *(const u32x4_a1 *)(p + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.w[i] = a[i];
-      r.w[4 + i] = b[i];
+  for (int i = 0; i < 4; ++i) {
+    r.w[i] = a[i];
+    r.w[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void load_all(const unsigned short *p, Raw<unsigned short> &r) {
+  const u32x4_a1 a = *(const u32x4_a1 *)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = a[i];
+}
+__device__ __forceinline__ void load_all(const uint8_t *p, Raw<uint8_t> &r) {
+  const u32x2_a1 a = *(const u32x2_a1 *)p;
+  r.w[0] = a[0];
+  r.w[1] = a[1];
+}
+
+__device__ __forceinline__ uint32_t element_bits(const float *p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t element_bits(const unsigned short *p) { return *p; }
+__device__ __forceinline__ uint32_t element_bits(const uint8_t *p) { return *p; }
+
+// Element `back` and the ones after it move to the front, zeros follow (back
+// in 1..7; words by selection, the rest by a funnel shift).
+template <int BY, int W> __device__ __forceinline__ void move_words(uint32_t (&w)[W], bool yes) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const uint32_t from = i + BY < W ? w[(i + BY) % W] : 0u;
+    w[i] = yes ? from : w[i];
+  }
+}
+__device__ __forceinline__ void move_front(Raw<float> &r, int back) {
+  move_words<4>(r.w, back & 4);
+  move_words<2>(r.w, back & 2);
+  move_words<1>(r.w, back & 1);
+}
+__device__ __forceinline__ void move_front(Raw<unsigned short> &r, int back) {
+  move_words<2>(r.w, back & 4);
+  move_words<1>(r.w, back & 2);
+  const uint32_t by = back & 1 ? 16u : 0u;
+  r.w[0] = __builtin_amdgcn_alignbit(r.w[1], r.w[0], by);
+  r.w[1] = __builtin_amdgcn_alignbit(r.w[2], r.w[1], by);
+  r.w[2] = __builtin_amdgcn_alignbit(r.w[3], r.w[2], by);
+  r.w[3] >>= by;
+}
+__device__ __forceinline__ void move_front(Raw<uint8_t> &r, int back) {
+  const uint64_t v = (((uint64_t)r.w[1] << 32) | r.w[0]) >> (8 * back);
+  r.w[0] = (uint32_t)v;
+  r.w[1] = (uint32_t)(v >> 32);
+}
+
+// The chunk at element c of a row of `cols`. Every lane loads eight existing
+// elements, without a branch: the row's last eight where fewer than eight (or
+// none) remain from c on. settle() then puts what exists of the chunk in front
+// and zeros behind it, where the values are first used, so that a load can be
+// under way for as long as its user likes. (A branch per element of the last
+// chunk cost eight round trips to memory per row: gradient of 8192 x 4095 86
+// us, TAIL_B this way.)
+template <typename T> __device__ __forceinline__ void load_raw(const T *row, int cols, int c, Raw<T> &r) {
+  if (cols >= kChunk) {
+    load_all(row + min(c, cols - kChunk), r);
+  } else {  // the elements go where a row's last eight would have them
+    constexpr int W = sizeof(r.w) / 4, PER = 4 / sizeof(T);  // words of a chunk, elements in a word
+#pragma unroll
+    for (int k = 0; k < W; ++k) r.w[k] = 0u;
+#pragma unroll 1
+    for (int i = 0; i < cols; ++i) {
+      const int at = i + kChunk - cols;
+      const uint32_t e = element_bits(row + i) << (32 / PER * (at % PER));
+#pragma unroll
+      for (int k = 0; k < W; ++k) r.w[k] |= at / PER == k ? e : 0u;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
   }
 }
-__device__ __forceinline__ void load_raw(const unsigned short *p, int n, Raw<unsigned short> &r) {
-  if (n >= kChunk) {
-    const u32x4_a1 a = *(const u32x4_a1 *)p;
+// n = cols - c elements of the chunk exist (8 or more: all, 0 or less: none).
+template <typename T> __device__ __forceinline__ void settle(Raw<T> &r, int n) {
+  if (n < kChunk) {
+    move_front(r, kChunk - max(n, 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[i] = a[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-  }
-}
-__device__ __forceinline__ void load_raw(const uint8_t *p, int n, Raw<uint8_t> &r) {
-  if (n >= kChunk) {
-    const u32x2_a1 a = *(const u32x2_a1 *)p;
-    r.w[0] = a[0];
-    r.w[1] = a[1];
-  } else {
-    r.w[0] = r.w[1] = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) r.w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+    for (int k = 0; k < (int)(sizeof(r.w) / 4); ++k) r.w[k] = n > 0 ? r.w[k] : 0u;
   }
 }
 
@@ -256,31 +303,29 @@ __device__ __forceinline__ void decode(const Raw<uint8_t> &r, uint32_t byte, flo
 // the 8-bit form (codes with their scales, tightly packed rows).
 template <int SRC, typename T> struct Chunk {
   Raw<T> raw;
-  __device__ __forceinline__ void load(const void *p, const uint8_t *, int64_t r, int64_t ld, int, int c, int n) {
-    load_raw((const T *)p + r * ld + c, n, raw);
+  __device__ __forceinline__ void load(const void *p, const uint8_t *, int64_t r, int64_t ld, int, int cols, int c) {
+    load_raw((const T *)p + r * ld, cols, c, raw);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const { to_f32(raw, v); }
+  __device__ __forceinline__ void get(int n, float (&v)[8]) {
+    settle(raw, n);
+    to_f32(raw, v);
+  }
 };
-template <typename T> struct Chunk<kFp8, T> {
+template <int FMT> struct StoredChunk {
   Raw<uint8_t> raw;
   uint32_t byte;
-  __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int c,
-                                       int n) {
-    load_raw((const uint8_t *)p + r * ld + c, n, raw);
-    byte = n > 0 ? scales[r * nblk + c / kBlock8] : 0u;
+  __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int cols,
+                                       int c) {
+    load_raw((const uint8_t *)p + r * ld, cols, c, raw);
+    byte = scales[r * nblk + min(c / kBlock8, nblk - 1)];
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const { decode<kFp8>(raw, byte, v); }
-};
-template <typename T> struct Chunk<kInt8, T> {
-  Raw<uint8_t> raw;
-  uint32_t byte;
-  __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int c,
-                                       int n) {
-    load_raw((const uint8_t *)p + r * ld + c, n, raw);
-    byte = n > 0 ? scales[r * nblk + c / kBlock8] : 0u;
+  __device__ __forceinline__ void get(int n, float (&v)[8]) {
+    settle(raw, n);
+    decode<FMT>(raw, byte, v);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const { decode<kInt8>(raw, byte, v); }
 };
+template <typename T> struct Chunk<kFp8, T> : StoredChunk<kFp8> {};
+template <typename T> struct Chunk<kInt8, T> : StoredChunk<kInt8> {};
 
 // ------------------------------------------------------------- positions
 // n / d for n < 2^29 by a multiply-high: m = ceil(2^(29 + l) / d) with

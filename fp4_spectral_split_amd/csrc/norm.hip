@@ -87,17 +87,19 @@ __device__ __forceinline__ float inverse_root(float v) {
 }
 
 // Chunk c of w or b, which may be absent (`fill`) and of either type.
-__device__ __forceinline__ void load_vec(const void *p, int bf16, int c, int n, float fill, float (&v)[8]) {
+__device__ __forceinline__ void load_vec(const void *p, int bf16, int cols, int c, float fill, float (&v)[8]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fill;
   } else if (bf16) {
     Raw<unsigned short> r;
-    load_raw((const unsigned short *)p + c, n, r);
+    load_raw((const unsigned short *)p, cols, c, r);
+    settle(r, cols - c);
     to_f32(r, v);
   } else {
     Raw<float> r;
-    load_raw((const float *)p + c, n, r);
+    load_raw((const float *)p, cols, c, r);
+    settle(r, cols - c);
     to_f32(r, v);
   }
 }
@@ -117,30 +119,32 @@ struct FwdArgs {
   float n, inv_n, eps;  // n = cols
 };
 
-// LANES threads hold a row as V chunks each; the workgroups take the rows in
-// turn (a wave per row: four rows per workgroup at once).
-template <typename T, typename TY, int LANES, int V, bool LAYER, int STORE>
-__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_fwd_kernel(FwdArgs g) {
-  constexpr int GROUPS = LANES < 256 ? 256 / LANES : 1;
-  __shared__ float red[2][1][LANES / 64];
+// LANES threads hold a row as V chunks each, GROUPS rows are worked on at once;
+// the workgroups take the rows in turn.
+template <typename T, typename TY, int LANES, int GROUPS, int V, bool LAYER, int STORE>
+__global__ void __launch_bounds__(LANES *GROUPS) norm_fwd_kernel(FwdArgs g) {
+  __shared__ float red[2][GROUPS][1][LANES / 64];
   const int t = threadIdx.x % LANES;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   float w[V][8], b[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * LANES + t) * kChunk;
-    load_vec(g.w, g.w_bf16, c, g.cols - c, 1.0f, w[v]);
-    load_vec(g.b, g.w_bf16, c, g.cols - c, 0.0f, b[v]);
+    load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
+    load_vec(g.b, g.w_bf16, g.cols, c, 0.0f, b[v]);
   }
   int slot = 0;
   const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
-  for (int64_t r = (int64_t)blockIdx.x * GROUPS + grp; r < g.rows; r += step) {
+  // every group runs the same steps (they meet at barriers); past the last row
+  // it works on zeros
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + grp; r < g.rows + grp; r += step) {
+    const int cols = r < g.rows ? g.cols : 0;
+    const T *row = (const T *)g.x + min(r, g.rows - 1) * g.ldx;
     Raw<T> raw[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk;
-      load_raw((const T *)g.x + r * g.ldx + c, g.cols - c, raw[v]);
-    }
+    for (int v = 0; v < V; ++v) load_raw(row, g.cols, (v * LANES + t) * kChunk, raw[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) settle(raw[v], cols - (v * LANES + t) * kChunk);
     float d[V][8], mean = 0.0f, sum[1];
 #pragma unroll
     for (int v = 0; v < V; ++v) to_f32(raw[v], d[v]);
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_fwd_kernel(Fwd
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[0] += d[v][i];
-      row_sum<LANES, 1>(sum, &red[slot]);
+      row_sum<LANES, 1>(sum, &red[slot][grp]);
       slot ^= 1;
       mean = divide(sum[0], g.n, g.inv_n);
 #pragma unroll
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_fwd_kernel(Fwd
     sum[0] = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int n = g.cols - (v * LANES + t) * kChunk;
+      const int n = cols - (v * LANES + t) * kChunk;
       if (!LAYER || n >= kChunk) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[0] = fmaf(d[v][i], d[v][i], sum[0]);
@@ -170,16 +174,16 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) norm_fwd_kernel(Fwd
         for (int i = 0; i < 8; ++i) sum[0] = i < n ? fmaf(d[v][i], d[v][i], sum[0]) : sum[0];
       }
     }
-    row_sum<LANES, 1>(sum, &red[slot]);
+    row_sum<LANES, 1>(sum, &red[slot][grp]);
     slot ^= 1;
     const float rstd = inverse_root(divide(sum[0], g.n, g.inv_n) + g.eps);
-    if (t == 0) {
+    if (t == 0 && r < g.rows) {
       if (LAYER && g.mean) g.mean[r] = mean;
       if (g.rstd) g.rstd[r] = rstd;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      const int c = (v * LANES + t) * kChunk, n = cols - c;
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = fmaf(d[v][i] * rstd, w[v][i], b[v][i]);
@@ -211,7 +215,8 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
     if (LAYER) {
       float s[1] = {0.0f};
       for (int c = t * kChunk; c < g.cols; c += step) {
-        load_raw(row + c, g.cols - c, raw);
+        load_raw(row, g.cols, c, raw);
+        settle(raw, g.cols - c);
         to_f32(raw, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] += x[i];
@@ -223,7 +228,8 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
     float ss[1] = {0.0f};
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
-      load_raw(row + c, n, raw);
+      load_raw(row, g.cols, c, raw);
+      settle(raw, n);
       to_f32(raw, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -241,10 +247,11 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
     for (int c = t * kChunk; c < end; c += step) {  // whole blocks: the lanes of a quad stay together
       const int n = g.cols - c;
       float w[8], b[8], y[8];
-      load_raw(row + c, n, raw);
+      load_raw(row, g.cols, c, raw);
+      settle(raw, n);
       to_f32(raw, x);
-      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
-      load_vec(g.b, g.w_bf16, c, n, 0.0f, b);
+      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      load_vec(g.b, g.w_bf16, g.cols, c, 0.0f, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = fmaf((x[i] - mean) * rstd, w[i], b[i]);
       store_chunk((TY *)g.y + r * g.ldy + c, y, n);
@@ -301,15 +308,15 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
   // every group runs the same steps (they meet at barriers); past the last row
   // it works on zeros
   auto load = [&](int64_t r, Row &row) {
-    const bool live = r < g.rows;
+    r = min(r, g.rows - 1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = live ? g.cols - c : 0;
-      load_raw((const TD *)g.dy + r * g.lddy + c, n, row.d[v]);
-      row.x[v].load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+      const int c = (v * LANES + t) * kChunk;
+      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, row.d[v]);
+      row.x[v].load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
     }
-    row.rstd = live ? g.rstd[r] : 0.0f;
-    row.mean = LAYER && live ? g.mean[r] : 0.0f;
+    row.rstd = g.rstd[r];
+    row.mean = LAYER ? g.mean[r] : 0.0f;
   };
   int64_t r0 = (int64_t)blockIdx.x * GROUPS + grp;
   const int64_t end = g.rows + grp;  // of r0: the same step for every group
@@ -320,19 +327,22 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * LANES + t) * kChunk;
-    load_vec(g.w, g.w_bf16, c, g.cols - c, 1.0f, w[v]);
+    load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.0f;
   }
   int slot = 0;
-  auto work = [&](int64_t r, const Row &row) {
+  auto work = [&](int64_t r, Row &row) {
     const float rstd = row.rstd, mean = row.mean;
+    const int cols = r < g.rows ? g.cols : 0;
     float dr[V][8], xc[V][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      const int n = cols - (v * LANES + t) * kChunk;
       float d[8];
+      settle(row.d[v], n);
       to_f32(row.d[v], d);
-      row.x[v].get(xc[v]);
+      row.x[v].get(n, xc[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // past the row's end dy is zero: no term of any sum
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
     const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = r < g.rows ? g.cols - c : 0;
+      const int c = (v * LANES + t) * kChunk, n = cols - c;
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = fmaf(dr[v][i], w[v][i], fmaf(-k2, xc[v][i], -k1));
@@ -417,11 +427,12 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
     Chunk<SRC, T> rx;
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
-      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
-      rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
-      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
+      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+      rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      settle(rd, n);
       to_f32(rd, d);
-      rx.get(x);
+      rx.get(n, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gi = d[i] * w[i];
@@ -435,11 +446,12 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
       float o[8];
-      load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
-      rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
-      load_vec(g.w, g.w_bf16, c, n, 1.0f, w);
+      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+      rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      settle(rd, n);
       to_f32(rd, d);
-      rx.get(x);
+      rx.get(n, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i] * rstd, w[i], fmaf(-k2, x[i] - mean, -k1));
       store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
@@ -460,10 +472,11 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(BwdArgs g) {
     Raw<TD> rd;
     Chunk<SRC, T> rx;
     float d[8], x[8];
-    load_raw((const TD *)g.dy + r * g.lddy + c, n, rd);
-    rx.load(g.x, g.scales, r, g.ldx, g.nblk, c, n);
+    load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+    rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+    settle(rd, n);
     to_f32(rd, d);
-    rx.get(x);
+    rx.get(n, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       aw[i] = fmaf(d[i] * rstd, x[i] - mean, aw[i]);
@@ -509,23 +522,28 @@ __global__ void __launch_bounds__(kFinishThreads)
 }
 
 // -------------------------------------------------------------- launches
-// A row is held by one wave up to 1024 columns, by four up to 8192 and by
-// sixteen up to kHeldCols. (4096 x 2048 fp32: four waves 10.2 us, one wave
-// 11.5; 8192 x 4096 bf16: four waves 26.5, two 29, one 48, eight 28.)
-int lanes_of(int64_t cols) { return cols <= 1024 ? 64 : (cols <= 8192 ? 256 : 1024); }
-
+#ifndef F1L
+#define F1L 256
+#define F1G 1
+#define F1V 1
+#define F2L 256
+#define F2G 1
+#define F2V 2
+#define F3L 512
+#define F3G 1
+#define F3V 2
+#define F3GRID 1024
+#endif
 template <typename T, typename TY, bool LAYER, int STORE> void fwd_launch(const FwdArgs &g, hipStream_t stream) {
-  const int lanes = lanes_of(g.cols);
   // enough workgroups to fill the GPU, each with its w and b over several rows
-  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(g.rows, lanes == 64 ? 4 : 1), lanes == 1024 ? 512 : 2048);
-  const int per = (int)cdiv(g.cols, (int64_t)lanes * kChunk);
-  if (g.cols > kHeldCols) norm_fwd_wide_kernel<T, TY, LAYER, STORE><<<grid, kWide, 0, stream>>>(g);
-  else if (lanes == 64 && per <= 1) norm_fwd_kernel<T, TY, 64, 1, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
-  else if (lanes == 64) norm_fwd_kernel<T, TY, 64, 2, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
-  else if (lanes == 256 && per <= 1) norm_fwd_kernel<T, TY, 256, 1, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
-  else if (lanes == 256 && per <= 2) norm_fwd_kernel<T, TY, 256, 2, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
-  else if (lanes == 256) norm_fwd_kernel<T, TY, 256, 4, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
-  else norm_fwd_kernel<T, TY, 1024, 2, LAYER, STORE><<<grid, 1024, 0, stream>>>(g);
+  auto grid = [&](int groups, int most) { return (unsigned)std::min<int64_t>(cdiv(g.rows, groups), most); };
+  if (g.cols <= 512) norm_fwd_kernel<T, TY, 64, 4, 1, LAYER, STORE><<<grid(4, 2048), 256, 0, stream>>>(g);
+  else if (g.cols <= 1024) norm_fwd_kernel<T, TY, 64, 4, 2, LAYER, STORE><<<grid(4, 2048), 256, 0, stream>>>(g);
+  else if (g.cols <= 2048) norm_fwd_kernel<T, TY, F1L, F1G, F1V, LAYER, STORE><<<grid(F1G, 2048), F1L * F1G, 0, stream>>>(g);
+  else if (g.cols <= 4096) norm_fwd_kernel<T, TY, F2L, F2G, F2V, LAYER, STORE><<<grid(F2G, 2048), F2L * F2G, 0, stream>>>(g);
+  else if (g.cols <= 8192) norm_fwd_kernel<T, TY, F3L, F3G, F3V, LAYER, STORE><<<grid(F3G, F3GRID), F3L * F3G, 0, stream>>>(g);
+  else if (g.cols <= kHeldCols) norm_fwd_kernel<T, TY, 1024, 1, 2, LAYER, STORE><<<grid(1, 512), 1024, 0, stream>>>(g);
+  else norm_fwd_wide_kernel<T, TY, LAYER, STORE><<<grid(1, 512), kWide, 0, stream>>>(g);
 }
 
 template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer, int store, hipStream_t stream) {
@@ -547,7 +565,7 @@ template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer
 // waiting for each other at every row's barrier. 8192 x 8192 bf16 with four
 // chunks of a row per thread, two rows at once: 84 us; one chunk and one row:
 // 81.
-int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 4096 ? 2 : 1); }
+int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 6144 ? 2 : 1); }
 
 // Workgroups of the backward pass, each leaving one partial sum of dw and db
 // (of a row beyond kHeldCols: row groups, fewer of them the wider the row is).
@@ -575,6 +593,8 @@ void bwd_launch(const BwdArgs &g, int parts, hipStream_t stream) {
     norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 1, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
   } else if (g.cols <= 4096) {
     norm_bwd_kernel<TD, SRC, T, TO, 256, 2, 2, 2, LAYER><<<parts, 512, 0, stream>>>(g);
+  } else if (g.cols <= 6144) {
+    norm_bwd_kernel<TD, SRC, T, TO, 384, 2, 2, 2, LAYER><<<parts, 768, 0, stream>>>(g);
   } else if (g.cols <= 8192) {
     norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 1, 2, LAYER><<<parts, 1024, 0, stream>>>(g);
   } else {
