@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t r = nb.div(blk);
   const int c = (int)((blk - r * nb.d) * kBlock8 + (u & 3u) * kChunk), n = cols - c;
   Raw<T> raw;
-  load_raw(x + r * ldx, cols, c, raw);
+  load_raw<true>(x + r * ldx, cols, c, raw);
   settle(raw, n);
   const uint32_t byte = scale_byte<FMT>(quad_max(amax_bits(raw)));
   float v[8];
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t r = nb.div(blk);
   const int c = (int)((blk - r * nb.d) * kBlock8 + (u & 3u) * kChunk), n = cols - c;
   Raw<uint8_t> raw;
-  load_raw(codes + (int64_t)r * cols, cols, c, raw);
+  load_raw<true>(codes + (int64_t)r * cols, cols, c, raw);
   settle(raw, n);
   float v[8];
   decode<FMT>(raw, scales[blk], v);

@@ -97,9 +97,11 @@ __device__ __forceinline__ void move_front(Raw<uint8_t> &r, int back) {
 // and zeros behind it, where the values are first used, so that a load can be
 // under way for as long as its user likes. (A branch per element of the last
 // chunk cost eight round trips to memory per row: gradient of 8192 x 4095 86
-// us, TAIL_B this way.)
-template <typename T> __device__ __forceinline__ void load_raw(const T *row, int cols, int c, Raw<T> &r) {
-  if (cols >= kChunk) {
+// us, 47 this way.)
+// NARROW: the row may have fewer than eight elements.
+template <bool NARROW, typename T>
+__device__ __forceinline__ void load_raw(const T *row, int cols, int c, Raw<T> &r) {
+  if (!NARROW || cols >= kChunk) {
     load_all(row + min(c, cols - kChunk), r);
   } else {  // the elements go where a row's last eight would have them
     constexpr int W = sizeof(r.w) / 4, PER = 4 / sizeof(T);  // words of a chunk, elements in a word
@@ -303,26 +305,22 @@ __device__ __forceinline__ void decode(const Raw<uint8_t> &r, uint32_t byte, flo
 // the 8-bit form (codes with their scales, tightly packed rows).
 template <int SRC, typename T> struct Chunk {
   Raw<T> raw;
+  template <bool NARROW>
   __device__ __forceinline__ void load(const void *p, const uint8_t *, int64_t r, int64_t ld, int, int cols, int c) {
-    load_raw((const T *)p + r * ld, cols, c, raw);
+    load_raw<NARROW>((const T *)p + r * ld, cols, c, raw);
   }
-  __device__ __forceinline__ void get(int n, float (&v)[8]) {
-    settle(raw, n);
-    to_f32(raw, v);
-  }
+  __device__ __forceinline__ void value(float (&v)[8]) const { to_f32(raw, v); }
 };
 template <int FMT> struct StoredChunk {
   Raw<uint8_t> raw;
   uint32_t byte;
+  template <bool NARROW>
   __device__ __forceinline__ void load(const void *p, const uint8_t *scales, int64_t r, int64_t ld, int nblk, int cols,
                                        int c) {
-    load_raw((const uint8_t *)p + r * ld, cols, c, raw);
+    load_raw<NARROW>((const uint8_t *)p + r * ld, cols, c, raw);
     byte = scales[r * nblk + min(c / kBlock8, nblk - 1)];
   }
-  __device__ __forceinline__ void get(int n, float (&v)[8]) {
-    settle(raw, n);
-    decode<FMT>(raw, byte, v);
-  }
+  __device__ __forceinline__ void value(float (&v)[8]) const { decode<FMT>(raw, byte, v); }
 };
 template <typename T> struct Chunk<kFp8, T> : StoredChunk<kFp8> {};
 template <typename T> struct Chunk<kInt8, T> : StoredChunk<kInt8> {};

@@ -48,27 +48,59 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (readlane_f32(v, 0) + readlane_f32(v, 16)) + (readlane_f32(v, 32) + readlane_f32(v, 48));
 }
 
-// Sums of N values over the LANES threads of a row: a wave, or several waves
-// through LDS. `slot` alternates between calls, so that one barrier per call
-// is enough: a wave writes a slot again only after the barrier of the call in
+// How a workgroup of up to MAXT threads is laid over rows: GROUPS rows at once,
+// each held by `lanes` threads (whole waves, as many as its width takes) as V
+// chunks per thread, chunk v of thread t being chunk v lanes + t of the row.
+template <int MAXT, int GROUPS> struct Layout {
+  static constexpr int kWaves = MAXT / GROUPS / 64;  // waves of a row at most
+  int lanes, grp, t;
+  __device__ __forceinline__ Layout() {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = kWaves == 1 ? 1 : (int)blockDim.x / (64 * GROUPS);
+    grp = 0;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) grp += wave >= k * waves;
+    lanes = 64 * waves;
+    t = (int)threadIdx.x - grp * lanes;
+  }
+};
+
+// Where the waves of a row leave their sums: N values of each, the entries past
+// the row's waves zero.
+template <int MAXT, int GROUPS, int N> struct RowSums {
+  static constexpr int kWaves = Layout<MAXT, GROUPS>::kWaves, kPad = (kWaves + 3) / 4 * 4;
+  float v[2][GROUPS][N][kPad];
+};
+template <int MAXT, int GROUPS, int N> __device__ __forceinline__ void clear(RowSums<MAXT, GROUPS, N> &red) {
+  if (Layout<MAXT, GROUPS>::kWaves == 1) return;
+  float *p = &red.v[0][0][0][0];
+  for (int i = threadIdx.x; i < (int)(sizeof(red) / sizeof(float)); i += blockDim.x) p[i] = 0.0f;
+  __syncthreads();
+}
+
+// Sums of N values over the threads of a row: a wave, or several waves through
+// LDS. `slot` alternates between calls, so that one barrier per call is
+// enough: a wave writes a slot again only after the barrier of the call in
 // between, which every wave reaches after it has read that slot.
-template <int LANES, int N> __device__ __forceinline__ void row_sum(float (&a)[N], float (*red)[N][LANES / 64]) {
+template <int MAXT, int GROUPS, int N>
+__device__ __forceinline__ void row_sum(float (&a)[N], RowSums<MAXT, GROUPS, N> &red, int &slot,
+                                        const Layout<MAXT, GROUPS> &at) {
 #pragma unroll
   for (int k = 0; k < N; ++k) a[k] = wave_sum(a[k]);
-  if (LANES > 64) {
-    const int wave = (threadIdx.x % LANES) >> 6;
+  if (Layout<MAXT, GROUPS>::kWaves > 1) {
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) (*red)[k][wave] = a[k];
+      for (int k = 0; k < N; ++k) red.v[slot][at.grp][k][at.t >> 6] = a[k];
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < LANES / 64; ++w) s += (*red)[k][w];
+      for (int w = 0; w < RowSums<MAXT, GROUPS, N>::kPad; ++w) s += red.v[slot][at.grp][k][w];
       a[k] = s;
     }
+    slot ^= 1;
   }
 }
 
@@ -87,18 +119,19 @@ __device__ __forceinline__ float inverse_root(float v) {
 }
 
 // Chunk c of w or b, which may be absent (`fill`) and of either type.
+template <bool NARROW>
 __device__ __forceinline__ void load_vec(const void *p, int bf16, int cols, int c, float fill, float (&v)[8]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fill;
   } else if (bf16) {
     Raw<unsigned short> r;
-    load_raw((const unsigned short *)p, cols, c, r);
+    load_raw<NARROW>((const unsigned short *)p, cols, c, r);
     settle(r, cols - c);
     to_f32(r, v);
   } else {
     Raw<float> r;
-    load_raw((const float *)p, cols, c, r);
+    load_raw<NARROW>((const float *)p, cols, c, r);
     settle(r, cols - c);
     to_f32(r, v);
   }
@@ -119,53 +152,53 @@ struct FwdArgs {
   float n, inv_n, eps;  // n = cols
 };
 
-// LANES threads hold a row as V chunks each, GROUPS rows are worked on at once;
-// the workgroups take the rows in turn.
-template <typename T, typename TY, int LANES, int GROUPS, int V, bool LAYER, int STORE>
-__global__ void __launch_bounds__(LANES *GROUPS) norm_fwd_kernel(FwdArgs g) {
-  __shared__ float red[2][GROUPS][1][LANES / 64];
-  const int t = threadIdx.x % LANES;
+// The rows of the workgroups in turn, held in registers.
+template <typename T, typename TY, int MAXT, int GROUPS, int V, bool LAYER, int STORE>
+__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(FwdArgs g) {
+  __shared__ RowSums<MAXT, GROUPS, 1> red;
+  constexpr bool NARROW = MAXT == 64 * GROUPS && V == 1;  // the kernel of the narrowest rows
+  const Layout<MAXT, GROUPS> at;
+  clear(red);
+  const int t = at.t, lanes = at.lanes;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   float w[V][8], b[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = (v * LANES + t) * kChunk;
-    load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
-    load_vec(g.b, g.w_bf16, g.cols, c, 0.0f, b[v]);
+    const int c = (v * lanes + t) * kChunk;
+    load_vec<NARROW>(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
+    load_vec<NARROW>(g.b, g.w_bf16, g.cols, c, 0.0f, b[v]);
   }
   int slot = 0;
-  const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
   // every group runs the same steps (they meet at barriers); past the last row
   // it works on zeros
-  for (int64_t r = (int64_t)blockIdx.x * GROUPS + grp; r < g.rows + grp; r += step) {
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + at.grp; r < g.rows + at.grp; r += step) {
     const int cols = r < g.rows ? g.cols : 0;
     const T *row = (const T *)g.x + min(r, g.rows - 1) * g.ldx;
     Raw<T> raw[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_raw(row, g.cols, (v * LANES + t) * kChunk, raw[v]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) settle(raw[v], cols - (v * LANES + t) * kChunk);
-    float d[V][8], mean = 0.0f, sum[1];
-#pragma unroll
-    for (int v = 0; v < V; ++v) to_f32(raw[v], d[v]);
-    if (LAYER) {
-      sum[0] = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] += d[v][i];
-      row_sum<LANES, 1>(sum, &red[slot][grp]);
-      slot ^= 1;
-      mean = divide(sum[0], g.n, g.inv_n);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[v][i] -= mean;
-    }
-    sum[0] = 0.0f;
+    for (int v = 0; v < V; ++v) load_raw<NARROW>(row, g.cols, (v * lanes + t) * kChunk, raw[v]);
+    float d[V][8], mean = 0.0f, sum[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int n = cols - (v * LANES + t) * kChunk;
+      settle(raw[v], cols - (v * lanes + t) * kChunk);
+      to_f32(raw[v], d[v]);
+      if (LAYER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[0] += d[v][i];
+      }
+    }
+    if (LAYER) {
+      row_sum(sum, red, slot, at);
+      mean = divide(sum[0], g.n, g.inv_n);
+      sum[0] = 0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (LAYER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[v][i] -= mean;
+      }
+      const int n = cols - (v * lanes + t) * kChunk;
       if (!LAYER || n >= kChunk) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[0] = fmaf(d[v][i], d[v][i], sum[0]);
@@ -174,8 +207,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_fwd_kernel(FwdArgs g) {
         for (int i = 0; i < 8; ++i) sum[0] = i < n ? fmaf(d[v][i], d[v][i], sum[0]) : sum[0];
       }
     }
-    row_sum<LANES, 1>(sum, &red[slot][grp]);
-    slot ^= 1;
+    row_sum(sum, red, slot, at);
     const float rstd = inverse_root(divide(sum[0], g.n, g.inv_n) + g.eps);
     if (t == 0 && r < g.rows) {
       if (LAYER && g.mean) g.mean[r] = mean;
@@ -183,7 +215,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_fwd_kernel(FwdArgs g) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = cols - c;
+      const int c = (v * lanes + t) * kChunk, n = cols - c;
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = fmaf(d[v][i] * rstd, w[v][i], b[v][i]);
@@ -205,7 +237,9 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_fwd_kernel(FwdArgs g) {
 // once for the result.
 template <typename T, typename TY, bool LAYER, int STORE>
 __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
-  __shared__ float red[2][1][kWide / 64];
+  __shared__ RowSums<kWide, 1, 1> red;
+  const Layout<kWide, 1> at;
+  clear(red);
   const int t = threadIdx.x, step = kWide * kChunk, end = g.nblk * kBlock8;
   int slot = 0;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
@@ -215,20 +249,19 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
     if (LAYER) {
       float s[1] = {0.0f};
       for (int c = t * kChunk; c < g.cols; c += step) {
-        load_raw(row, g.cols, c, raw);
+        load_raw<false>(row, g.cols, c, raw);
         settle(raw, g.cols - c);
         to_f32(raw, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] += x[i];
       }
-      row_sum<kWide, 1>(s, &red[slot]);
-      slot ^= 1;
+      row_sum(s, red, slot, at);
       mean = divide(s[0], g.n, g.inv_n);
     }
     float ss[1] = {0.0f};
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
-      load_raw(row, g.cols, c, raw);
+      load_raw<false>(row, g.cols, c, raw);
       settle(raw, n);
       to_f32(raw, x);
 #pragma unroll
@@ -237,8 +270,7 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
         ss[0] = fmaf(d, d, ss[0]);
       }
     }
-    row_sum<kWide, 1>(ss, &red[slot]);
-    slot ^= 1;
+    row_sum(ss, red, slot, at);
     const float rstd = inverse_root(divide(ss[0], g.n, g.inv_n) + g.eps);
     if (t == 0) {
       if (LAYER && g.mean) g.mean[r] = mean;
@@ -247,11 +279,11 @@ __global__ void __launch_bounds__(kWide) norm_fwd_wide_kernel(FwdArgs g) {
     for (int c = t * kChunk; c < end; c += step) {  // whole blocks: the lanes of a quad stay together
       const int n = g.cols - c;
       float w[8], b[8], y[8];
-      load_raw(row, g.cols, c, raw);
+      load_raw<false>(row, g.cols, c, raw);
       settle(raw, n);
       to_f32(raw, x);
-      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
-      load_vec(g.b, g.w_bf16, g.cols, c, 0.0f, b);
+      load_vec<false>(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      load_vec<false>(g.b, g.w_bf16, g.cols, c, 0.0f, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = fmaf((x[i] - mean) * rstd, w[i], b[i]);
       store_chunk((TY *)g.y + r * g.ldy + c, y, n);
@@ -291,18 +323,20 @@ template <typename TD, int SRC, typename T, int V> struct BwdRow {
   float mean, rstd;
 };
 
-// LANES threads hold a row, GROUPS rows are worked on at once, and every
-// thread keeps the sums of dw and db of its columns in registers over all rows
-// of its group. With dr = dy rstd and xc = x - mean held from the reductions
+// GROUPS rows are worked on at once, and every thread keeps the sums of dw and
+// db of its columns in registers over all rows of its group. With dr = dy rstd and xc = x - mean held from the reductions
 // (S1 = sum(dy w), S2 = sum(dy w xc)) the result is
 //   dx = dr w - rstd S1 / n - xc rstd^3 S2 / n.
 // DEPTH sets of rows are in registers: one worked on, the others on their way
 // (8192 x 4096, bf16 dy and MXFP8 x: one set 42.0 us with the join of the sums,
 // two 39.7, three 40.7).
-template <typename TD, int SRC, typename T, typename TO, int LANES, int GROUPS, int V, int DEPTH, bool LAYER>
-__global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
-  __shared__ float red[2][GROUPS][2][LANES / 64];
-  const int t = threadIdx.x % LANES, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+template <typename TD, int SRC, typename T, typename TO, int MAXT, int GROUPS, int V, int DEPTH, bool LAYER>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(BwdArgs g) {
+  __shared__ RowSums<MAXT, GROUPS, 2> red;
+  constexpr bool NARROW = MAXT == 64 * GROUPS && V == 1;  // the kernel of the narrowest rows
+  const Layout<MAXT, GROUPS> at;
+  clear(red);
+  const int t = at.t, lanes = at.lanes, grp = at.grp;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   typedef BwdRow<TD, SRC, T, V> Row;
   // every group runs the same steps (they meet at barriers); past the last row
@@ -311,9 +345,9 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
     r = min(r, g.rows - 1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk;
-      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, row.d[v]);
-      row.x[v].load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+      const int c = (v * lanes + t) * kChunk;
+      load_raw<NARROW>((const TD *)g.dy + r * g.lddy, g.cols, c, row.d[v]);
+      row.x[v].template load<NARROW>(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
     }
     row.rstd = g.rstd[r];
     row.mean = LAYER ? g.mean[r] : 0.0f;
@@ -326,8 +360,8 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
   float w[V][8], aw[V][8], ab[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = (v * LANES + t) * kChunk;
-    load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
+    const int c = (v * lanes + t) * kChunk;
+    load_vec<NARROW>(g.w, g.w_bf16, g.cols, c, 1.0f, w[v]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.0f;
   }
@@ -338,11 +372,12 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
     float dr[V][8], xc[V][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int n = cols - (v * LANES + t) * kChunk;
+      const int n = cols - (v * lanes + t) * kChunk;
       float d[8];
       settle(row.d[v], n);
+      settle(row.x[v].raw, n);
       to_f32(row.d[v], d);
-      row.x[v].get(n, xc[v]);
+      row.x[v].value(xc[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // past the row's end dy is zero: no term of any sum
@@ -355,12 +390,11 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
         ab[v][i] += d[i];
       }
     }
-    row_sum<LANES, 2>(s, &red[slot][grp]);
-    slot ^= 1;
+    row_sum(s, red, slot, at);
     const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = cols - c;
+      const int c = (v * lanes + t) * kChunk, n = cols - c;
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = fmaf(dr[v][i], w[v][i], fmaf(-k2, xc[v][i], -k1));
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
   if (!g.pw && !g.pb) return;
   // the groups of a workgroup join through LDS, in order
   if (GROUPS > 1) {
-    __shared__ float join[GROUPS > 1 ? V * LANES * kChunk : 1];
+    __shared__ float join[GROUPS > 1 ? V * (MAXT / GROUPS) * kChunk : 1];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       for (int k = 1; k < GROUPS; ++k) {
@@ -388,7 +422,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
 #pragma unroll
           for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) join[(v * 8 + i) * LANES + t] = which ? ab[v][i] : aw[v][i];
+            for (int i = 0; i < 8; ++i) join[(v * 8 + i) * lanes + t] = which ? ab[v][i] : aw[v][i];
         }
         __syncthreads();
         if (grp == 0) {
@@ -397,7 +431,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float &a = which ? ab[v][i] : aw[v][i];
-              a += join[(v * 8 + i) * LANES + t];
+              a += join[(v * 8 + i) * lanes + t];
             }
         }
       }
@@ -406,7 +440,7 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
   if (grp == 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * LANES + t) * kChunk, n = g.cols - c;
+      const int c = (v * lanes + t) * kChunk, n = g.cols - c;
       if (g.pw) store_chunk(g.pw + (int64_t)blockIdx.x * g.cols + c, aw[v], n);
       if (g.pb) store_chunk(g.pb + (int64_t)blockIdx.x * g.cols + c, ab[v], n);
     }
@@ -417,7 +451,9 @@ __global__ void __launch_bounds__(LANES *GROUPS) norm_bwd_kernel(BwdArgs g) {
 // of their own.
 template <typename TD, int SRC, typename T, typename TO, bool LAYER>
 __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
-  __shared__ float red[2][2][kWide / 64];
+  __shared__ RowSums<kWide, 1, 2> red;
+  const Layout<kWide, 1> at;
+  clear(red);
   const int t = threadIdx.x, step = kWide * kChunk;
   int slot = 0;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
@@ -427,12 +463,13 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
     Chunk<SRC, T> rx;
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
-      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
-      rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
-      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      load_raw<false>((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+      rx.template load<false>(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+      load_vec<false>(g.w, g.w_bf16, g.cols, c, 1.0f, w);
       settle(rd, n);
       to_f32(rd, d);
-      rx.get(n, x);
+      settle(rx.raw, n);
+      rx.value(x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gi = d[i] * w[i];
@@ -440,18 +477,18 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
         s[1] = fmaf(gi, x[i] - mean, s[1]);
       }
     }
-    row_sum<kWide, 2>(s, &red[slot]);
-    slot ^= 1;
+    row_sum(s, red, slot, at);
     const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
       float o[8];
-      load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
-      rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
-      load_vec(g.w, g.w_bf16, g.cols, c, 1.0f, w);
+      load_raw<false>((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+      rx.template load<false>(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+      load_vec<false>(g.w, g.w_bf16, g.cols, c, 1.0f, w);
       settle(rd, n);
       to_f32(rd, d);
-      rx.get(n, x);
+      settle(rx.raw, n);
+      rx.value(x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i] * rstd, w[i], fmaf(-k2, x[i] - mean, -k1));
       store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
@@ -472,11 +509,12 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(BwdArgs g) {
     Raw<TD> rd;
     Chunk<SRC, T> rx;
     float d[8], x[8];
-    load_raw((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
-    rx.load(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
+    load_raw<false>((const TD *)g.dy + r * g.lddy, g.cols, c, rd);
+    rx.template load<false>(g.x, g.scales, r, g.ldx, g.nblk, g.cols, c);
     settle(rd, n);
     to_f32(rd, d);
-    rx.get(n, x);
+    settle(rx.raw, n);
+    rx.value(x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       aw[i] = fmaf(d[i] * rstd, x[i] - mean, aw[i]);
@@ -522,28 +560,39 @@ __global__ void __launch_bounds__(kFinishThreads)
 }
 
 // -------------------------------------------------------------- launches
-#ifndef F1L
-#define F1L 256
-#define F1G 1
-#define F1V 1
-#define F2L 256
-#define F2G 1
-#define F2V 2
-#define F3L 512
-#define F3G 1
-#define F3V 2
-#define F3GRID 1024
-#endif
+// Workgroups for `sets` of rows, at most `most` of them: as few as finish in
+// the same number of rounds, so that none runs a round nearly alone.
+int64_t balanced(int64_t sets, int64_t most) { return cdiv(sets, cdiv(sets, most)); }
+
+// Threads that hold a row as v chunks each, in units of `unit`.
+unsigned lanes_for(int cols, int v, int unit) { return (unsigned)cdiv(cols, (int64_t)v * unit * kChunk) * unit; }
+
 template <typename T, typename TY, bool LAYER, int STORE> void fwd_launch(const FwdArgs &g, hipStream_t stream) {
-  // enough workgroups to fill the GPU, each with its w and b over several rows
-  auto grid = [&](int groups, int most) { return (unsigned)std::min<int64_t>(cdiv(g.rows, groups), most); };
-  if (g.cols <= 512) norm_fwd_kernel<T, TY, 64, 4, 1, LAYER, STORE><<<grid(4, 2048), 256, 0, stream>>>(g);
-  else if (g.cols <= 1024) norm_fwd_kernel<T, TY, 64, 4, 2, LAYER, STORE><<<grid(4, 2048), 256, 0, stream>>>(g);
-  else if (g.cols <= 2048) norm_fwd_kernel<T, TY, F1L, F1G, F1V, LAYER, STORE><<<grid(F1G, 2048), F1L * F1G, 0, stream>>>(g);
-  else if (g.cols <= 4096) norm_fwd_kernel<T, TY, F2L, F2G, F2V, LAYER, STORE><<<grid(F2G, 2048), F2L * F2G, 0, stream>>>(g);
-  else if (g.cols <= 8192) norm_fwd_kernel<T, TY, F3L, F3G, F3V, LAYER, STORE><<<grid(F3G, F3GRID), F3L * F3G, 0, stream>>>(g);
-  else if (g.cols <= kHeldCols) norm_fwd_kernel<T, TY, 1024, 1, 2, LAYER, STORE><<<grid(1, 512), 1024, 0, stream>>>(g);
-  else norm_fwd_wide_kernel<T, TY, LAYER, STORE><<<grid(1, 512), kWide, 0, stream>>>(g);
+  if (g.cols <= 1024) {  // a wave per row
+    const unsigned grid = (unsigned)balanced(cdiv(g.rows, 4), 2048);
+    if (g.cols <= 512) norm_fwd_kernel<T, TY, 256, 4, 1, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+    else norm_fwd_kernel<T, TY, 256, 4, 2, LAYER, STORE><<<grid, 256, 0, stream>>>(g);
+    return;
+  }
+  if (g.cols > kHeldCols) {
+    norm_fwd_wide_kernel<T, TY, LAYER, STORE><<<(unsigned)std::min<int64_t>(g.rows, 512), kWide, 0, stream>>>(g);
+    return;
+  }
+  // Up to 6144 columns at most four waves, one on each SIMD: the fifth wave of a
+  // workgroup shares the first one's SIMD, and so does every workgroup's (8192 x
+  // 4100 with its input stored, five waves of two chunks 57 us, four of three
+  // 47); beyond, whole sets of four (14336 columns in 16 waves 119 us, in 14
+  // 143). As many workgroups as the GPU holds, each with its w and b over
+  // several rows.
+  const unsigned lanes = g.cols <= 2048   ? lanes_for(g.cols, 1, 64)
+                         : g.cols <= 4096 ? lanes_for(g.cols, 2, 64)
+                         : g.cols <= 6144 ? 256
+                                          : lanes_for(g.cols, 2, 256);
+  const unsigned grid = (unsigned)balanced(g.rows, 2048 * 256 / lanes);
+  if (g.cols <= 2048) norm_fwd_kernel<T, TY, 256, 1, 1, LAYER, STORE><<<grid, lanes, 0, stream>>>(g);
+  else if (g.cols <= 4096) norm_fwd_kernel<T, TY, 256, 1, 2, LAYER, STORE><<<grid, lanes, 0, stream>>>(g);
+  else if (g.cols <= 6144) norm_fwd_kernel<T, TY, 256, 1, 3, LAYER, STORE><<<grid, lanes, 0, stream>>>(g);
+  else norm_fwd_kernel<T, TY, 1024, 1, 2, LAYER, STORE><<<grid, lanes, 0, stream>>>(g);
 }
 
 template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer, int store, hipStream_t stream) {
@@ -574,7 +623,7 @@ int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 6144 ? 2 : 1); 
 // CUs better.
 int bwd_parts(int64_t rows, int64_t cols) {
   if (cols > kHeldCols) return (int)std::min<int64_t>(rows, std::max<int64_t>(1, kMaxParts * (int64_t)kHeldCols / cols));
-  return (int)std::min<int64_t>(cdiv(rows, groups_of(cols)), cols <= 1024 ? 2 * kMaxParts : kMaxParts);
+  return (int)balanced(cdiv(rows, groups_of(cols)), cols <= 1024 ? 2 * kMaxParts : kMaxParts);
 }
 
 template <typename TD, int SRC, typename T, typename TO, bool LAYER>
@@ -586,19 +635,17 @@ void bwd_launch(const BwdArgs &g, int parts, hipStream_t stream) {
       norm_bwd_wide_cols_kernel<TD, SRC, T, LAYER>
           <<<dim3((unsigned)cdiv(g.cols, 256 * kChunk), (unsigned)parts), 256, 0, stream>>>(g);
   } else if (g.cols <= 512) {
-    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 1, 1, LAYER><<<parts, 256, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 1, 1, LAYER><<<parts, 256, 0, stream>>>(g);
   } else if (g.cols <= 1024) {
-    norm_bwd_kernel<TD, SRC, T, TO, 64, 4, 2, 1, LAYER><<<parts, 256, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 2, 1, LAYER><<<parts, 256, 0, stream>>>(g);
   } else if (g.cols <= 2048) {
-    norm_bwd_kernel<TD, SRC, T, TO, 256, 4, 1, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
-  } else if (g.cols <= 4096) {
-    norm_bwd_kernel<TD, SRC, T, TO, 256, 2, 2, 2, LAYER><<<parts, 512, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 4, 1, 1, LAYER><<<parts, 4 * lanes_for(g.cols, 1, 64), 0, stream>>>(g);
   } else if (g.cols <= 6144) {
-    norm_bwd_kernel<TD, SRC, T, TO, 384, 2, 2, 2, LAYER><<<parts, 768, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 768, 2, 2, 2, LAYER><<<parts, 2 * lanes_for(g.cols, 2, 64), 0, stream>>>(g);
   } else if (g.cols <= 8192) {
-    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 1, 2, LAYER><<<parts, 1024, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 1, 2, LAYER><<<parts, lanes_for(g.cols, 1, 64), 0, stream>>>(g);
   } else {
-    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 2, 1, LAYER><<<parts, 1024, 0, stream>>>(g);
+    norm_bwd_kernel<TD, SRC, T, TO, 1024, 1, 2, 1, LAYER><<<parts, lanes_for(g.cols, 2, 256), 0, stream>>>(g);
   }
 }
 

@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_fwd_kernel(FwdArgs g) {
   const uint32_t r = g.nb.div(blk);
   const int c = (int)((blk - r * g.nb.d) * kBlock8 + (u & 3u) * kChunk), n = g.cols - c;
   Raw<T> ra, rb;
-  load_raw((const T *)g.a + r * g.lda, g.cols, c, ra);
-  load_raw((const T *)g.b + r * g.ldb, g.cols, c, rb);
+  load_raw<true>((const T *)g.a + r * g.lda, g.cols, c, ra);
+  load_raw<true>((const T *)g.b + r * g.ldb, g.cols, c, rb);
   settle(ra, n);
   settle(rb, n);
   float a[8], b[8], h[8];
@@ -108,14 +108,16 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(BwdArgs g) {
   const int c = (int)((blk - r * g.nb.d) * kBlock8 + (u & 3u) * kChunk), n = g.cols - c;
   Raw<TD> rd;
   Chunk<SRC, T> xa, xb;
-  load_raw((const TD *)g.dh + r * g.lddh, g.cols, c, rd);
-  xa.load(g.a, g.sa, r, g.lda, (int)g.nb.d, g.cols, c);
-  xb.load(g.b, g.sb, r, g.ldb, (int)g.nb.d, g.cols, c);
+  load_raw<true>((const TD *)g.dh + r * g.lddh, g.cols, c, rd);
+  xa.template load<true>(g.a, g.sa, r, g.lda, (int)g.nb.d, g.cols, c);
+  xb.template load<true>(g.b, g.sb, r, g.ldb, (int)g.nb.d, g.cols, c);
   float d[8], a[8], b[8], da[8], db[8], h[8];
   settle(rd, n);
+  settle(xa.raw, n);
+  settle(xb.raw, n);
   to_f32(rd, d);
-  xa.get(n, a);
-  xb.get(n, b);
+  xa.value(a);
+  xb.value(b);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float s, q;

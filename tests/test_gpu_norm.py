@@ -13,9 +13,10 @@ product); then y = xh w + b:
 Backward, at the GPU's own mean and rstd: xh carries 2 u, g u; the row sums
 e1 = (K + 3) u mean|g| and e2 = (K + 6) u mean|g xh|; then
   rstd (3 u |g| + e1 + 2 u |s1| + |xh| e2 + 5 u |xh s2|) + 3 u |dx| + hs |dx|.
-dw, db: a column's sum over rows, at most K2 = rows / parts + parts / 4 + 16
-additions on the longest path (parts <= 512 workgroups, each with up to four
-rows at once), so with K2 = min(rows, rows / 128 + 144) + 16:
+dw, db: a column's sum over rows, a group's rows in turn, up to four groups,
+then the workgroups' partial sums (at least 128 of them where rows allow, at
+most 512, sixteen at a time): the longest path has at most rows / 128 + 144
+additions, and no more than rows, so with K2 = min(rows, rows / 128 + 144) + 16:
 (K2 + 4) u sum|dy xh| and (K2 + 1) u sum|dy|."""
 import numpy as np
 import pytest
