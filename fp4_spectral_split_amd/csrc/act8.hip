@@ -1,7 +1,9 @@
 // 8-bit storage of activations: act8_block_quant / act8_block_dequant.
 //
 // Streaming passes, HBM bound: a lane takes one chunk of eight elements, four
-// lanes one block.
+// lanes one block. 8192 x 14336 bf16 to MXFP8 61 us, back 60 us (5.8 TB/s both;
+// plain kernels that move the same streams 59 and 54); two or four chunks per
+// lane change nothing (60.5, 62.5) and cost up to a quarter in fp32.
 #include <algorithm>
 
 #include "act8.hpp"

@@ -13,10 +13,10 @@
 // results are bitwise reproducible.
 //
 // Measured for 8192 x 4096 (a plain kernel that moves the same streams in
-// brackets): forward bf16 to bf16 26.5 us (23.4), with x stored in MXFP8 as
-// well 33 us (30.7); gradient from bf16 dy and MXFP8 x to bf16 dx 38 us
-// (30.6, and 1.5 for the partial sums), from fp32 dy 41 us; the partial sums
-// joined 4 us.
+// brackets): forward bf16 to bf16 27 us (23.4), with x stored in MXFP8 as well
+// 32.5 us, 5.2 TB/s (30.7); gradient from bf16 dy and MXFP8 x to bf16 dx 30.6
+// us, 5.5 TB/s (30.6), from fp32 dy and MXINT8 x 37 us, 6.4 TB/s; the partial
+// sums joined 4 us.
 #include <algorithm>
 #include <type_traits>
 

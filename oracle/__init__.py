@@ -12,6 +12,8 @@ split    Randomized spectral split A = U_k S_k V_k^T + R (Householder QR,
          one-sided Jacobi SVD), and the quantized split record.
 linear   Y = X W^T, dX = dY W, dW = dY^T X on the dequantized split operands
          (reconstruction route, plus the four-term expansion as a second route).
+act8     8-bit block storage of activations (MXFP8 with E4M3, MXINT8).
+ffn      Layer / RMS norm and the SwiGLU gate with their gradients.
 optim    The adaptive spectral learning rate (rescaling a gradient's mid and
          low singular directions) and the dual-range regularizer.
 
