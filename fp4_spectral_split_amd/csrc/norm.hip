@@ -105,10 +105,12 @@ __device__ __forceinline__ void row_sum(float (&a)[N], RowSums<MAXT, GROUPS, N> 
 }
 
 // s / n with inv_n = fp32(1 / n): one Newton step on the quotient, so that
-// a row of one value has exactly that value as its mean.
+// a row of one value has exactly that value as its mean. An infinite sum stays
+// infinite (the step would take infinity from infinity).
 __device__ __forceinline__ float divide(float s, float n, float inv_n) {
   const float q = s * inv_n;
-  return fmaf(fmaf(-q, n, s), inv_n, q);
+  const float r = fmaf(fmaf(-q, n, s), inv_n, q);
+  return fabsf(q) < INFINITY ? r : q;
 }
 
 // v^(-1/2): the hardware's estimate (1 ulp) and one Newton step.

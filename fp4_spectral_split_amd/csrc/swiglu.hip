@@ -27,7 +27,8 @@ constexpr int kThreads = 256;
 // held at 2^125 so that 1 + e and its reciprocal stay normal numbers (below
 // a = -86.6 s is 2^-125 instead of less, 1e-36 in the products with a), and at
 // 2^-126, where 1 + e is 1 anyway. An infinite or NaN a makes the products
-// with a infinite or NaN, as it should.
+// with a infinite or NaN, as it should. (Correction and Newton step cost
+// nothing measurable: the arithmetic hides behind the loads.)
 __device__ __forceinline__ void sigmoid(float a, float &s, float &one_minus_s) {
   const float c = -1.44269502f, c_lo = -1.92596299e-8f;  // log2(e) as two fp32
   const float t = __builtin_amdgcn_fmed3f(a * c, -126.0f, 125.0f);

@@ -167,3 +167,34 @@ def test_int8_code_from_the_low_bits_of_a_sum():
     t = (q * 64.0 + 12582912.0).astype(np.float32)  # exact in fp64: 24 bits and an integer below 2^24, one rounding
     code = t.view(np.uint32) & 255
     assert np.array_equal(code, np.round(q * 64.0).astype(np.int64) & 255)
+
+
+def test_a_launch_has_its_tensors_device_as_the_current_one(monkeypatch):
+    """Tensors of another device than the current one: the call runs inside that
+    device's context, on that device's current stream."""
+    seen, inside = [], []
+
+    class Context:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            inside.append(self.device.index)
+
+        def __exit__(self, *exc):
+            inside.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: inside[-1] if inside else 0)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+
+    def call(*args):
+        seen.append((torch.cuda.current_device(),) + args)
+        return 0
+
+    M._run(torch.device("cuda:0"), call, 7)
+    M._run(torch.device("cuda:1"), call, 8)
+    assert seen == [(0, 7, 100), (1, 8, 101)] and not inside
+    with pytest.raises(M.MetisError):
+        M._run(torch.device("cuda:1"), lambda *a: INVALID, 9)
+    assert not inside

@@ -143,6 +143,42 @@ def test_two_captured_steps_replayed_together():
             assert all(torch.equal(p, q) for p, q in zip(got, ref))
 
 
+def test_two_threads_at_once():
+    """Two host threads, each on its own stream and its own sizes, many calls:
+    every result as alone."""
+    import threading
+
+    g = H.rng(45)
+    jobs = []
+    for rows, cols in ((200, 1365), (90, 5000)):
+        x = H.to_dev(TN._stream(g, (rows, cols)), torch.bfloat16)
+        dy = H.to_dev(g.standard_normal((rows, cols)), torch.float32)
+
+        def work(x=x, dy=dy):
+            y, mean, rstd, q = M.metis_norm_fwd(x, save="mxint8")
+            h, a, b = M.metis_swiglu_fwd(x, y, save="mxfp8")
+            return [y, *M.metis_norm_bwd(dy, q, None, mean, rstd), h, *M.metis_swiglu_bwd(dy, a, b, need_h=True)]
+
+        jobs.append((work, work()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(work, want):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = work()
+                if not all(torch.equal(p, q) for p, q in zip(got, want)):
+                    failed.append(1)
+
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+
+
 def test_calls_on_another_stream_than_the_default():
     g = H.rng(44)
     x, dy = H.to_dev(g.standard_normal((300, 700)), torch.bfloat16), H.to_dev(g.standard_normal((300, 700)), torch.bfloat16)

@@ -236,6 +236,22 @@ def test_constant_and_zero_rows():
         assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("cols", [8, 96, 5000, 17000])
+def test_rows_whose_squares_overflow(cols):
+    """1e25 squared is beyond fp32: rstd is 0, so is the row, and so is its
+    gradient; the rows beside it are as ever."""
+    x = torch.ones(3, cols, device="cuda")
+    x[:, ::2] = -1.0
+    want = {k: M.metis_norm_fwd(x[:1].clone(), kind=k) for k in ("layer", "rms")}
+    x[1] *= 1e25
+    for kind in ("layer", "rms"):
+        y, mean, rstd, _ = M.metis_norm_fwd(x, kind=kind)
+        assert rstd[1].item() == 0.0 and torch.equal(y[1], torch.zeros_like(y[1]))
+        assert torch.equal(y[0], want[kind][0][0]) and torch.equal(y[2], y[0])
+        dx, dw, _ = M.metis_norm_bwd(torch.ones_like(x), x, None, mean, rstd, kind=kind)
+        assert torch.equal(dx[1], torch.zeros_like(dx[1])) and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
 @pytest.mark.parametrize("shape", [(4, 64), (4, 4096), (4, 16400)])
 def test_non_finite_rows_stay_in_place(shape):
     x = H.rng(37).standard_normal(shape)
