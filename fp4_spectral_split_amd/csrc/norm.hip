@@ -27,9 +27,9 @@ using namespace metis_host;
 
 namespace {
 
-constexpr int kWide = 1024;         // threads on a row that does not fit registers
-constexpr int kHeldCols = 16384;    // widest row held in registers
-constexpr int kMaxParts = 256;  // partial sums of dw and db
+constexpr int kWide = 1024;       // threads on a row that does not fit registers
+constexpr int kHeldCols = 16384;  // widest row held in registers
+constexpr int kMaxParts = 256;    // partial sums of dw and db
 constexpr int kFinishThreads = 1024;
 
 // ------------------------------------------------------------ reductions
@@ -113,11 +113,15 @@ __device__ __forceinline__ float divide(float s, float n, float inv_n) {
   return fabsf(q) < INFINITY ? r : q;
 }
 
-// v^(-1/2): the hardware's estimate (1 ulp) and one Newton step.
+// v^(-1/2): the hardware's estimate (1 ulp, for normal numbers: small ones are
+// scaled by 2^96) and one Newton step.
 __device__ __forceinline__ float inverse_root(float v) {
+  const bool low = v < 0x1p-96f;
+  v = low ? v * 0x1p96f : v;
   const float y = __builtin_amdgcn_rsqf(v);
   const float r = fmaf(0.5f * y, fmaf(-v * y, y, 1.0f), y);
-  return y > 0.0f && y < INFINITY ? r : y;  // v = 0 and infinity: no 0 * infinity
+  const float root = y > 0.0f && y < INFINITY ? r : y;  // v = 0 and infinity: no 0 * infinity
+  return low ? root * 0x1p48f : root;
 }
 
 // Chunk c of w or b, which may be absent (`fill`) and of either type.

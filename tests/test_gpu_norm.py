@@ -237,6 +237,18 @@ def test_constant_and_zero_rows():
 
 
 @pytest.mark.parametrize("cols", [8, 96, 5000, 17000])
+def test_rows_whose_squares_are_subnormal(cols):
+    """eps = 0 and elements of +-2^-66: their squares, 2^-132, and the mean of
+    those are subnormal numbers held exactly, and rstd is 2^66 (to 2 u)."""
+    x = torch.full((2, cols), 2.0 ** -66, device="cuda")
+    x[:, ::2] *= -1
+    for kind in ("layer", "rms"):
+        y, _, rstd, _ = M.metis_norm_fwd(x, kind=kind, eps=0.0)
+        assert torch.all((rstd.double() * 2.0 ** -66 - 1).abs() <= 3 * U)
+        assert torch.all((y.double() - x.double() * 2.0 ** 66).abs() <= 4 * U)
+
+
+@pytest.mark.parametrize("cols", [8, 96, 5000, 17000])
 def test_rows_whose_squares_overflow(cols):
     """1e25 squared is beyond fp32: rstd is 0, so is the row, and so is its
     gradient; the rows beside it are as ever."""
