@@ -385,8 +385,9 @@ metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int
  *          NULL without dw and db. Sums over rows run in a fixed order (no
  *          atomics): bitwise reproducible. rstd^2 times the gradient's size
  *          has to stay in fp32's range: only eps = 0 with a deviation below
- *          1e-19 can leave it. A NaN or an infinity in a row spoils that row
- *          of dx and the sums of its own column, nothing else. */
+ *          1e-19 can leave it. A NaN or an infinity in dy spoils its row of
+ *          dx and its column of dw and db; one in x, through the row's
+ *          statistics, its row of dx and all of dw. */
 size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, const void *x, metis_dtype_t xdt,
                               int64_t ldx, const metis_act8_t *stored, const void *w, metis_dtype_t wdt,
