@@ -24,10 +24,11 @@ constexpr int kThreads = 256;
 // s = 1 / (1 + e) and 1 - s = e s for e = exp(-a), each free of cancellation.
 // exp(-a) = 2^t, t = -a log2(e); the rounding of t and the rest of log2(e) are
 // carried as t's correction, or the error would grow with |a|. The exponent is
-// held at 2^125 so that 1 + e and its reciprocal stay normal numbers (below
-// a = -86.6 s is 2^-125 instead of less, 1e-36 in the products with a), and at
-// 2^-126, where 1 + e is 1 anyway. An infinite or NaN a makes the products
-// with a infinite or NaN, as it should. (Correction and Newton step cost
+// held within [-126, 125] so that 1 + e and its reciprocal stay normal numbers.
+// A factor left at such an end would be multiplied by a, however large a is, so
+// where t is held s (below a = -86.6) and 1 - s (above a = 87.3) are 0: every
+// a s and a s (1 - s) they stand for is below 2^-118. A NaN makes the products
+// with a NaN, an infinite a infinite or NaN. (Correction and Newton step cost
 // nothing measurable: the arithmetic hides behind the loads.)
 __device__ __forceinline__ void sigmoid(float a, float &s, float &one_minus_s) {
   const float c = -1.44269502f, c_lo = -1.92596299e-8f;  // log2(e) as two fp32
@@ -38,8 +39,8 @@ __device__ __forceinline__ void sigmoid(float a, float &s, float &one_minus_s) {
   const float d = 1.0f + e;
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(r, fmaf(-d, r, 1.0f), r);
-  s = r;
-  one_minus_s = e * r;
+  s = t < 125.0f ? r : 0.0f;
+  one_minus_s = t > -126.0f ? e * r : 0.0f;
 }
 
 struct FwdArgs {

@@ -403,9 +403,9 @@ metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int64_t lddy, 
  *  h:      rows x cols of type hdt, rounded once from fp32.
  *  qa, qb: optional, both or neither and of one format: a and b in 8 bits as
  *          act8_block_quant writes them, from the same read.
- * A NaN or an infinity reaches the outputs of its own element only. Below
- * a = -86.6 the sigmoid is held at 2^-125, so that |h| is up to 2^-118 |b|
- * where it should be smaller still. */
+ * A NaN or an infinity reaches the outputs of its own element only (a = -inf
+ * gives NaN, as a / (1 + exp(-a)) does). Below a = -86.6 the sigmoid is taken
+ * as 0, so that h is 0 where it should be up to 2^-118 |b|. */
 metis_status_t metis_swiglu_fwd(const void *a, int64_t lda, const void *b, int64_t ldb, metis_dtype_t dt, int64_t rows,
                                 int64_t cols, void *h, metis_dtype_t hdt, int64_t ldh, metis_act8_t *qa,
                                 metis_act8_t *qb, hipStream_t stream);
@@ -415,6 +415,9 @@ metis_status_t metis_swiglu_fwd(const void *a, int64_t lda, const void *b, int64
  *  dh:     rows x cols of type dhdt.
  *  a, b:   dense, type dt; or both NULL with qa and qb their 8-bit forms.
  *  da, db: rows x cols of type odt, rounded once from fp32.
+ *          Below a = -86.6 both are 0 (off by up to 2^-118 |dh b| and 2^-118
+ *          |dh|); above a = 87.3 the slope in da is 1. dh b has to stay in
+ *          fp32's range. An infinite a gives infinity or NaN.
  *  h:      optional, type odt: silu(a) b again, from the a and b given (the
  *          weight gradient of the down projection reads it). */
 metis_status_t metis_swiglu_bwd(const void *dh, metis_dtype_t dhdt, int64_t lddh, const void *a, int64_t lda,

@@ -178,3 +178,37 @@ def test_empty_and_refused():
     for call in bad:
         with pytest.raises(M.MetisError):
             call()
+
+
+# past both ends of the exponential: each magnitude in a row of its own, both signs
+FAR = [80.0, 86.0, 86.5, 86.75, 87.0, 87.25, 87.5, 88.0, 90.0, 104.0, 128.0, 200.0, 1e4, 65504.0, 1e30, 1e36, 1e38, 3e38]
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("source", ["f32", "bf16", "mxfp8", "mxint8"])
+@pytest.mark.parametrize("cols", [64, 77])
+def test_inputs_past_the_ends_of_the_exponential(cols, source, odt):
+    """Finite a of any size: what is left out below a = -86.6 is the true
+    |a s| <= 87 * 2^-125 < 2^-118 times |b|, |dh| or |dh b|, whatever |a| is.
+    |b| and |dh| are at most 1, so no product overflows."""
+    g = H.rng(26)
+    shape = (len(FAR), cols)
+    a = np.array(FAR)[:, None] * np.where(np.arange(cols) % 2 == 0, -1.0, 1.0)
+    b, dh = (g.uniform(0.25, 1.0, shape) * g.choice([-1.0, 1.0], shape) for _ in range(2))
+    dtype = H.T.get(source, torch.float32)
+    ad, bd, dd = H.to_dev(a, dtype, 1), H.to_dev(b, dtype), H.to_dev(dh, torch.float32)
+    hs, a64, b64, d64 = H.HALF[H.T[odt]], H.np64(ad), H.np64(bd), H.np64(dd)
+    print("case swiglu far", shape, source, odt, flush=True)
+    h, qa, qb = M.metis_swiglu_fwd(ad, bd, dtype=H.T[odt], save=source if source in ("mxfp8", "mxint8") else None)
+    want = O.swiglu_fwd(a64, b64)
+    _close(H.np64(h), want, (10 * U + hs) * (1 + U) * np.abs(want) + 2.0 ** -118 * np.abs(b64) + 2.0 ** -126, "h")
+    if qa is not None:
+        a64, b64 = A.restored(a64, source), A.restored(b64, source)
+    da, db, again = M.metis_swiglu_bwd(dd, ad if qa is None else qa, bd if qb is None else qb, dtype=H.T[odt],
+                                       need_h=True)
+    wa, wb, wh = O.swiglu_bwd(d64, a64, b64)
+    s, q = O.sigmoid(a64), O.sigmoid(-a64)
+    _close(H.np64(da), wa, (1 + hs) * np.abs(d64 * b64) * (11 * U * s + 26 * U * np.abs(a64 * s * q) + 2.0 ** -118) +
+           (2 * U + hs) * np.abs(wa) + 2.0 ** -126, "da")
+    _close(H.np64(db), wb, (10 * U + hs) * (1 + U) * np.abs(wb) + 2.0 ** -118 * np.abs(d64) + 2.0 ** -126, "db")
+    _close(H.np64(again), wh, (10 * U + hs) * (1 + U) * np.abs(wh) + 2.0 ** -118 * np.abs(b64) + 2.0 ** -126, "h again")
