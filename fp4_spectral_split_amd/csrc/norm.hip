@@ -329,10 +329,25 @@ template <typename TD, int SRC, typename T, int V> struct BwdRow {
   float mean, rstd;
 };
 
+// Deviations from the mean of a chunk of which n elements exist; zero past the
+// row's end, where -mean times rstd could be infinite and spoil the row's sums.
+__device__ __forceinline__ void center(float (&x)[8], float mean, int n) {
+  if (n >= kChunk) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] -= mean;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] - mean : 0.0f;
+  }
+}
+
 // GROUPS rows are worked on at once, and every thread keeps the sums of dw and
-// db of its columns in registers over all rows of its group. With dr = dy rstd and xc = x - mean held from the reductions
-// (S1 = sum(dy w), S2 = sum(dy w xc)) the result is
-//   dx = dr w - rstd S1 / n - xc rstd^3 S2 / n.
+// db of its columns in registers over all rows of its group. With dr = dy rstd
+// and xh held from the reductions (S1 = sum(dy w), S2 = sum(dy w xh)) the
+// result is dx = dr w - rstd S1 / n - xh rstd S2 / n.
+// xh is formed before anything else: it is of the order of 1 whatever the size
+// of x, so that only rstd times the gradient has to stay in fp32's range (with
+// x - mean held instead, rstd^3 S2 fell below it for deviations from 1e16 on).
 // DEPTH sets of rows are in registers: one worked on, the others on their way
 // (8192 x 4096, bf16 dy and MXFP8 x: one set 42.0 us with the join of the sums,
 // two 39.7, three 40.7).
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(BwdArgs g) {
   auto work = [&](int64_t r, Row &row) {
     const float rstd = row.rstd, mean = row.mean;
     const int cols = r < g.rows ? g.cols : 0;
-    float dr[V][8], xc[V][8], s[2] = {0.0f, 0.0f};
+    float dr[V][8], xh[V][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int n = cols - (v * lanes + t) * kChunk;
@@ -383,27 +398,28 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(BwdArgs g) {
       settle(row.d[v], n);
       settle(row.x[v].raw, n);
       to_f32(row.d[v], d);
-      row.x[v].value(xc[v]);
+      row.x[v].value(xh[v]);
+      if (LAYER) center(xh[v], mean, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // past the row's end dy is zero: no term of any sum
-        if (LAYER) xc[v][i] -= mean;
+        xh[v][i] *= rstd;
         dr[v][i] = d[i] * rstd;
         const float gi = d[i] * w[v][i];
         if (LAYER) s[0] += gi;
-        s[1] = fmaf(gi, xc[v][i], s[1]);
-        aw[v][i] = fmaf(dr[v][i], xc[v][i], aw[v][i]);
+        s[1] = fmaf(gi, xh[v][i], s[1]);
+        aw[v][i] = fmaf(d[i], xh[v][i], aw[v][i]);
         ab[v][i] += d[i];
       }
     }
     row_sum(s, red, slot, at);
-    const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
+    const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * (s[1] * g.inv_n);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * lanes + t) * kChunk, n = cols - c;
       float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(dr[v][i], w[v][i], fmaf(-k2, xc[v][i], -k1));
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(dr[v][i], w[v][i], fmaf(-k2, xh[v][i], -k1));
       store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
     }
   };
@@ -476,15 +492,16 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
       to_f32(rd, d);
       settle(rx.raw, n);
       rx.value(x);
+      if (LAYER) center(x, mean, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gi = d[i] * w[i];
         s[0] += gi;
-        s[1] = fmaf(gi, x[i] - mean, s[1]);
+        s[1] = fmaf(gi, x[i] * rstd, s[1]);
       }
     }
     row_sum(s, red, slot, at);
-    const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * rstd * (rstd * (s[1] * g.inv_n));
+    const float k1 = LAYER ? rstd * (s[0] * g.inv_n) : 0.0f, k2 = rstd * (s[1] * g.inv_n);
     for (int c = t * kChunk; c < g.cols; c += step) {
       const int n = g.cols - c;
       float o[8];
@@ -495,8 +512,9 @@ __global__ void __launch_bounds__(kWide) norm_bwd_wide_kernel(BwdArgs g) {
       to_f32(rd, d);
       settle(rx.raw, n);
       rx.value(x);
+      if (LAYER) center(x, mean, n);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i] * rstd, w[i], fmaf(-k2, x[i] - mean, -k1));
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i] * rstd, w[i], fmaf(-k2, x[i] * rstd, -k1));
       store_chunk((TO *)g.dx + r * g.lddx + c, o, n);
     }
   }
@@ -521,9 +539,10 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(BwdArgs g) {
     to_f32(rd, d);
     settle(rx.raw, n);
     rx.value(x);
+    if (LAYER) center(x, mean, n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      aw[i] = fmaf(d[i] * rstd, x[i] - mean, aw[i]);
+      aw[i] = fmaf(d[i], x[i] * rstd, aw[i]);
       ab[i] += d[i];
     }
   }

@@ -383,9 +383,8 @@ metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int
  *          (stored) or kept (added).
  *  ws:     metis_norm_bwd_workspace_bytes() bytes, 256-byte aligned; may be
  *          NULL without dw and db. Sums over rows run in a fixed order (no
- *          atomics): bitwise reproducible. rstd^2 times the gradient's size
- *          has to stay in fp32's range: only eps = 0 with a deviation below
- *          1e-19 can leave it. A NaN or an infinity in dy spoils its row of
+ *          atomics): bitwise reproducible. xh, dy w, rstd dy and
+ *          their products have to stay in fp32's range. A NaN or an infinity in dy spoils its row of
  *          dx and its column of dw and db; one in x, through the row's
  *          statistics, its row of dx and all of dw. */
 size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);

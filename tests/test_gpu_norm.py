@@ -306,3 +306,41 @@ def test_rows_zero_and_refused():
     for call in bad:
         with pytest.raises(M.MetisError):
             call()
+
+
+# a width of every layout of the gradient's kernels
+WIDTHS = [77, 700, 1365, 5000, 7000, 9000, 17000]
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("source", ["dense", "mxint8"])
+@pytest.mark.parametrize("scale", [2.0 ** 55, 2.0 ** 50, 2.0 ** -60, 2.0 ** -64])
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_gradient_at_the_ends_of_the_range(cols, scale, source, kind):
+    """Deviations from 5e-20 (eps = 0) to 4e16 under gradients of 1e-8: every
+    term of dx is of the size of rstd dy, from 2^-82 to 2^38, a normal number."""
+    g = H.rng(38)
+    x = H.to_dev(scale * (g.standard_normal((9, cols)) + 0.25), torch.float32)
+    dy = H.to_dev(1e-8 * (1.0 + g.standard_normal((9, cols))), torch.float32)
+    w = torch.from_numpy(1 + 0.1 * g.standard_normal(cols)).float().cuda()
+    print("case norm range", cols, scale, source, kind, flush=True)
+    _, mean, rstd, q = M.metis_norm_fwd(x, w, kind=kind, eps=0.0, save=None if source == "dense" else source)
+    x64 = H.np64(x) if q is None else A.restored(H.np64(x), source)
+    m64 = None if mean is None else H.np64(mean)
+    for dxdt in (torch.float32, torch.bfloat16):
+        out = M.metis_norm_bwd(dy, x if q is None else q, w, mean, rstd, kind=kind, dtype=dxdt, need_dbias=True)
+        _check_bwd(out, H.np64(dy), x64, H.np64(w), m64, H.np64(rstd), kind, dxdt)
+
+
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_gradient_of_constant_rows_of_large_values(cols):
+    """x = 2^113 throughout (its sum is exact): the deviation is zero and rstd
+    1e6; 2^113 times rstd, which lanes past the row's end could form, is not
+    finite."""
+    g = H.rng(39)
+    x = torch.full((6, cols), 2.0 ** 113, device="cuda")
+    dy = H.to_dev(g.standard_normal((6, cols)), torch.float32)
+    _, mean, rstd, _ = M.metis_norm_fwd(x, eps=1e-12)
+    out = M.metis_norm_bwd(dy, x, None, mean, rstd)
+    assert torch.all(mean == 2.0 ** 113)
+    _check_bwd(out, H.np64(dy), H.np64(x), None, H.np64(mean), H.np64(rstd), "layer", torch.float32)
