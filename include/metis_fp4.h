@@ -363,7 +363,13 @@ metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, metis_dtype_t
  *  stored: optional: x in 8 bits as act8_block_quant writes it (fmt, codes and
  *          scales set by the caller), from the same read of x.
  *  eps >= 0 (else METIS_ERR_INVALID). Sums in fp32; the deviation is summed
- * around the mean, in a second pass over the row on chip. */
+ * around the mean, in a second pass over the row on chip. A finite row has a
+ * finite mean. Where the sum of squares passes fp32's largest number (n
+ * elements 1.8e19 / sqrt(n) from the mean; from 0 for RMS) rstd is 0: y is b
+ * and the row adds nothing to any gradient (an element farther from the mean
+ * than that number gives NaN). At the other end, squares below 1e-38 lose bits,
+ * which shows where eps is no larger; with eps = 0 a row whose squares are all
+ * 0 has rstd = infinity and y = NaN. */
 typedef enum { METIS_NORM_LAYER = 0, METIS_NORM_RMS = 1 } metis_norm_t;
 metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx, const void *w,
                               const void *b, metis_dtype_t wdt, metis_norm_t kind, float eps, void *y,

@@ -344,3 +344,34 @@ def test_gradient_of_constant_rows_of_large_values(cols):
     out = M.metis_norm_bwd(dy, x, None, mean, rstd)
     assert torch.all(mean == 2.0 ** 113)
     _check_bwd(out, H.np64(dy), H.np64(x), None, H.np64(mean), H.np64(rstd), "layer", torch.float32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [300, 700, 1365, 3000, 5000, 9000, 17000])
+def test_rows_whose_sum_overflows(cols, dtype):
+    """Elements of 2^120 and more sum to beyond fp32, their mean does not: exact
+    for a constant row (deviation 0, y = b), within the sum's roundings
+    otherwise, where the squares overflow (rstd = 0, y = b, no gradient). The
+    rows beside them are as ever."""
+    g = H.rng(40)
+    x = g.standard_normal((6, cols))
+    x[1] = 2.0 ** 120
+    x[2] = -3.3e38
+    x[3] = 1e36 * (1.0 + 0.1 * g.uniform(-1, 1, cols))
+    X, dy = H.to_dev(x, H.T[dtype]), H.to_dev(g.standard_normal((6, cols)), torch.float32)
+    b = torch.from_numpy(g.standard_normal(cols)).float().cuda()
+    x64, keep = H.np64(X), [0, 4, 5]
+    print("case norm sum overflow", cols, dtype, flush=True)
+    y, mean, rstd, _ = M.metis_norm_fwd(X, None, b, eps=1e-5, dtype=torch.float32)
+    near = M.metis_norm_fwd(X[keep].contiguous(), None, b, eps=1e-5, dtype=torch.float32)
+    assert all(torch.equal(p[keep], q) for p, q in zip((y, mean, rstd), near[:3]))
+    m64 = H.np64(mean)
+    assert m64[1] == 2.0 ** 120 and torch.equal(y[1], b)
+    tol = (66 + cols / 1024) * U
+    assert np.all(np.abs(m64 / x64.mean(axis=1) - 1)[[2, 3]] <= tol)
+    assert rstd[3].item() == 0.0 and torch.equal(y[3], b)
+    dx, dw, _ = M.metis_norm_bwd(dy, X, None, mean, rstd, dtype=torch.float32)
+    assert torch.isfinite(y).all() and torch.isfinite(dx[keep + [1, 3]]).all()
+    assert torch.equal(dx[3], torch.zeros_like(dx[3]))
+    # row 2's deviation is its mean's rounding: 0, or at least a step of 3.3e38, whose square overflows
+    assert torch.equal(y[2], b)
