@@ -575,16 +575,16 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_cols_kernel(BwdArgs g) {
   if (g.pb) store_chunk(g.pb + (int64_t)blockIdx.y * g.cols + c, ab, n);
 }
 
-// dw and db from the partial sums: 64 columns per workgroup, each wave every
-// 16th partial, sixteen loads in flight, then the waves in order. With parts = 0
-// (no rows) the sums are zero.
+// dw and db from the partial sums: 64 columns (from column c0 on) per workgroup,
+// each wave every 16th partial, sixteen loads in flight, then the waves in
+// order. With parts = 0 (no rows) the sums are zero.
 __global__ void __launch_bounds__(kFinishThreads)
-    norm_finish_kernel(const float *__restrict__ pw, const float *__restrict__ pb, int parts, int cols,
+    norm_finish_kernel(const float *__restrict__ pw, const float *__restrict__ pb, int parts, int cols, int c0,
                        float *__restrict__ dw, float *__restrict__ db, int accumulate) {
   constexpr int WAVES = kFinishThreads / 64, DEEP = 16;
   __shared__ float red[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  const int c = c0 + (int)blockIdx.x * 64 + lane;
   const float *src = blockIdx.y ? pb : pw;
   float *dst = blockIdx.y ? db : dw;
   if (!dst) return;  // the whole workgroup
@@ -674,6 +674,17 @@ int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 6144 ? 2 : 1); 
 int bwd_parts(int64_t rows, int64_t cols) {
   if (cols > kHeldCols) return (int)std::min<int64_t>(rows, std::max<int64_t>(1, kMaxParts * (int64_t)kHeldCols / cols));
   return (int)balanced(cdiv(rows, groups_of(cols)), cols <= 1024 ? 2 * kMaxParts : kMaxParts);
+}
+
+// A grid numbers fewer than 2^32 threads, sixteen of them per column here: wide
+// rows take several launches.
+void finish_launch(const float *pw, const float *pb, int parts, int cols, float *dw, float *db, int accumulate,
+                   hipStream_t stream) {
+  constexpr int kSlab = 1 << 26;
+  for (int c0 = 0; c0 < cols; c0 += kSlab) {
+    const dim3 grid((unsigned)cdiv(std::min(kSlab, cols - c0), 64), 2);
+    norm_finish_kernel<<<grid, kFinishThreads, 0, stream>>>(pw, pb, parts, cols, c0, dw, db, accumulate);
+  }
 }
 
 template <typename TD, int SRC, typename T, typename TO, bool LAYER>
@@ -798,10 +809,9 @@ extern "C" metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int
   if (rows > kMaxRows || cols > kMaxCols) return METIS_ERR_UNSUPPORTED;
   if (cols == 0) return METIS_OK;
   const bool layer = kind == METIS_NORM_LAYER, sums = dw || db;
-  const dim3 finish((unsigned)cdiv(cols, 64), 2);
   if (rows == 0) {  // dw and db are empty sums
     if (sums && !accumulate) {
-      norm_finish_kernel<<<finish, kFinishThreads, 0, stream>>>(nullptr, nullptr, 0, (int)cols, dw, db, 0);
+      finish_launch(nullptr, nullptr, 0, (int)cols, dw, db, 0, stream);
       METIS_LAUNCH_CHECK();
     }
     return METIS_OK;
@@ -835,7 +845,7 @@ extern "C" metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int
   const int src = stored ? stored->fmt : kDense;
   if (layer) bwd_by_type<true>(g, dydt, dxdt, src, xdt, parts, stream);
   else bwd_by_type<false>(g, dydt, dxdt, src, xdt, parts, stream);
-  if (sums) norm_finish_kernel<<<finish, kFinishThreads, 0, stream>>>(pw, pb, parts, (int)cols, dw, db, accumulate);
+  if (sums) finish_launch(pw, pb, parts, (int)cols, dw, db, accumulate, stream);
   METIS_LAUNCH_CHECK();
   return METIS_OK;
 }

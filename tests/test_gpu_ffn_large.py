@@ -110,3 +110,32 @@ def test_more_rows_than_one_launch_numbers():
         part = M.Act8Tensor.from_codes("mxfp8", c, s)
         grads = M.metis_swiglu_bwd(x[i:j], part, part)
         assert torch.equal(da[i:j], grads[0]) and torch.equal(db[i:j], grads[1])
+
+
+def test_gradient_of_rows_whose_columns_pass_one_launch():
+    """dw and db are joined with sixteen threads per column: rows of 2^28
+    columns and more have 2^32 of them. Two rows at given statistics, so a
+    column's sums have two terms: 4 half steps of fp32 each, one addition."""
+    cols = (1 << 28) + 40
+    spans = [(0, 64), ((1 << 26) - 32, (1 << 26) + 32), (1 << 27, (1 << 27) + 64), ((1 << 28) - 32, cols)]
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(6)
+    dy = torch.zeros(2, cols, device=DEV, dtype=torch.bfloat16)
+    x = torch.zeros(2, cols, device=DEV, dtype=torch.bfloat16)
+    for i, j in spans:
+        dy[:, i:j] = torch.randn(2, j - i, device=DEV, generator=gen).to(torch.bfloat16)
+        x[:, i:j] = torch.randn(2, j - i, device=DEV, generator=gen).to(torch.bfloat16)
+    mean, rstd = torch.tensor([0.25, -0.5], device=DEV), torch.tensor([0.75, 1.5], device=DEV)
+    buf = torch.full((2, cols + 1), 7.0, device=DEV)
+    print("case wide norm bwd", cols, flush=True)
+    _, dw, db = M.metis_norm_bwd(dy, x, None, mean, rstd, dweight=buf[0, :cols], dbias=buf[1, :cols])
+    assert dw.data_ptr() == buf.data_ptr() and torch.all(buf[:, cols] == 7.0)
+    for i, j in spans:
+        d = dy[:, i:j].double()
+        term = d * (x[:, i:j].double() - mean[:, None].double()) * rstd[:, None].double()
+        assert torch.all((dw[i:j].double() - term.sum(dim=0)).abs() <= 5 * H.U32 * term.abs().sum(dim=0))
+        assert torch.all((db[i:j].double() - d.sum(dim=0)).abs() <= 2 * H.U32 * d.abs().sum(dim=0))
+    assert torch.all(dw[64:1 << 20] == 0) and torch.all(db[64:1 << 20] == 0)
+    print("case wide norm bwd without rows", cols, flush=True)
+    M.metis_norm_bwd(dy[:0], x[:0], None, mean[:0], rstd[:0], dweight=dw, dbias=db)
+    assert not dw.any() and not db.any() and torch.all(buf[:, cols] == 7.0)
