@@ -620,7 +620,10 @@ def _sum_out(t, name, n, device):
 
 def act8_block_quant(x, fmt="mxfp8", out=None):
     """Store a 2-D fp32/bf16 CUDA tensor (any width, rows contiguous) in 8
-    bits: MXFP8 (E4M3) or MXINT8 codes with one scale per 32 elements."""
+    bits: MXFP8 (E4M3) or MXINT8 codes with one scale per 32 elements. Here and
+    in the calls below, outputs that are given (out, save, ...) must not share
+    memory with an input or with each other (MetisError): no call works in
+    place. The two halves of one matrix are apart."""
     ld = _matrix(x, "x")
     shape, dev, dt = x.shape, x.device, _code(x.dtype)
     if out is None:

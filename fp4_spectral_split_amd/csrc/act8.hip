@@ -87,6 +87,10 @@ extern "C" metis_status_t act8_block_quant(const void *x, metis_dtype_t dt, int6
   out->cols = cols;
   if (rows == 0 || cols == 0) return METIS_OK;
   if (!dense_ok(x, dt, cols, ldx) || !out->codes || !out->scales) return METIS_ERR_INVALID;
+  Operands o;
+  o.out(out);
+  o.in(x, rows, cols, ldx, elem_bytes(dt));
+  if (!o.distinct()) return METIS_ERR_INVALID;
   const bool fp8 = out->fmt == METIS_MXFP8;
   if (dt == METIS_F32) {
     if (fp8) launch_quant<float, kFp8>((const float *)x, rows, cols, ldx, out, stream);
@@ -105,6 +109,10 @@ extern "C" metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, me
   if (in->rows > kMaxRows || in->cols > kMaxCols) return METIS_ERR_UNSUPPORTED;
   if (in->rows == 0 || in->cols == 0) return METIS_OK;
   if (!dense_ok(y, dt, in->cols, ldy) || !in->codes || !in->scales) return METIS_ERR_INVALID;
+  Operands o;
+  o.out(y, in->rows, in->cols, ldy, elem_bytes(dt));
+  o.in(in);
+  if (!o.distinct()) return METIS_ERR_INVALID;
   const bool fp8 = in->fmt == METIS_MXFP8;
   if (dt == METIS_F32) {
     if (fp8) launch_dequant<float, kFp8>(in, (float *)y, ldy, stream);

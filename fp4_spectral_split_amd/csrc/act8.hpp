@@ -361,6 +361,64 @@ inline bool act8_fmt_ok(const metis_act8_t *q) {
   return q && (q->fmt == METIS_MXFP8 || q->fmt == METIS_MXINT8);
 }
 
+// The bytes of a matrix: `rows` ranges of `width` bytes, `pitch` apart. One
+// range where the rows follow each other without a gap; empty where p is NULL.
+struct Region {
+  uint64_t at, rows, width, pitch;
+  uint64_t end() const { return at + (rows - 1) * pitch + width; }
+};
+inline Region region(const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
+  const uint64_t w = (uint64_t)cols * (unsigned)bytes, step = (uint64_t)ld * (unsigned)bytes;
+  if (!p) return {0, 1, 0, 0};
+  if (rows == 1 || step == w) return {(uint64_t)(uintptr_t)p, 1, (uint64_t)rows * w, 0};
+  return {(uint64_t)(uintptr_t)p, (uint64_t)rows, w, step};
+}
+
+// Whether two regions share no byte. Two matrices of different pitch count as
+// sharing where their address ranges meet.
+inline bool apart(const Region &a, const Region &b) {
+  if (!a.width || !b.width || a.end() <= b.at || b.end() <= a.at) return true;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return false;
+  const Region &m = a.rows > 1 ? a : b, &o = a.rows > 1 ? b : a;
+  if (m.rows == 1) return false;
+  // place of o in m's rows: between m's columns, or over them somewhere
+  const uint64_t d = o.at >= m.at ? (o.at - m.at) % m.pitch : (m.pitch - (m.at - o.at) % m.pitch) % m.pitch;
+  return d >= m.width && d + o.width <= m.pitch;
+}
+
+// The operands of a call. No output may share memory with an input or with
+// another output: a lane reads up to seven elements of its neighbours, and
+// rows run in any order.
+struct Operands {
+  Region outs[8], ins[8];
+  int nout = 0, nin = 0;
+  void out(const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
+    outs[nout++] = region(p, rows, cols, ld, bytes);
+  }
+  void in(const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
+    ins[nin++] = region(p, rows, cols, ld, bytes);
+  }
+  void out(const metis_act8_t *q) {
+    if (!q) return;
+    out(q->codes, 1, q->rows * q->cols, 0, 1);
+    out(q->scales, 1, q->rows * metis::cdiv(q->cols, metis::kBlock8), 0, 1);
+  }
+  void in(const metis_act8_t *q) {
+    if (!q) return;
+    in(q->codes, 1, q->rows * q->cols, 0, 1);
+    in(q->scales, 1, q->rows * metis::cdiv(q->cols, metis::kBlock8), 0, 1);
+  }
+  bool distinct() const {
+    for (int i = 0; i < nout; ++i) {
+      for (int k = 0; k < nin; ++k)
+        if (!apart(outs[i], ins[k])) return false;
+      for (int k = 0; k < i; ++k)
+        if (!apart(outs[i], outs[k])) return false;
+    }
+    return true;
+  }
+};
+
 // A launch numbers at most 2^31 chunks; taller matrices take several.
 inline int64_t slab_rows(int64_t blocks_per_row) {
   const int64_t r = (((int64_t)1 << 29) - 1) / blocks_per_row;

@@ -750,6 +750,16 @@ extern "C" metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_
   if (!dense_ok(x, dt, cols, ldx) || !dense_ok(y, ydt, cols, ldy)) return METIS_ERR_INVALID;
   if (((uintptr_t)mean & 3) || ((uintptr_t)rstd & 3)) return METIS_ERR_INVALID;
   if (stored && (!stored->codes || !stored->scales)) return METIS_ERR_INVALID;
+  const bool layer = kind == METIS_NORM_LAYER;
+  Operands o;
+  o.out(y, rows, cols, ldy, elem_bytes(ydt));
+  o.out(layer ? mean : nullptr, 1, rows, 0, 4);
+  o.out(rstd, 1, rows, 0, 4);
+  o.out(stored);
+  o.in(x, rows, cols, ldx, elem_bytes(dt));
+  o.in(w, 1, cols, 0, elem_bytes(wdt));
+  o.in(b, 1, cols, 0, elem_bytes(wdt));
+  if (!o.distinct()) return METIS_ERR_INVALID;
   FwdArgs g = {};
   g.x = x;
   g.ldx = ldx;
@@ -768,7 +778,6 @@ extern "C" metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_
   g.n = (float)cols;
   g.inv_n = 1.0f / (float)cols;
   g.eps = eps;
-  const bool layer = kind == METIS_NORM_LAYER;
   const int store = stored ? stored->fmt : kDense;
   if (dt == METIS_F32) {
     if (ydt == METIS_F32) fwd_by_kind<float, float>(g, layer, store, stream);
@@ -821,6 +830,18 @@ extern "C" metis_status_t metis_norm_bwd(const void *dy, metis_dtype_t dydt, int
   if (!rstd || ((uintptr_t)rstd & 3) || (layer && (!mean || ((uintptr_t)mean & 3)))) return METIS_ERR_INVALID;
   if (sums && (!ws || ws_bytes < metis_norm_bwd_workspace_bytes(rows, cols))) return METIS_ERR_WORKSPACE;
   if (sums && ((uintptr_t)ws & 255)) return METIS_ERR_INVALID;
+  Operands o;
+  o.out(dx, rows, cols, lddx, elem_bytes(dxdt));
+  o.out(dw, 1, cols, 0, 4);
+  o.out(db, 1, cols, 0, 4);
+  if (sums) o.out(ws, 1, (int64_t)metis_norm_bwd_workspace_bytes(rows, cols), 0, 1);
+  o.in(dy, rows, cols, lddy, elem_bytes(dydt));
+  if (stored) o.in(stored);
+  else o.in(x, rows, cols, ldx, elem_bytes(xdt));
+  o.in(w, 1, cols, 0, elem_bytes(wdt));
+  o.in(layer ? mean : nullptr, 1, rows, 0, 4);
+  o.in(rstd, 1, rows, 0, 4);
+  if (!o.distinct()) return METIS_ERR_INVALID;
   const int parts = bwd_parts(rows, cols);
   Carver carve(ws);
   float *pw = carve.take<float>((size_t)parts * (size_t)cols), *pb = carve.take<float>((size_t)parts * (size_t)cols);

@@ -216,6 +216,13 @@ extern "C" metis_status_t metis_swiglu_fwd(const void *a, int64_t lda, const voi
   if (!dense_ok(a, dt, cols, lda) || !dense_ok(b, dt, cols, ldb) || !dense_ok(h, hdt, cols, ldh))
     return METIS_ERR_INVALID;
   if (qa && (!qa->codes || !qa->scales || !qb->codes || !qb->scales)) return METIS_ERR_INVALID;
+  Operands o;
+  o.out(h, rows, cols, ldh, elem_bytes(hdt));
+  o.out(qa);
+  o.out(qb);
+  o.in(a, rows, cols, lda, elem_bytes(dt));
+  o.in(b, rows, cols, ldb, elem_bytes(dt));
+  if (!o.distinct()) return METIS_ERR_INVALID;
   FwdArgs g = {};
   g.a = a;
   g.b = b;
@@ -262,6 +269,18 @@ extern "C" metis_status_t metis_swiglu_bwd(const void *dh, metis_dtype_t dhdt, i
       (h && !dense_ok(h, odt, cols, ldh)))
     return METIS_ERR_INVALID;
   if (!qa && (!dense_ok(a, dt, cols, lda) || !dense_ok(b, dt, cols, ldb))) return METIS_ERR_INVALID;
+  Operands o;
+  o.out(da, rows, cols, ldda, elem_bytes(odt));
+  o.out(db, rows, cols, lddb, elem_bytes(odt));
+  o.out(h, rows, cols, ldh, elem_bytes(odt));
+  o.in(dh, rows, cols, lddh, elem_bytes(dhdt));
+  o.in(qa);
+  o.in(qb);
+  if (!qa) {
+    o.in(a, rows, cols, lda, elem_bytes(dt));
+    o.in(b, rows, cols, ldb, elem_bytes(dt));
+  }
+  if (!o.distinct()) return METIS_ERR_INVALID;
   BwdArgs g = {};
   g.dh = dh;
   g.lddh = lddh;

@@ -341,7 +341,10 @@ typedef struct {
  * width) into out, whose fmt, codes and scales the caller sets; the library
  * writes out->rows and out->cols. Beyond 2^31 - 1 rows or 2^30 columns:
  * METIS_ERR_UNSUPPORTED, here and in the calls below. In these calls no output
- * may overlap an input or another output. */
+ * (nor the workspace) may share memory with an input or another output, else
+ * METIS_ERR_INVALID; the two halves of one matrix share none. (Two matrices of
+ * different leading dimension are taken to share memory where their address
+ * ranges meet.) */
 metis_status_t act8_block_quant(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx,
                                 metis_act8_t *out, hipStream_t stream);
 /* The stored values as type dt, exact in both types (no element has more than

@@ -198,3 +198,46 @@ def test_a_launch_has_its_tensors_device_as_the_current_one(monkeypatch):
     with pytest.raises(M.MetisError):
         M._run(torch.device("cuda:1"), lambda *a: INVALID, 9)
     assert not inside
+
+
+def test_outputs_that_share_memory_are_refused():
+    """Operands at made-up addresses, 4 MiB apart but for the one pair named:
+    refused on the host, before anything is launched."""
+    L = M.load()
+    far = lambda k: (k + 1) << 22  # operand k
+    same = lambda k: far(k) + 32   # inside operand k
+    act = lambda codes, scales, fmt=2: M._Act8(fmt, 0, 4, 40, codes, scales)
+
+    def quant(x=far(0), codes=far(1), scales=far(2)):
+        return L.act8_block_quant(x, 0, 4, 40, 40, act(codes, scales), None)
+
+    def dequant(codes=far(0), scales=far(1), y=far(2)):
+        return L.act8_block_dequant(act(codes, scales), y, 0, 40, None)
+
+    def norm(x=far(0), w=far(1), b=far(2), y=far(3), mean=far(4), rstd=far(5), codes=far(6), scales=far(7)):
+        return L.metis_norm_fwd(x, 0, 4, 40, 48, w, b, 0, 0, 1e-5, y, 0, 40, mean, rstd, act(codes, scales), None)
+
+    nws = L.metis_norm_bwd_workspace_bytes(4, 40)
+
+    def grad(dy=far(0), x=far(1), w=far(2), mean=far(3), rstd=far(4), dx=far(5), dw=far(6), db=far(7), ws=far(8), q=None):
+        return L.metis_norm_bwd(dy, 0, 40, x, 0, 44, q, w, 0, 0, mean, rstd, 4, 40, dx, 0, 40, dw, db, 0, ws, nws, None)
+
+    def gate(a=far(0), b=far(1), h=far(2), ca=far(3), sa=far(4), cb=far(5), sb=far(6)):
+        return L.metis_swiglu_fwd(a, 40, b, 40, 0, 4, 40, h, 0, 40, act(ca, sa), act(cb, sb), None)
+
+    def back(dh=far(0), a=far(1), b=far(2), da=far(3), db=far(4), h=far(5), q=(None, None)):
+        return L.metis_swiglu_bwd(dh, 0, 40, a, 40, b, 40, 0, q[0], q[1], 4, 40, da, 40, db, 40, h, 40, 0, None)
+
+    refused = [quant(codes=same(0)), quant(scales=same(0)), quant(scales=far(1) + 159), quant(codes=far(0) - 159),
+               dequant(y=same(0)), dequant(y=far(1) - 4), dequant(y=far(1) + 4),
+               norm(y=far(0)), norm(y=same(1)), norm(y=same(2)), norm(mean=same(0)), norm(rstd=same(3)),
+               norm(rstd=far(4) + 12), norm(codes=same(0)), norm(scales=same(3)), norm(codes=far(7) - 1),
+               norm(y=far(0) + 48 * 4 - 4),  # rows of another pitch over each other
+               grad(dx=far(0)), grad(dx=same(1)), grad(dw=same(2)), grad(db=far(6) + 156), grad(dw=same(5)),
+               grad(dx=far(3) + 12), grad(dx=far(4) - 636), grad(ws=far(5)), grad(ws=far(0)), grad(db=same(8)),
+               grad(x=None, q=act(far(5) + 1, far(9))), grad(x=None, q=act(far(9), far(5) + 1)),
+               gate(h=far(0)), gate(h=far(1)), gate(ca=same(0)), gate(cb=far(3)), gate(sb=far(4) + 4), gate(sa=same(2)),
+               back(da=far(0)), back(db=far(1)), back(h=far(2)), back(da=far(4)), back(h=far(3) + 636), back(db=same(5)),
+               back(a=None, b=None, q=(act(far(3), far(9)), act(far(10), far(11)))),
+               back(a=None, b=None, q=(act(far(10), far(9)), act(far(11), far(5))))]
+    assert refused == [INVALID] * len(refused), [i for i, r in enumerate(refused) if r != INVALID]

@@ -191,3 +191,75 @@ def test_calls_on_another_stream_than_the_default():
         got = M.metis_norm_bwd(dy, x, None, mean2, rstd2)
     st.synchronize()
     assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_outputs_over_operands_are_refused():
+    """Every output that can be given, over an input and over another output;
+    halves of one matrix are apart."""
+    g = H.rng(46)
+    new = lambda: H.to_dev(g.standard_normal((6, 77)), torch.float32)
+    x, a, b, dy = new(), new(), new(), new()
+    w = torch.ones(77, device="cuda")
+    y, mean, rstd, q = M.metis_norm_fwd(x, w, w, save="mxint8")
+    _, qa, qb = M.metis_swiglu_fwd(a, b, save="mxint8")
+    over = M.Act8Tensor(M.MXINT8, 6, 77, qa.codes, qb.scales)
+    inside = M.Act8Tensor(M.MXINT8, 6, 77, x.view(torch.uint8).view(-1)[:6 * 77], q.scales)
+    spare = torch.zeros(2 * 77 + 76, device="cuda")
+    bad = [lambda: M.act8_block_quant(x, "mxint8", out=inside),
+           lambda: M.act8_block_dequant(inside, out=x),
+           lambda: M.metis_norm_fwd(x, out=x), lambda: M.metis_norm_fwd(x, save=inside),
+           lambda: M.metis_norm_fwd(a, out=x, save=inside),
+           lambda: M.metis_norm_bwd(dy, x, w, mean, rstd, out=dy), lambda: M.metis_norm_bwd(dy, x, w, mean, rstd, out=x),
+           lambda: M.metis_norm_bwd(dy, inside, w, mean, rstd, out=x),
+           lambda: M.metis_norm_bwd(dy, x, w, mean, rstd, dweight=w),
+           lambda: M.metis_norm_bwd(dy, x, None, mean, rstd, dweight=spare[:77], dbias=spare[76:153]),
+           lambda: M.metis_norm_bwd(dy, x, w, mean, rstd, out=y, dbias=y[3]),
+           lambda: M.metis_swiglu_fwd(a, b, out=a), lambda: M.metis_swiglu_fwd(a, b, out=b),
+           lambda: M.metis_swiglu_fwd(a, b, save=(qa, over)), lambda: M.metis_swiglu_fwd(a, x, save=(inside, qb)),
+           lambda: M.metis_swiglu_bwd(dy, a, b, da=dy), lambda: M.metis_swiglu_bwd(dy, a, b, db=a),
+           lambda: M.metis_swiglu_bwd(dy, a, b, da=x, db=x), lambda: M.metis_swiglu_bwd(dy, inside, qb, da=x),
+           lambda: M.metis_swiglu_bwd(dy, a, b, da=x, need_h=True, h=x)]
+    keep = [t.clone() for t in (x, a, b, dy, w, y)]
+    torch.cuda.synchronize()
+    for call in bad:
+        with pytest.raises(M.MetisError):
+            call()
+    assert all(torch.equal(p, t) for p, t in zip(keep, (x, a, b, dy, w, y)))
+    # apart: halves of one matrix, rows above and below, the two sums in one buffer, an output that is not asked for
+    both, tall = torch.zeros(6, 154, device="cuda"), torch.zeros(12, 77, device="cuda")
+    want = M.metis_swiglu_bwd(dy, a, b)
+    got = M.metis_swiglu_bwd(dy, a, b, da=both[:, :77], db=both[:, 77:], h=a)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2] is None
+    tall[:6] = x
+    assert torch.equal(M.metis_norm_fwd(tall[:6], w, w, out=tall[6:])[0], y)
+    grads = M.metis_norm_bwd(dy, x, w, mean, rstd, dweight=spare[:77], dbias=spare[77:154])
+    assert all(torch.equal(p, r) for p, r in zip(grads, M.metis_norm_bwd(dy, x, w, mean, rstd)))
+
+
+def test_shared_memory_is_found_wherever_it_lies():
+    """Random views of one buffer as input and output against the sets of their
+    elements: refused where they share one, and only there if their row pitch
+    is the same or one of them is a single row."""
+    g = H.rng(47)
+    buf = torch.zeros(2048, device="cuda")
+    index = torch.arange(2048)
+    cells = lambda t: set(index.as_strided(t.shape, t.stride(), t.storage_offset()).reshape(-1).tolist())
+    seen = {True: 0, False: 0}
+    for trial in range(1500):
+        rows, cols = int(g.integers(1, 5)), int(g.integers(1, 24))
+        pitch = [int(g.integers(cols, cols + 40))] * 2
+        if trial % 3 == 0:
+            pitch[1] = int(g.integers(cols, cols + 40))
+        x, y = (buf.as_strided((rows, cols), (ld, 1), int(g.integers(0, 150))) for ld in pitch)
+        try:
+            M.metis_swiglu_fwd(x, x, out=y)
+            taken = True
+        except M.MetisError:
+            taken = False
+        shared = bool(cells(x) & cells(y))
+        assert not (taken and shared), (trial, rows, cols, pitch)
+        if pitch[0] == pitch[1] or rows == 1:
+            assert taken != shared, (trial, rows, cols, pitch)
+        seen[taken] += 1
+    torch.cuda.synchronize()
+    assert min(seen.values()) > 200
