@@ -670,6 +670,10 @@ def metis_norm_fwd(x, weight=None, bias=None, kind="layer", eps=1e-5, dtype=None
     y, ldy = _out(out, "out", x, dtype, dev)
     mean = torch.empty(rows, dtype=torch.float32, device=dev) if k == NORM_LAYER else None
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    if not cols:  # rows of no elements, which the call leaves alone: 0 / 0
+        rstd.fill_(float("nan"))
+        if mean is not None:
+            mean.fill_(float("nan"))
     stored = _save(save, x)
     _run(dev, load().metis_norm_fwd, x.data_ptr(), dt, rows, cols, ldx, wp, bp, wdt, k, eps, y.data_ptr(), ydt, ldy,
          None if mean is None else mean.data_ptr(), rstd.data_ptr(), None if stored is None else stored.c())

@@ -362,7 +362,8 @@ metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, metis_dtype_t
  *  w, b:   cols elements of type wdt; either may be NULL (w = 1, b = 0).
  *  y:      rows x cols of type ydt, rounded once from fp32.
  *  mean, rstd: optional fp32 outputs, one per row (mean: LAYER only, not
- *          written for RMS); the backward pass needs them.
+ *          written for RMS; neither with cols = 0); the backward pass needs
+ *          them.
  *  stored: optional: x in 8 bits as act8_block_quant writes it (fmt, codes and
  *          scales set by the caller), from the same read of x.
  *  eps >= 0 (else METIS_ERR_INVALID). Sums in fp32; the deviation is summed

@@ -375,3 +375,16 @@ def test_rows_whose_sum_overflows(cols, dtype):
     assert torch.equal(dx[3], torch.zeros_like(dx[3]))
     # row 2's deviation is its mean's rounding: 0, or at least a step of 3.3e38, whose square overflows
     assert torch.equal(y[2], b)
+
+
+def test_rows_of_no_elements():
+    """Their statistics are 0 / 0, not what the allocator left there."""
+    junk = [torch.full((5,), 3.0, device="cuda") for _ in range(8)]
+    del junk
+    e = torch.empty(5, 0, device="cuda", dtype=torch.bfloat16)
+    for kind in ("layer", "rms"):
+        y, mean, rstd, q = M.metis_norm_fwd(e, kind=kind, save="mxfp8")
+        assert tuple(y.shape) == (5, 0) and tuple(rstd.shape) == (5,) and q.cols == 0
+        assert torch.isnan(rstd).all() and (mean is None if kind == "rms" else torch.isnan(mean).all())
+        dx, dw, db = M.metis_norm_bwd(e, q, None, mean, rstd, kind=kind, need_dbias=True)
+        assert tuple(dx.shape) == (5, 0) and dw.numel() == 0 and db.numel() == 0
