@@ -550,6 +550,8 @@ class Act8Tensor:
     def from_codes(fmt, codes, scales):
         """The record of given codes (rows x cols) and scale bytes (rows x
         ceil(cols / 32))."""
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise MetisError("codes must be a 2-D tensor")
         q = Act8Tensor(_fmt8(fmt), codes.shape[0], codes.shape[1], codes, scales)
         _stored(q, "codes", codes.shape, codes.device)
         return q
@@ -575,7 +577,7 @@ def _stored(q, name, shape, device):
     if q.rows != rows or q.cols != cols:
         raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
     for buf, n in ((q.codes, rows * cols), (q.scales, rows * -(-cols // BLOCK8))):
-        if buf.dtype != torch.uint8 or buf.numel() != n or not buf.is_contiguous() or not buf.is_cuda:
+        if not isinstance(buf, torch.Tensor) or buf.dtype != torch.uint8 or buf.numel() != n or not buf.is_contiguous() or not buf.is_cuda:
             raise MetisError("%s needs contiguous uint8 CUDA codes and scales of its size" % name)
         if buf.device != device:
             raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))

@@ -241,3 +241,11 @@ def test_outputs_that_share_memory_are_refused():
                back(a=None, b=None, q=(act(far(3), far(9)), act(far(10), far(11)))),
                back(a=None, b=None, q=(act(far(10), far(9)), act(far(11), far(5))))]
     assert refused == [INVALID] * len(refused), [i for i, r in enumerate(refused) if r != INVALID]
+
+
+def test_records_of_other_things_than_matrices_are_refused():
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    for c, s in ((codes.view(-1), scales), (codes.view(2, 2, 64), scales), (codes[0, 0], scales), (None, scales),
+                 ([1, 2], scales), (codes, None), (codes, codes), (codes.float(), scales)):
+        with pytest.raises(M.MetisError):
+            M.Act8Tensor.from_codes("mxfp8", c, s)
