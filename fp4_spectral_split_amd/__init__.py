@@ -685,8 +685,9 @@ def metis_norm_fwd(x, weight=None, bias=None, kind="layer", eps=1e-5, dtype=None
 def metis_norm_bwd(dy, x, weight, mean, rstd, kind="layer", dtype=None, need_dweight=True, need_dbias=None,
                    dweight=None, dbias=None, accumulate=False, out=None):
     """Gradients of metis_norm_fwd: (dx, dweight, dbias). x: the forward's
-    input, dense or as the Act8Tensor it stored; mean and rstd: as it returned
-    them. dx is of type `dtype` (default: dy's); dweight and dbias are fp32
+    input, dense or as the Act8Tensor it stored (rows whose mean is many times
+    their deviation are better kept dense: the storage rounds x, not x - mean);
+    mean and rstd: as it returned them. dx is of type `dtype` (default: dy's); dweight and dbias are fp32
     (need_dbias defaults to the layer norm), added to the tensors given with
     accumulate=True."""
     lddy = _matrix(dy, "dy")

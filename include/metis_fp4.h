@@ -385,7 +385,11 @@ metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int
  *   dw = sum over rows of dy xh,  db = sum over rows of dy.
  *  dy:     rows x cols of type dydt. x: dense, type xdt; or NULL with `stored`
  *          the 8-bit form of x (its rows and cols set): then xh is formed from
- *          the stored values with the mean and rstd given.
+ *          the stored values with the mean and rstd given, and off by up to
+ *          |x| rstd / 16 (MXFP8) or max |x of its block| rstd / 127 (MXINT8).
+ *          For a row whose mean is m deviations that is about m / 16 or
+ *          (m + 3) / 127 in an xh of order 1: beyond m of a few (MXFP8) or a
+ *          few tens (MXINT8) keep x dense.
  *  mean, rstd: as written by metis_norm_fwd (mean may be NULL for RMS).
  *  dx:     rows x cols of type dxdt, rounded once from fp32.
  *  dw, db: optional fp32 of cols elements, stored (accumulate == 0) or added

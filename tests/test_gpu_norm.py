@@ -388,3 +388,30 @@ def test_rows_of_no_elements():
         assert torch.isnan(rstd).all() and (mean is None if kind == "rms" else torch.isnan(mean).all())
         dx, dw, db = M.metis_norm_bwd(e, q, None, mean, rstd, kind=kind, need_dbias=True)
         assert tuple(dx.shape) == (5, 0) and dw.numel() == 0 and db.numel() == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("offset", [0.0, 4.0, 64.0, 4096.0])
+@pytest.mark.parametrize("cols", [1000, 5000, 17000])
+def test_stored_input_under_a_large_mean(cols, offset, fmt):
+    """x with a mean of 0 to 4096 deviations, stored: the gradient is that of
+    the stored values at the forward's statistics, and xh (dw of a single row
+    under dy = 1) is off the dense one's by no more than the storage: half an
+    E4M3 step, |x| / 16, or 2^-10 of a scale below max|x| / 224; half an integer
+    step, 2^-7 of a scale below max|x| 128 / 127."""
+    g = H.rng(48)
+    x = H.to_dev(offset + g.standard_normal((3, cols)), torch.float32)
+    _, mean, rstd, q = M.metis_norm_fwd(x, save=fmt)
+    x64, m64, r64 = H.np64(x), H.np64(mean), H.np64(rstd)
+    x8 = A.restored(x64, fmt)
+    dy = H.to_dev(g.standard_normal((3, cols)), torch.float32)
+    out = M.metis_norm_bwd(dy, q, None, mean, rstd)
+    _check_bwd(out, H.np64(dy), x8, None, m64, r64, "layer", torch.float32)
+    blocks = np.pad(np.abs(x64), ((0, 0), (0, -cols % 32))).reshape(3, -1, 32)
+    top = np.repeat(blocks.max(axis=2), 32, axis=1)[:, :cols]
+    held = np.maximum(np.abs(x64) / 16, top / 224 / 1024) if fmt == "mxfp8" else top / 127
+    for r in range(3):
+        one = M.Act8Tensor.from_codes(fmt, q.codes.view(3, cols)[r:r + 1], q.scales.view(3, -1)[r:r + 1])
+        _, xh, _ = M.metis_norm_bwd(torch.ones(1, cols, device="cuda"), one, None, mean[r:r + 1], rstd[r:r + 1])
+        true = (x64[r] - m64[r]) * r64[r]
+        _close(H.np64(xh), true, held[r] * r64[r] * (1 + 4 * U) + 4 * U * np.abs(true), "xh")
