@@ -139,3 +139,38 @@ def test_gradient_of_rows_whose_columns_pass_one_launch():
     print("case wide norm bwd without rows", cols, flush=True)
     M.metis_norm_bwd(dy[:0], x[:0], None, mean[:0], rstd[:0], dweight=dw, dbias=db)
     assert not dw.any() and not db.any() and torch.all(buf[:, cols] == 7.0)
+
+
+def test_gate_over_two_launches_with_storage_and_rebuilt_output():
+    """The gate's pointers advance from launch to launch: of the 8-bit forms it
+    writes, of dense and of stored inputs and of h, on both sides of row 524287,
+    where the second launch starts."""
+    rows, cols = (1 << 19) + 24, 1 << 15
+    spans = [(0, 16), (524280, 524296), (rows - 4, rows)]
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(7)
+    x = torch.zeros(rows, cols, device=DEV, dtype=torch.bfloat16)
+    for i, j in spans:
+        x[i:j] = torch.randn(j - i, cols, device=DEV, generator=gen).to(torch.bfloat16)
+    print("case two launches gate storing", flush=True)
+    h, qa, qb = M.metis_swiglu_fwd(x, x, save="mxint8")
+    parts = []
+    for i, j in spans:
+        part = M.metis_swiglu_fwd(x[i:j], x[i:j], save="mxint8")
+        parts.append(part[1:])
+        assert torch.equal(h[i:j], part[0])
+        assert all(torch.equal(a, b) for a, b in zip(_rows_of(qa, i, j) + _rows_of(qb, i, j),
+                                                     _rows_of(part[1], 0, j - i) + _rows_of(part[2], 0, j - i)))
+    del h
+    torch.cuda.empty_cache()
+    print("case two launches gate gradient, stored", flush=True)
+    grads = M.metis_swiglu_bwd(x, qa, qb, need_h=True)
+    for (i, j), (pa, pb) in zip(spans, parts):
+        alone = M.metis_swiglu_bwd(x[i:j], pa, pb, need_h=True)
+        assert all(torch.equal(a[i:j], b) for a, b in zip(grads, alone))
+    del qa, qb
+    print("case two launches gate gradient, dense", flush=True)
+    grads = M.metis_swiglu_bwd(x, x, x, need_h=True, da=grads[0], db=grads[1], h=grads[2])
+    for i, j in spans:
+        alone = M.metis_swiglu_bwd(x[i:j], x[i:j], x[i:j], need_h=True)
+        assert all(torch.equal(a[i:j], b) for a, b in zip(grads, alone))
