@@ -263,3 +263,41 @@ def test_shared_memory_is_found_wherever_it_lies():
         seen[taken] += 1
     torch.cuda.synchronize()
     assert min(seen.values()) > 200
+
+
+def test_two_threads_finish_all_their_calls():
+    """Two host threads again, with whatever ends one recorded and its calls counted."""
+    import threading
+
+    g = H.rng(49)
+    jobs = []
+    for rows, cols in ((150, 2056), (70, 9000)):
+        x = H.to_dev(TN._stream(g, (rows, cols)), torch.float32)
+        dy = H.to_dev(g.standard_normal((rows, cols)), torch.bfloat16)
+
+        def work(x=x, dy=dy):
+            y, mean, rstd, q = M.metis_norm_fwd(x, save="mxfp8", kind="layer")
+            h, a, b = M.metis_swiglu_fwd(x, y, save="mxint8")
+            return [y, *M.metis_norm_bwd(dy, q, None, mean, rstd), h, *M.metis_swiglu_bwd(dy, a, b, need_h=True)]
+
+        jobs.append((work, work()))
+    torch.cuda.synchronize()
+    ended = [None, None]
+
+    def run(k, work, want):
+        done = 0
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    done += all(torch.equal(p, q) for p, q in zip(work(), want))
+            ended[k] = done
+        except BaseException as e:  # kept for the assertion below
+            ended[k] = e
+
+    threads = [threading.Thread(target=run, args=(k, *j)) for k, j in enumerate(jobs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert ended == [50, 50]
