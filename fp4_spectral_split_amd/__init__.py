@@ -639,7 +639,8 @@ def act8_block_quant(x, fmt="mxfp8", out=None):
 
 
 def act8_block_dequant(q, dtype=torch.float32, out=None):
-    """The values of an Act8Tensor as fp32 or bf16 (both hold them exactly)."""
+    """The values of an Act8Tensor as fp32 or bf16: exact but for bf16
+    subnormals and for MXFP8 values rounded to 2^128 (infinity)."""
     dev, shape, dt = q.codes.device, (q.rows, q.cols), _code(dtype)
     _stored(q, "q", shape, dev)
     out, ld = _out(out, "out", q.codes.view(shape), dtype, dev)
@@ -658,7 +659,9 @@ def metis_norm_fwd(x, weight=None, bias=None, kind="layer", eps=1e-5, dtype=None
     """Layer ("layer") or RMS ("rms") norm of the rows of a 2-D fp32/bf16 CUDA
     tensor: (y, mean, rstd, stored). y is of type `dtype` (default: x's); mean
     (None for RMS) and rstd are fp32, one per row. save: "mxfp8" / "mxint8" or
-    an Act8Tensor to write into: x in 8 bits for the backward pass, as stored."""
+    an Act8Tensor to write into: x in 8 bits for the backward pass, as stored.
+    Where a row's sum of squares passes fp32's range its rstd is 0 and y the
+    bias."""
     ldx = _matrix(x, "x")
     dev, shape = x.device, x.shape
     rows, cols = shape

@@ -1,9 +1,12 @@
 // 8-bit storage of activations: act8_block_quant / act8_block_dequant.
 //
 // Streaming passes, HBM bound: a lane takes one chunk of eight elements, four
-// lanes one block. 8192 x 14336 bf16 to MXFP8 61 us, back 60 us (5.8 TB/s both;
-// plain kernels that move the same streams 59 and 54); two or four chunks per
-// lane change nothing (60.5, 62.5) and cost up to a quarter in fp32.
+// lanes one block. 8192 x 14336 bf16, inputs taking turns: to MXFP8 69 us (5.2
+// TB/s), back from the codes just written 56 us, both as one pass 124 us (5.7
+// TB/s). With one input used again and again, and so partly in the Infinity
+// Cache, 61 and 60 us, plain kernels that move the same streams 59 and 54; two
+// or four chunks per lane change nothing there (60.5, 62.5) and cost up to a
+// quarter in fp32.
 #include <algorithm>
 
 #include "act8.hpp"

@@ -6,17 +6,23 @@
 //   dw = sum over rows of dy xh,    db = sum over rows of dy
 //
 // HBM bound. A row is held in registers between its reduction and its use,
-// by one wave or one workgroup, so that x (and dy) are read once; rows beyond
-// what a workgroup holds are read again, out of the L2. All sums are fp32.
+// by one wave or one workgroup, so that x (and dy) are read once. Rows beyond
+// what a workgroup holds (16384 columns) are read again by each pass over them:
+// two or three times by the forward pass, in part out of the L2, and by the
+// gradient twice for dx and once more, behind it, for dw and db. All sums are
+// fp32.
 // The gradients of w and b are summed over rows in two steps of fixed order
 // (a workgroup's rows in its registers, then the workgroups), without atomics:
 // results are bitwise reproducible.
 //
-// Measured for 8192 x 4096 (a plain kernel that moves the same streams in
-// brackets): forward bf16 to bf16 27 us (23.4), with x stored in MXFP8 as well
-// 32.5 us, 5.2 TB/s (30.7); gradient from bf16 dy and MXFP8 x to bf16 dx 30.6
-// us, 5.5 TB/s (30.6), from fp32 dy and MXINT8 x 37 us, 6.4 TB/s; the partial
-// sums joined 4 us.
+// Kernel durations at 8192 x 4096, inputs taking turns (a plain kernel that
+// moves the same streams in brackets): forward bf16 to bf16 with x stored in
+// MXFP8 31.4 us, 5.4 TB/s (30.7); gradient from fp32 dy and MXINT8 x to bf16 dx
+// 38.7 us, 6.1 TB/s; behind its forward pass, and so with x in part still in the
+// Infinity Cache, from bf16 dy and MXFP8 x 30.8 us (30.6), from fp32 dy and x 55
+// us; the partial sums joined 4 to 5 us. Beyond 16384 columns, 1024 x 32768
+// bf16: forward 45 us, 2.1 times its bytes at 6.2 TB/s; gradient 50 and 27 us
+// and 7 for the join, 2.6 times.
 #include <algorithm>
 #include <type_traits>
 
@@ -631,7 +637,7 @@ template <typename T, typename TY, bool LAYER, int STORE> void fwd_launch(const 
   // Up to 6144 columns at most four waves, one on each SIMD: the fifth wave of a
   // workgroup shares the first one's SIMD, and so does every workgroup's (8192 x
   // 4100 with its input stored, five waves of two chunks 57 us, four of three
-  // 47); beyond, whole sets of four (14336 columns in 16 waves 119 us, in 14
+  // 47, layer norm with its second sum 49); beyond, whole sets of four (14336 columns in 16 waves 119 us, in 14
   // 143). As many workgroups as the GPU holds, each with its w and b over
   // several rows.
   const unsigned lanes = g.cols <= 2048   ? lanes_for(g.cols, 1, 64)
@@ -665,6 +671,10 @@ template <typename T, typename TY> void fwd_by_kind(const FwdArgs &g, bool layer
 // chunks of a row per thread, two rows at once: 84 us; one chunk and one row:
 // 81.
 int groups_of(int64_t cols) { return cols <= 2048 ? 4 : (cols <= 6144 ? 2 : 1); }
+
+// (Registers: of dense fp32 x with a layer norm at 2049 to 6144 columns 8 or 12
+// bytes a lane spill, of stored x, fp32 dy and bf16 dx with a layer norm at 8193
+// to 16384 columns 8 bytes; no other type does.)
 
 // Workgroups of the backward pass, each leaving one partial sum of dw and db
 // (of a row beyond kHeldCols: row groups, fewer of them the wider the row is).

@@ -6,9 +6,9 @@
 // projection behind the gate.
 //
 // Streaming passes, HBM bound: a lane takes one chunk of eight elements of
-// every operand. 8192 x 14336, fp32 a and b to bf16 h with MXINT8 storage 262
+// every operand. 8192 x 14336, fp32 a and b to bf16 h with MXINT8 storage 260
 // us, 5.4 TB/s (a plain kernel that moves the same streams 243); from fp32 dh
-// and the stored inputs to bf16 da, db and h 240 us, 5.9 TB/s (252).
+// and the stored inputs to bf16 da, db and h 248 us, 5.7 TB/s (252).
 #include <algorithm>
 #include <type_traits>
 

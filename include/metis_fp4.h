@@ -369,9 +369,9 @@ metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, metis_dtype_t
  *  eps >= 0 (else METIS_ERR_INVALID). Sums in fp32; the deviation is summed
  * around the mean, in a second pass over the row on chip. A finite row has a
  * finite mean. Where the sum of squares passes fp32's largest number (n
- * elements 1.8e19 / sqrt(n) from the mean; from 0 for RMS) rstd is 0: y is b
- * and the row adds nothing to any gradient (an element farther from the mean
- * than that number gives NaN). At the other end, squares below 1e-38 lose bits,
+ * elements 1.8e19 / sqrt(n) from the mean; from 0 for RMS) rstd is 0: y is b,
+ * dx is 0 and the row adds nothing to dw (an element farther from the mean than
+ * that number gives NaN). At the other end, squares below 1e-38 lose bits,
  * which shows where eps is no larger; with eps = 0 a row whose squares are all
  * 0 has rstd = infinity and y = NaN. */
 typedef enum { METIS_NORM_LAYER = 0, METIS_NORM_RMS = 1 } metis_norm_t;
@@ -397,8 +397,8 @@ metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int
  *          (stored) or kept (added).
  *  ws:     metis_norm_bwd_workspace_bytes() bytes, 256-byte aligned; may be
  *          NULL without dw and db. Sums over rows run in a fixed order (no
- *          atomics): bitwise reproducible. xh, dy w, rstd dy and
- *          their products have to stay in fp32's range. A NaN or an infinity in dy spoils its row of
+ *          atomics): bitwise reproducible. xh, dy w, rstd dy, their
+ *          products and the sums have to stay in fp32's range. A NaN or an infinity in dy spoils its row of
  *          dx and its column of dw and db; one in x, through the row's
  *          statistics, its row of dx and all of dw. */
 size_t metis_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);

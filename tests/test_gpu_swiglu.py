@@ -181,6 +181,8 @@ def test_empty_and_refused():
 
 
 # past both ends of the exponential: each magnitude in a row of its own, both signs
+# (the kernel takes s as 0 below a = -86.6: what the tests above allow there, in
+# proportion to |a|, is more than it needs)
 FAR = [80.0, 86.0, 86.5, 86.75, 87.0, 87.25, 87.5, 88.0, 90.0, 104.0, 128.0, 200.0, 1e4, 65504.0, 1e30, 1e36, 1e38, 3e38]
 
 
