@@ -577,7 +577,8 @@ def _stored(q, name, shape, device):
     if q.rows != rows or q.cols != cols:
         raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
     for buf, n in ((q.codes, rows * cols), (q.scales, rows * -(-cols // BLOCK8))):
-        if not isinstance(buf, torch.Tensor) or buf.dtype != torch.uint8 or buf.numel() != n or not buf.is_contiguous() or not buf.is_cuda:
+        if (not isinstance(buf, torch.Tensor) or buf.dtype != torch.uint8 or buf.numel() != n
+                or not buf.is_contiguous() or not buf.is_cuda):
             raise MetisError("%s needs contiguous uint8 CUDA codes and scales of its size" % name)
         if buf.device != device:
             raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))
@@ -690,9 +691,9 @@ def metis_norm_bwd(dy, x, weight, mean, rstd, kind="layer", dtype=None, need_dwe
     """Gradients of metis_norm_fwd: (dx, dweight, dbias). x: the forward's
     input, dense or as the Act8Tensor it stored (rows whose mean is many times
     their deviation are better kept dense: the storage rounds x, not x - mean);
-    mean and rstd: as it returned them. dx is of type `dtype` (default: dy's); dweight and dbias are fp32
-    (need_dbias defaults to the layer norm), added to the tensors given with
-    accumulate=True."""
+    mean and rstd: as it returned them. dx is of type `dtype` (default: dy's);
+    dweight and dbias are fp32 (need_dbias defaults to the layer norm), added to
+    the tensors given with accumulate=True."""
     lddy = _matrix(dy, "dy")
     dev, shape = dy.device, dy.shape
     rows, cols = shape
