@@ -21,6 +21,11 @@ Calls (same names as the C ABI in include/metis_fp4.h):
   metis_norm_bwd(dy, x, weight, mean, rstd)    -> (dx, dweight, dbias)
   metis_swiglu_fwd(a, b)                       -> (silu(a) b, stored a, stored b)
   metis_swiglu_bwd(dh, a, b)                   -> (da, db, silu(a) b)
+  metis_qk_norm_rope_fwd(q, k, positions, ...) -> (q', k') normed and rotated
+  metis_qk_norm_rope_bwd(dq, dk, q, k, ...)    -> (dq, dk, dwq, dwk)
+  metis_fp4_gemv(x, W)                         -> y = x W^T of a few tokens
+  metis_kv_append(k, v, batch, cache)          -> the KvCache (paged, FP4)
+  metis_kv_attention(q, batch, cache)          -> (o, log-sum-exp)
 """
 import ctypes
 import os
@@ -40,9 +45,12 @@ _FMT_NAME = {MXFP4: "mxfp4", NVFP4: "nvfp4"}
 BLOCK = {MXFP4: 32, NVFP4: 16}
 MXFP8, MXINT8 = 2, 3
 BLOCK8 = 32
-NORM_LAYER, NORM_RMS = 0, 1
+NORM_LAYER, NORM_RMS, NORM_NONE = 0, 1, 2
 _FMT8 = {"mxfp8": MXFP8, "mxint8": MXINT8, MXFP8: MXFP8, MXINT8: MXINT8}
 _FMT8_NAME = {MXFP8: "mxfp8", MXINT8: "mxint8"}
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+_PAIRS = {"halves": ROPE_HALVES, "neighbours": ROPE_NEIGHBOURS, ROPE_HALVES: ROPE_HALVES,
+          ROPE_NEIGHBOURS: ROPE_NEIGHBOURS}
 _KIND = {"layer": NORM_LAYER, "rms": NORM_RMS, NORM_LAYER: NORM_LAYER, NORM_RMS: NORM_RMS}
 
 
@@ -65,6 +73,16 @@ class _Split(ctypes.Structure):
 class _Act8(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("k", _Fp4),
+                ("v", _Fp4)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("ldt", ctypes.c_int64), ("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -140,6 +158,26 @@ def load():
     L.metis_swiglu_bwd.restype = i32
     L.metis_swiglu_bwd.argtypes = [vp, i32, i64, vp, i64, vp, i64, i32, q8, q8, i64, i64, vp, i64, vp, i64, vp, i64,
                                    i32, vp]
+    L.metis_qk_norm_rope_fwd.restype = i32
+    L.metis_qk_norm_rope_fwd.argtypes = [vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, i32, i32, f32, vp, vp, i64,
+                                         i32, i32, vp, i64, vp, i64, i32, vp]
+    L.metis_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    L.metis_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    L.metis_qk_norm_rope_bwd.restype = i32
+    L.metis_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, i32,
+                                         i32, f32, vp, vp, i64, i32, i32, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz,
+                                         vp]
+    L.metis_fp4_gemv_workspace_bytes.restype = sz
+    L.metis_fp4_gemv_workspace_bytes.argtypes = [i64, i32, sp]
+    L.metis_fp4_gemv.restype = i32
+    L.metis_fp4_gemv.argtypes = [vp, i32, i64, i64, sp, vp, i32, i64, vp, sz, vp]
+    kc, kb = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
+    L.metis_kv_append.restype = i32
+    L.metis_kv_append.argtypes = [vp, i64, vp, i64, i32, i64, kb, vp, i64, i32, i32, kc, vp]
+    L.metis_kv_attention_workspace_bytes.restype = sz
+    L.metis_kv_attention_workspace_bytes.argtypes = [i64, i32, i32, i64, kb, kc]
+    L.metis_kv_attention.restype = i32
+    L.metis_kv_attention.argtypes = [vp, i32, i64, i64, i32, kb, kc, i32, i64, f32, i64, vp, i32, i64, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -152,7 +190,9 @@ EXPORTS = ["metis_status_str", "metis_abi_version", "fp4_block_quant_workspace_b
            "metis_gemm_nt_prepare", "metis_gemm_nt_main", "metis_spectral_lr_rescale",
            "metis_dual_range_workspace_bytes", "metis_dual_range_reg", "act8_block_quant", "act8_block_dequant",
            "metis_norm_fwd", "metis_norm_bwd_workspace_bytes", "metis_norm_bwd", "metis_swiglu_fwd",
-           "metis_swiglu_bwd"]
+           "metis_swiglu_bwd", "metis_qk_norm_rope_fwd", "metis_qk_norm_rope_bwd_workspace_bytes",
+           "metis_qk_norm_rope_bwd", "metis_fp4_gemv_workspace_bytes", "metis_fp4_gemv", "metis_kv_append",
+           "metis_kv_attention_workspace_bytes", "metis_kv_attention"]
 
 
 def _check(status):
@@ -793,3 +833,343 @@ def metis_swiglu_bwd(dh, a, b, dtype=None, need_h=False, da=None, db=None, h=Non
     _run(dev, load().metis_swiglu_bwd, dh.data_ptr(), dhdt, lddh, ap, lda, bp, ldb, dt, qa, qb, shape[0], shape[1],
          da.data_ptr(), ldda, db.data_ptr(), lddb, hp, ldh, odt)
     return da, db, h
+
+
+# ------------------------- attention around the projections, and few tokens
+def _heads(t, name, dim, device=None):
+    """Checks a tokens x (heads * dim) tensor; returns (leading dimension,
+    heads)."""
+    ld = _matrix(t, name, None, device)
+    cols = t.shape[1]
+    if dim < 1 or cols % dim or not cols:
+        raise MetisError("%s must have a whole number of heads of %d columns, got %d" % (name, dim, cols))
+    return ld, cols // dim
+
+
+def _pairs(pairs):
+    p = _PAIRS.get(pairs)
+    if p is None:
+        raise MetisError("pairs must be halves or neighbours, got %r" % (pairs,))
+    return p
+
+
+def _rope(rope, device):
+    """Checks an optional table of angles; returns (address, rows, elements
+    turned)."""
+    if rope is None:
+        return None, 0, 0
+    if (not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype != torch.float32
+            or not rope.is_contiguous() or not rope.is_cuda):
+        raise MetisError("rope must be a contiguous 2-D float32 CUDA tensor")
+    if rope.device != device:
+        raise MetisError("rope is on %s, the other operands on %s" % (rope.device, device))
+    return rope.data_ptr(), rope.shape[0], rope.shape[1]
+
+
+def _qk_common(q, k, positions, rope, head_dim, weight_q, weight_k, kind, tokens, dev):
+    """The arguments that both directions share: (kind, weights' addresses and
+    type, position and rope arguments)."""
+    kd = NORM_NONE if kind is None else _norm_kind(kind)
+    for w, name in ((weight_q, "weight_q"), (weight_k, "weight_k")):
+        if w is not None and kd == NORM_NONE:
+            raise MetisError("%s needs a norm" % name)
+    if weight_k is not None and k is None:
+        raise MetisError("weight_k without k")
+    wq = _vector(weight_q, "weight_q", head_dim, dev)
+    wk = _vector(weight_k, "weight_k", head_dim, dev, weight_q.dtype if weight_q is not None else None)
+    wt = weight_q if weight_q is not None else weight_k
+    rp, rows, rot = _rope(rope, dev)
+    pos = None
+    if rope is not None:
+        if positions is None:
+            raise MetisError("the rotation needs positions")
+        pos = _vector(positions, "positions", tokens, dev, torch.int32)
+    return kd, wq, wk, _code(wt.dtype) if wt is not None else F32, pos, rp, rows, rot
+
+
+def metis_qk_norm_rope_fwd(q, k, positions, rope, head_dim, weight_q=None, weight_k=None, kind="rms", eps=1e-6,
+                           pairs="halves", dtype=None, out_q=None, out_k=None):
+    """Norm of every head of queries and keys ("rms", "layer", or None for
+    none) and rotation of its first elements in the same pass: (q', k'). q, k:
+    tokens x (heads * head_dim) fp32/bf16 CUDA tensors of one type with
+    contiguous rows, parts of one projection's output as well; k may be None.
+    weight_q, weight_k: head_dim elements, shared by the heads. rope: fp32,
+    positions x rot_dim, the cosines of a position's angles, then their sines
+    (None: no rotation); positions: int32, one per token, NaN where outside it.
+    pairs: "halves" turns elements i and i + rot_dim / 2 together,
+    "neighbours" 2 i and 2 i + 1. The outputs are of type `dtype` (default:
+    q's) and must not share memory with an input or with each other."""
+    ldq, hq = _heads(q, "q", head_dim)
+    dev, tokens, dt = q.device, q.shape[0], _code(q.dtype)
+    ldk = hk = 0
+    if k is not None:
+        ldk, hk = _heads(k, "k", head_dim, dev)
+        if k.shape[0] != tokens or k.dtype != q.dtype:
+            raise MetisError("q and k must be of one type and have one row per token")
+    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(q, k, positions, rope, head_dim, weight_q, weight_k, kind, tokens,
+                                                     dev)
+    dtype = q.dtype if dtype is None else dtype
+    odt = _code(dtype)
+    out_q, ldqo = _out(out_q, "out_q", q, dtype, dev)
+    ldko = 0
+    if k is not None:
+        out_k, ldko = _out(out_k, "out_k", k, dtype, dev)
+    else:
+        out_k = None
+    _run(dev, load().metis_qk_norm_rope_fwd, q.data_ptr(), ldq, hq, None if k is None else k.data_ptr(), ldk, hk, dt,
+         tokens, head_dim, wq, wk, wdt, kd, eps, pos, rp, rows, rot, _pairs(pairs), out_q.data_ptr(), ldqo,
+         None if k is None else out_k.data_ptr(), ldko, odt)
+    return out_q, out_k
+
+
+def metis_qk_norm_rope_bwd(dq, dk, q, k, positions, rope, head_dim, weight_q=None, weight_k=None, kind="rms", eps=1e-6,
+                           pairs="halves", dtype=None, need_dweight=None, dweight_q=None, dweight_k=None,
+                           accumulate=False, out_q=None, out_k=None):
+    """Gradients of metis_qk_norm_rope_fwd: (dq, dk, dweight_q, dweight_k).
+    dq, dk: the gradients of its outputs; q, k: its inputs (not read, and may
+    be None, with kind=None). The gradients of q and k are of type `dtype`
+    (default: dq's); those of the weights fp32 (need_dweight defaults to the
+    weights given), added to the tensors given with accumulate=True."""
+    lddq, hq = _heads(dq, "dq", head_dim)
+    dev, tokens, dydt = dq.device, dq.shape[0], _code(dq.dtype)
+    lddk = hk = ldq = ldk = 0
+    if dk is not None:
+        lddk, hk = _heads(dk, "dk", head_dim, dev)
+        if dk.shape[0] != tokens or dk.dtype != dq.dtype:
+            raise MetisError("dq and dk must be of one type and have one row per token")
+    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(dq, dk, positions, rope, head_dim, weight_q, weight_k, kind,
+                                                     tokens, dev)
+    qp = kp = None
+    dt = F32
+    if kd != NORM_NONE:
+        if q is None or (dk is not None and k is None):
+            raise MetisError("the gradient of a norm needs its inputs q and k")
+        ldq, qp, dt = _matrix(q, "q", dq.shape, dev), q.data_ptr(), _code(q.dtype)
+        if dk is not None:
+            ldk, kp = _matrix(k, "k", dk.shape, dev), k.data_ptr()
+            if k.dtype != q.dtype:
+                raise MetisError("q and k must be of one type")
+    dtype = dq.dtype if dtype is None else dtype
+    dxdt = _code(dtype)
+    want_q = weight_q is not None if need_dweight is None else bool(need_dweight) and kd != NORM_NONE
+    want_k = (weight_k is not None if need_dweight is None else bool(need_dweight) and kd != NORM_NONE) and hk > 0
+    if accumulate and ((want_q and dweight_q is None) or (want_k and dweight_k is None)):
+        raise MetisError("accumulate needs the gradients to add to")
+    out_q, lddqi = _out(out_q, "out_q", dq, dtype, dev)
+    lddki = 0
+    if dk is not None:
+        out_k, lddki = _out(out_k, "out_k", dk, dtype, dev)
+    else:
+        out_k = None
+    wqp = wkp = ws = None
+    if want_q:
+        dweight_q, wqp = _sum_out(dweight_q, "dweight_q", head_dim, dev)
+    if want_k:
+        dweight_k, wkp = _sum_out(dweight_k, "dweight_k", head_dim, dev)
+    L, nws = load(), 0
+    if want_q or want_k:  # a buffer of its own per call, as in metis_norm_bwd
+        nws = L.metis_qk_norm_rope_bwd_workspace_bytes(tokens, hq, hk, head_dim)
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _run(dev, L.metis_qk_norm_rope_bwd, dq.data_ptr(), lddq, None if dk is None else dk.data_ptr(), lddk, dydt, qp,
+         ldq, hq, kp, ldk, hk, dt, tokens, head_dim, wq, wk, wdt, kd, eps, pos, rp, rows, rot, _pairs(pairs),
+         out_q.data_ptr(), lddqi, None if dk is None else out_k.data_ptr(), lddki, dxdt, wqp, wkp,
+         1 if accumulate else 0, ws.data_ptr() if nws else None, nws)
+    return out_q, out_k, dweight_q if want_q else None, dweight_k if want_k else None
+
+
+def _fp4_buffers(q, name, rows, cols, device, fmt=None):
+    """Checks an Fp4Tensor: its buffers hold the matrix it says, on the device."""
+    if not isinstance(q, Fp4Tensor) or q.fmt not in _FMT_NAME or (fmt is not None and q.fmt != fmt):
+        raise MetisError("%s must be an Fp4Tensor%s" % (name, "" if fmt is None else " in " + _FMT_NAME[fmt]))
+    if q.rows != rows or q.cols != cols:
+        raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
+    sizes = [(q.codes, rows * cols // 2, torch.uint8), (q.scales, rows * (cols // BLOCK[q.fmt]), torch.uint8)]
+    if q.fmt == NVFP4:
+        sizes.append((q.tensor_scale, 1, torch.float32))
+    for buf, n, dtype in sizes:
+        if (not isinstance(buf, torch.Tensor) or buf.dtype != dtype or buf.numel() != n or not buf.is_contiguous()
+                or not buf.is_cuda):
+            raise MetisError("%s needs contiguous CUDA codes and scales of its size" % name)
+        if buf.device != device:
+            raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))
+
+
+def metis_fp4_gemv(x, W, dtype=None, out=None):
+    """y = x W_hat^T of a few tokens: x a 2-D fp32/bf16 CUDA tensor (tokens x
+    W.n, not quantized), W a SplitRecord (split or plain) with its R_q; y is
+    tokens x W.m of type `dtype` (default: x's). W is read once for each 64
+    tokens: many tokens are better quantized for spectral_fp4_linear_fwd."""
+    if not isinstance(W, SplitRecord) or W.R_q is None:
+        raise MetisError("W must be a SplitRecord with R_q")
+    ldx = _matrix(x, "x")
+    dev, tokens, dt = x.device, x.shape[0], _code(x.dtype)
+    if x.shape[1] != W.n:
+        raise MetisError("x must have %d columns, got %d" % (W.n, x.shape[1]))
+    _fp4_buffers(W.R_q, "R_q", W.m, W.n, dev, W.fmt)
+    if W.k:
+        _fp4_buffers(W.Ut_q, "Ut_q", W.k, W.m, dev, W.fmt)
+        _fp4_buffers(W.Vt_q, "Vt_q", W.k, W.n, dev, W.fmt)
+        if _vector(W.S, "S", W.k, dev, torch.float32) is None:
+            raise MetisError("a split weight needs its S")
+    dtype = x.dtype if dtype is None else dtype
+    ydt = _code(dtype)
+    if out is None:
+        out, ldy = x.new_empty((tokens, W.m), dtype=dtype), W.m
+    else:
+        ldy = _matrix(out, "out", (tokens, W.m), dev)
+        if out.dtype != dtype:
+            raise MetisError("out must be %s" % dtype)
+    L, w = load(), W.c()
+    nws = L.metis_fp4_gemv_workspace_bytes(tokens, dt, w)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _run(dev, L.metis_fp4_gemv, x.data_ptr(), dt, tokens, ldx, w, out.data_ptr(), ydt, ldy,
+         ws.data_ptr() if nws else None, nws)
+    return out
+
+
+@dataclass
+class KvCache:
+    """Paged cache of keys and values in FP4 (see metis_kv_cache_t): k and v
+    are Fp4Tensors of pages * heads * page_size rows and head_dim columns, the
+    row of place s in page p for head h being (p * heads + h) * page_size + s."""
+    pages: int
+    page_size: int
+    heads: int
+    k: Fp4Tensor
+    v: Fp4Tensor
+
+    @staticmethod
+    def empty(fmt, pages, page_size, heads, head_dim, device, k_scale=None, v_scale=None):
+        """A cache of zeros. k_scale, v_scale (NVFP4): the tensor scales that
+        everything stored is quantized with, for magnitudes up to 2688 times
+        them."""
+        f = _FMT.get(fmt)
+        if f is None:
+            raise MetisError("FP4 format must be mxfp4 or nvfp4, got %r" % (fmt,))
+        if (f == NVFP4) != (k_scale is not None) or (f == NVFP4) != (v_scale is not None):
+            raise MetisError("k_scale and v_scale belong to nvfp4, and to it alone")
+        if min(pages, page_size, heads, head_dim) < 1 or head_dim % 32:
+            raise MetisError("a cache needs pages of at least one place and heads of a multiple of 32")
+        rows = pages * heads * page_size
+        parts = []
+        for s in (k_scale, v_scale):
+            q = Fp4Tensor.empty(f, rows, head_dim, device)
+            q.codes.zero_()
+            q.scales.zero_()
+            if f == NVFP4:
+                q.tensor_scale.fill_(float(s))
+            parts.append(q)
+        return KvCache(pages, page_size, heads, *parts)
+
+    @staticmethod
+    def from_codes(fmt, pages, page_size, heads, head_dim, keys, values):
+        """The cache of given (codes, scale bytes, tensor scale or None) of
+        keys and values."""
+        f = _FMT.get(fmt)
+        if f is None:
+            raise MetisError("FP4 format must be mxfp4 or nvfp4, got %r" % (fmt,))
+        rows = pages * heads * page_size
+        c = KvCache(pages, page_size, heads, Fp4Tensor(f, rows, head_dim, *keys), Fp4Tensor(f, rows, head_dim, *values))
+        _cache(c, c.k.codes.device if isinstance(c.k.codes, torch.Tensor) else None)
+        return c
+
+    @property
+    def head_dim(self):
+        return self.k.cols
+
+    def c(self):
+        return _KvCache(self.pages, self.page_size, self.heads, self.k.c(), self.v.c())
+
+
+@dataclass
+class KvBatch:
+    """Sequences and their new tokens (see metis_kv_batch_t). table: int32,
+    sequences x pages, each sequence's pages in order. lengths: int32, tokens
+    of each sequence with its new ones (0: not in use). starts: int32, one more
+    than sequences: sequence s has the rows starts[s] .. starts[s + 1] - 1;
+    None: row s belongs to sequence s. max_new: at least the most new tokens of
+    any sequence. max_length: about the largest length (default: what the table
+    holds), which attention divides its work by."""
+    table: torch.Tensor
+    lengths: torch.Tensor
+    starts: Optional[torch.Tensor] = None
+    max_new: int = 1
+    max_length: Optional[int] = None
+
+
+def _cache(cache, device):
+    if not isinstance(cache, KvCache):
+        raise MetisError("cache must be a KvCache")
+    rows, cols = cache.pages * cache.heads * cache.page_size, getattr(cache.k, "cols", 0)
+    _fp4_buffers(cache.k, "the cache's k", rows, cols, device)
+    _fp4_buffers(cache.v, "the cache's v", rows, cols, device, cache.k.fmt)
+    return cache.c()
+
+
+def _batch(batch, device):
+    if not isinstance(batch, KvBatch):
+        raise MetisError("batch must be a KvBatch")
+    t = batch.table
+    ldt = _matrix(t, "table", None, device)
+    if t.dtype != torch.int32:
+        raise MetisError("table must be int32")
+    seqs, pages = t.shape
+    lengths = _vector(batch.lengths, "lengths", seqs, device, torch.int32)
+    if lengths is None:
+        raise MetisError("a batch needs its lengths")
+    starts = _vector(batch.starts, "starts", seqs + 1, device, torch.int32)
+    return _KvBatch(t.data_ptr(), lengths, starts, ldt, seqs, pages)
+
+
+def metis_kv_append(k, v, batch, cache, rope=None, pairs="halves"):
+    """Store the new tokens' keys (turned by their positions' angles where rope
+    is given, see metis_qk_norm_rope_fwd) and values in the cache, quantized as
+    fp4_block_quant does; returns the cache. k, v: tokens x (heads * head_dim)
+    fp32/bf16 CUDA tensors of one type. Tokens outside the batch, its table or
+    the rope are not stored; pages written to belong to one sequence each."""
+    ldk = _matrix(k, "k")
+    dev, dt = k.device, _code(k.dtype)
+    c, b = _cache(cache, dev), _batch(batch, dev)
+    n = cache.heads * cache.head_dim
+    if k.shape[1] != n:
+        raise MetisError("k must have %d columns, got %d" % (n, k.shape[1]))
+    ldv = _matrix(v, "v", k.shape, dev)
+    if v.dtype != k.dtype:
+        raise MetisError("k and v must be of one type")
+    rp, rows, rot = _rope(rope, dev)
+    _run(dev, load().metis_kv_append, k.data_ptr(), ldk, v.data_ptr(), ldv, dt, k.shape[0], b, rp, rows, rot,
+         _pairs(pairs), c)
+    return cache
+
+
+def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=None, need_lse=False):
+    """Attention of the new tokens over the cache: (o, log-sum-exp or None). q:
+    tokens x (heads * head_dim), heads a multiple of the cache's; every query
+    sees the tokens up to its own position, of them the last `window` (0: all).
+    scale: default 1 / sqrt(head_dim). o is of type `dtype` (default: q's).
+    Rows outside the batch keep what `out` holds (a new output: zeros)."""
+    c = _cache(cache, q.device if isinstance(q, torch.Tensor) else None)
+    ldq, heads = _heads(q, "q", cache.head_dim)
+    dev, tokens, dt = q.device, q.shape[0], _code(q.dtype)
+    b = _batch(batch, dev)
+    if heads % cache.heads:
+        raise MetisError("%d query heads over %d heads in the cache" % (heads, cache.heads))
+    dtype = q.dtype if dtype is None else dtype
+    odt = _code(dtype)
+    every = batch.starts is None and tokens == b.seqs  # each row belongs to a sequence
+    if out is None and not every:
+        out = torch.zeros(q.shape, dtype=dtype, device=dev)
+    out, ldo = _out(out, "out", q, dtype, dev)
+    lse = None
+    if need_lse:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+        if not every:
+            lse.fill_(float("-inf"))
+    L = load()
+    longest = max(1, int(batch.max_length) if batch.max_length is not None else b.max_pages * cache.page_size)
+    nws = L.metis_kv_attention_workspace_bytes(tokens, heads, batch.max_new, longest, b, c)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _run(dev, L.metis_kv_attention, q.data_ptr(), dt, tokens, ldq, heads, b, c, batch.max_new, longest,
+         cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), odt, ldo,
+         None if lse is None else lse.data_ptr(), ws.data_ptr() if nws else None, nws)
+    return out, lse

@@ -390,7 +390,7 @@ inline bool apart(const Region &a, const Region &b) {
 // another output: a lane reads up to seven elements of its neighbours, and
 // rows run in any order.
 struct Operands {
-  Region outs[8], ins[8];
+  Region outs[8], ins[16];
   int nout = 0, nin = 0;
   void out(const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
     outs[nout++] = region(p, rows, cols, ld, bytes);
@@ -407,6 +407,12 @@ struct Operands {
     if (!q) return;
     in(q->codes, 1, q->rows * q->cols, 0, 1);
     in(q->scales, 1, q->rows * metis::cdiv(q->cols, metis::kBlock8), 0, 1);
+  }
+  void in(const metis_fp4_t &q) {
+    const int64_t block = q.fmt == METIS_NVFP4 ? 16 : 32;
+    in(q.codes, 1, q.rows * (q.cols / 2), 0, 1);
+    in(q.scales, 1, q.rows * (q.cols / block), 0, 1);
+    if (q.fmt == METIS_NVFP4) in(q.tensor_scale, 1, 1, 0, 4);
   }
   bool distinct() const {
     for (int i = 0; i < nout; ++i) {

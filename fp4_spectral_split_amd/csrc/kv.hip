@@ -1,0 +1,800 @@
+// The paged FP4 cache: new keys (turned by their positions' angles) and values
+// are quantized into it, and attention reads it.
+//
+// Append. A workgroup stores one token, eight elements of a head in a lane;
+// four lanes (MXFP4) or two (NVFP4) hold a block, so its largest magnitude
+// takes two DPP steps or one. HBM bound: reads k and v once. The rotation is
+// formed in fp64 (its products are exact there) and rounded once to fp32, so
+// that the codes do not depend on how the sum was formed; the arithmetic
+// hides behind the loads.
+//
+// Attention over the cache, for the query row q of a head:
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp2(s_t - max s),  s_t = q . k_t scale log2(e)
+// Bound by reading the codes of k and v once. One pass over the tokens with a
+// running maximum, the tokens divided over workgroups (joined by a second
+// launch) and over the four waves of each (joined in LDS). Sixteen query rows
+// (the query heads of one key head, for each new token) share a pass. Per 32
+// tokens of a wave:
+//  - S^T = K Q^T on 16x16x32 products: a lane decodes a quarter of one token's
+//    key. The sum over d may run in any order, so the lanes' elements are used
+//    as they lie (one load of up to 16 bytes for 128 elements of the head).
+//  - A lane then holds the scores of one query row for eight tokens, which is
+//    what the second product wants of it: p needs no exchange between lanes.
+//  - O^T = V^T P^T: v is decoded to bf16 into LDS, one token to a row, and read
+//    back transposed (ds_read_b64_tr_b16). Rows are 32 bytes longer than a head,
+//    so the eight rows that half a wave reads at once lie in different banks.
+//    Row statistics and the rescaling of O then belong to one lane's own row.
+// The next 32 tokens' codes are under way while these are worked on, and the
+// table entries of the 32 after them.
+#include <algorithm>
+
+#include "decode4.hpp"
+
+using namespace metis;
+using namespace metis_host;
+
+namespace {
+
+constexpr int kMaxDim = 256;
+constexpr int64_t kMaxTokens = (int64_t)1 << 29;  // max_pages * page_size
+
+struct Batch {
+  const int32_t *table, *lengths, *starts;
+  int64_t ldt;
+  int seqs, max_pages;
+};
+struct Pages {
+  int pages, page_size, heads;
+  FastDiv by_page;
+};
+
+// ----------------------------------------------------------------- append
+struct AppendArgs {
+  const void *x[2];  // k, v
+  int64_t ldx[2];
+  Batch b;
+  Pages p;
+  const float *rope;
+  int64_t rope_rows;
+  int rot, neighbours;
+  int64_t tokens;
+  uint8_t *codes[2], *scales[2];
+  const float *whole[2];
+  int dim;
+  int64_t first;  // row of this launch's first workgroup
+};
+
+// The sequence that row t belongs to, -1 if to none.
+__device__ __forceinline__ int sequence_of(const Batch &b, int64_t t) {
+  if (!b.starts) return t < b.seqs ? (int)t : -1;
+  int lo = 0, hi = b.seqs;  // the first s with starts[s + 1] > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (b.starts[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo < b.seqs && b.starts[lo] <= t ? lo : -1;
+}
+
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+  Raw<T> r;
+  load_all(p, r);
+  to_f32(r, v);
+}
+
+// Elements d .. d + 7 of a key turned by the angles of its position.
+template <typename T>
+__device__ __forceinline__ void turned(const AppendArgs &g, const T *head, int d, int64_t position, float (&v)[8]) {
+  const int half = g.rot / 2;
+  const float *cs = g.rope + position * g.rot, *sn = cs + half;
+  if (g.neighbours) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if (d + i < g.rot) {
+        const double c = cs[(d + i) / 2], s = sn[(d + i) / 2], a = v[i], b = v[i + 1];
+        v[i] = (float)(a * c - b * s);
+        v[i + 1] = (float)(b * c + a * s);
+      }
+    }
+  } else if (half % 8 == 0) {  // the chunk's partners are a chunk too
+    if (d < g.rot) {
+      const bool first = d < half;
+      const int at = first ? d : d - half;
+      float o[8], c[8], s[8];
+      load8(head + (first ? d + half : at), o);
+      load8(cs + at, c);
+      load8(sn + at, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double t = (double)o[i] * s[i];
+        v[i] = (float)((double)v[i] * c[i] + (first ? -t : t));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = d + i;
+      if (e < g.rot) {
+        const bool first = e < half;
+        const int at = first ? e : e - half;
+        const double t = (double)load_f32(head + (first ? e + half : at)) * sn[at];
+        v[i] = (float)((double)v[i] * cs[at] + (first ? -t : t));
+      }
+    }
+  }
+}
+
+template <typename T, bool NV> __global__ void __launch_bounds__(256) append_kernel(AppendArgs g) {
+  const int64_t t = g.first + blockIdx.x;
+  const int seq = sequence_of(g.b, t);
+  if (seq < 0) return;  // the same for the whole workgroup, as are the ways out below
+  const int64_t end = g.b.starts ? g.b.starts[seq + 1] : t + 1;
+  if (end > g.tokens || (g.b.starts && g.b.starts[seq] < 0)) return;
+  const int64_t position = g.b.lengths[seq] - (end - t);
+  if (position < 0 || position >= (int64_t)g.b.max_pages * g.p.page_size) return;
+  if (g.rot && position >= g.rope_rows) return;
+  const uint32_t at = g.p.by_page.div((uint32_t)position);
+  const int page = g.b.table[seq * g.b.ldt + at];
+  if (page < 0 || page >= g.p.pages) return;
+  const int place = (int)((uint32_t)position - at * g.p.by_page.d);
+  const int per_head = g.dim / 8, per_side = g.p.heads * per_head;
+  for (int u = threadIdx.x; u < 2 * per_side; u += blockDim.x) {  // whole quads: per_head is a multiple of four
+    const int side = u >= per_side, w = side ? u - per_side : u;
+    const int head = w / per_head, d = (w - head * per_head) * 8;
+    const T *x = (const T *)(side ? g.x[1] : g.x[0]) + t * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.dim;
+    float v[8];
+    load8(x + d, v);
+    if (!side && g.rot) turned(g, x, d, position, v);
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+    uint32_t m = __float_as_uint(top);  // not negative: ordered like its bits
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));            // lanes 1 0 3 2
+    if (!NV) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+    top = __uint_as_float(m);
+    uint32_t code, byte;
+    if (NV) {
+      const float whole = *(side ? g.whole[1] : g.whole[0]);
+      byte = e4m3_rne_sat(__fdiv_rn(top, 6.0f * whole));
+      const float by = e4m3_value(byte) * whole;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = byte ? __fdiv_rn(v[i], by) : v[i] * 0.0f;
+      code = e2m1_pack8(v);
+    } else {
+      const int e = mx_shared_exponent(top);
+      byte = (uint32_t)(e + 127);
+      uint32_t packed[1];
+      e2m1_pack_scaled<8>(v, pow2_f32(e), packed);
+      code = packed[0];
+    }
+    const int64_t row = ((int64_t)page * g.p.heads + head) * g.p.page_size + place;
+    *(uint32_t *)((side ? g.codes[1] : g.codes[0]) + row * (g.dim / 2) + d / 2) = code;
+    if (d % kBlock4<NV> == 0) (side ? g.scales[1] : g.scales[0])[row * (g.dim / kBlock4<NV>) + d / kBlock4<NV>] = (uint8_t)byte;
+  }
+}
+
+// -------------------------------------------------------------- attention
+constexpr int kWaves = 4;
+constexpr int kTile = 32;  // tokens of a wave's step
+constexpr int kStepTokens = kWaves * kTile;
+constexpr int kRowsQ = 16;
+
+struct AttendArgs {
+  const void *q;
+  int64_t ldq;
+  Batch b;
+  Pages p;
+  const uint8_t *kc, *ks, *vc, *vs;
+  const float *k_whole, *v_whole;
+  int64_t tokens;
+  int heads, group;  // query heads, and of them for each head of the cache
+  FastDiv by_group;
+  int tiles, splits, chunk;  // chunk: least tokens of a workgroup, a multiple of kStepTokens
+  int max_new;
+  float scale;               // times log2(e)
+  int64_t window;
+  void *o;
+  int64_t ldo;
+  int o_bf16;
+  float *lse;
+  float *part;   // splits x tokens x heads x dim
+  float2 *stat;  // splits x tokens x heads: (maximum, sum)
+};
+
+constexpr float kLn2 = 0.693147181f;
+constexpr uint32_t kNoRow = 0xFFFFFFFFu, kBadRow = 0xFFFFFFFEu;
+
+__device__ __forceinline__ float nan_f32() { return __uint_as_float(0x7FC00000u); }
+
+// N words at a 4-byte aligned address, in loads as wide as they go.
+template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+  typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+  if constexpr (N >= 4) {
+    const u32x4_a4 v = *(const u32x4_a4 *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+    if constexpr (N > 4) load_words<N - 4>(p + 16, w + 4);
+  } else if constexpr (N >= 2) {
+    const u32x2_a4 v = *(const u32x2_a4 *)p;
+    w[0] = v[0];
+    w[1] = v[1];
+    if constexpr (N > 2) w[2] = *(const uint32_t *)(p + 8);
+  } else {
+    w[0] = *(const uint32_t *)p;
+  }
+}
+
+// NC: head size / 32. PQ, PP: bf16 parts of q and of the weights.
+template <bool NV, int NC, int PQ, int PP, typename TQ>
+__global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
+  constexpr int D = 32 * NC;
+  constexpr int kUnitsPerScale = NV ? 2 : 4;                      // units of eight elements under one scale
+  constexpr bool kEven = NC % kUnitsPerScale == 0 || kUnitsPerScale % NC == 0;  // a lane's key units fill whole scales, or share one
+  constexpr int kKeyScales = NC % kUnitsPerScale == 0 ? NC / kUnitsPerScale : (kUnitsPerScale % NC == 0 ? 1 : NC);
+  constexpr int kV = (NC + 1) / 2;                                // 32-element pieces of values in a lane
+  constexpr int kStride = D + 16;                                 // bf16 elements of a row of v in LDS
+  constexpr int kVBytes = kTile * kStride * 2;
+  constexpr int kOStride = D + 4;
+  static_assert(kRowsQ * kOStride * 4 + kRowsQ * 8 <= kVBytes, "the join fits where v was");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kVBytes];
+
+  const int lane = threadIdx.x & 63, r = lane & 15, gq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t id = blockIdx.x;
+  const int split = id % g.splits;
+  id /= g.splits;
+  const int tile = id % g.tiles;
+  id /= g.tiles;
+  const int kvh = id % g.p.heads, seq = id / g.p.heads;
+
+  const int64_t start = g.b.starts ? g.b.starts[seq] : seq, stop = g.b.starts ? g.b.starts[seq + 1] : seq + 1;
+  if (start < 0 || stop > g.tokens || start >= stop) return;
+  const int new_tokens = (int)(stop - start), count = min(new_tokens, g.max_new);
+  if (tile * kRowsQ >= count * (int64_t)g.group) return;
+  const int64_t length = max(g.b.lengths[seq], 0);
+  // this lane's query row
+  const int at = tile * kRowsQ + r;
+  const int j = (int)g.by_group.div((uint32_t)at), h = kvh * g.group + at - j * g.group;
+  const bool row_there = j < count;
+  const int64_t row = start + j;
+  const int64_t capacity = (int64_t)g.b.max_pages * g.p.page_size;
+  const bool beyond = length > capacity;
+  const int64_t end_row = row_there ? max((int64_t)0, length - new_tokens + j + 1) : 0;  // tokens below it are seen
+  const int64_t end = beyond ? 0 : end_row;
+  const int64_t begin = g.window > 0 ? max((int64_t)0, end - g.window) : 0;
+  // tokens that any row of the tile sees
+  const int j0 = (int)g.by_group.div((uint32_t)(tile * kRowsQ));
+  const int j1 = min(count - 1, (int)g.by_group.div((uint32_t)(tile * kRowsQ + kRowsQ - 1)));
+  int64_t hi = beyond ? 0 : max((int64_t)0, length - new_tokens + j1 + 1);
+  int64_t lo = g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0;
+  lo = lo / kTile * kTile;
+  // all of it, whatever the length that the launch was made for
+  const int64_t each = (hi - lo + g.splits - 1) / g.splits;
+  const int64_t chunk = max((int64_t)g.chunk, (each + kStepTokens - 1) / kStepTokens * kStepTokens);
+  const int64_t from = lo + split * chunk, to = min(hi, from + chunk);
+  if (g.splits > 1 && from >= to) {  // nothing here; the join skips (-inf, 0)
+    if (threadIdx.x < kRowsQ && row_there)
+      g.stat[((int64_t)split * g.tokens + row) * g.heads + h] = make_float2(-INFINITY, beyond && end_row > 0 ? nan_f32() : 0.0f);
+    return;
+  }
+
+  floatx4 o[2 * NC];
+#pragma unroll
+  for (int i = 0; i < 2 * NC; ++i) o[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  float top = -INFINITY, sum = 0.0f;  // sum: this lane's tokens only
+
+  if (from < to) {
+    // q: element 8 i of this lane's quarter of the head, as B operands
+    ushortx8 qf[NC][PQ];
+    {
+      const TQ *p = (const TQ *)g.q + row * g.ldq + (int64_t)h * D + gq * (D / 4);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (row_there) load8(p + 8 * i, v);
+        parts_bf16<PQ>(v, qf[i]);
+      }
+    }
+    const float scale = NV ? g.scale * *g.k_whole : g.scale;
+    uint8_t *mine = lds + wave * kVBytes;
+    const int32_t *table = g.b.table + seq * g.b.ldt;
+
+    // row of the cache of token (tile base + lane % 32)
+    auto row_of = [&](int64_t base) -> uint32_t {
+      const int64_t t = base + (lane & 31);
+      if (t >= to) return kNoRow;
+      const uint32_t pg = g.p.by_page.div((uint32_t)t);
+      const int page = table[pg];
+      if (page < 0 || page >= g.p.pages) return kBadRow;
+      return ((uint32_t)page * g.p.heads + kvh) * g.p.page_size + ((uint32_t)t - pg * g.p.by_page.d);
+    };
+    struct Tile {
+      uint32_t k[2][NC], ks[2][kKeyScales];
+      uint32_t v[kV][4], vs[kV];
+      uint32_t row;
+    };
+    auto load = [&](uint32_t row32, Tile &t) {
+      t.row = row32;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t kr = __shfl(row32, 16 * s + r, 64);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) t.k[s][i] = 0u;
+#pragma unroll
+        for (int i = 0; i < kKeyScales; ++i) t.ks[s][i] = 0u;
+        if (kr < kBadRow) {
+          load_words<NC>(g.kc + (int64_t)kr * (D / 2) + gq * (D / 8), t.k[s]);
+          const uint8_t *p = g.ks + (int64_t)kr * (D / kBlock4<NV>);
+#pragma unroll
+          for (int i = 0; i < kKeyScales; ++i)
+            t.ks[s][i] = p[kKeyScales == NC ? (gq * NC + i) / kUnitsPerScale
+                                            : (NC % kUnitsPerScale == 0 ? gq * kKeyScales + i : gq * NC / kUnitsPerScale)];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        const int piece = lane + 64 * x, token = piece / NC, c = piece - token * NC;
+        const uint32_t vr = __shfl(row32, token & 31, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.v[x][i] = 0u;
+        t.vs[x] = 0u;
+        if (piece < kTile * NC && vr < kBadRow) {
+          load_words<4>(g.vc + (int64_t)vr * (D / 2) + 16 * c, t.v[x]);
+          const uint8_t *p = g.vs + (int64_t)vr * (D / kBlock4<NV>);
+          t.vs[x] = NV ? (uint32_t)p[2 * c] | (uint32_t)p[2 * c + 1] << 8 : p[c];
+        }
+      }
+    };
+
+    auto compute = [&](const Tile &t, int64_t base) {
+      // v to LDS as bf16
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        const int piece = lane + 64 * x, token = piece / NC, c = piece - token * NC;
+        if (piece < kTile * NC) {
+          const float s0 = scale4<NV>(t.vs[x] & 255u), s1 = NV ? scale4<NV>(t.vs[x] >> 8) : s0;
+          ushortx8 *dst = (ushortx8 *)(mine + token * (kStride * 2) + c * 64);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = decode4<NV>(t.v[x][i], i < 2 ? s0 : s1);
+        }
+      }
+      // scores of this lane's row for tokens base + 16 s + 4 gq + i
+      float p[8];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int k = kKeyScales == NC ? i : (NC % kUnitsPerScale == 0 ? i / kUnitsPerScale : 0);
+          const ushortx8 a = decode4<NV>(t.k[s][i], scale4<NV>(t.ks[s][k]));
+#pragma unroll
+          for (int part = PQ - 1; part >= 0; --part) acc = mfma16_bf16(a, qf[i][part], acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[4 * s + i] = acc[i] * scale;
+      }
+      if (base < begin || base + kTile > end) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t token = base + 16 * (i / 4) + 4 * gq + i % 4;
+          p[i] = token >= begin && token < end ? p[i] : -INFINITY;
+        }
+      }
+      if (__ballot(t.row == kBadRow)) {  // a page outside the cache: its tokens have no scores
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t there = __shfl(t.row, 16 * (i / 4) + 4 * gq + i % 4, 64);
+          p[i] = there == kBadRow && p[i] != -INFINITY ? nan_f32() : p[i];
+        }
+      }
+      float m = p[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, p[i]);
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      m = fmaxf(m, top);
+      if (__ballot(m != top)) {
+        // nothing seen before: O is zero, and exp2(-inf) leaves it so
+        const float by = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+        top = m;
+        sum *= by;
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) o[i] *= by;
+      }
+      const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
+        sum += p[i];
+      }
+      ushortx8 pf[PP];
+      parts_bf16<PP>(p, pf);
+      // the wave's own LDS rows: its writes are done before its reads
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int i = 0; i < 2 * NC; ++i) {
+        typedef short shortx4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) shortx4 *lds_ptr;
+        const uint8_t *src = mine + (4 * gq + r / 4) * (kStride * 2) + 32 * i + 8 * (r & 3);
+        const shortx4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)src);
+        const shortx4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(src + 16 * (kStride * 2)));
+        ushortx8 a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[e] = (unsigned short)a0[e];
+          a[4 + e] = (unsigned short)a1[e];
+        }
+#pragma unroll
+        for (int part = PP - 1; part >= 0; --part) o[i] = mfma16_bf16(a, pf[part], o[i]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+
+    constexpr int64_t kNext = kStepTokens;
+    int64_t base = from + (int64_t)wave * kTile;
+    if (base < to) {
+      Tile cur, next;
+      load(row_of(base), cur);
+      uint32_t ahead = row_of(base + kNext);
+      for (; base < to; base += kNext) {
+        load(ahead, next);
+        ahead = row_of(base + 2 * kNext);
+        compute(cur, base);
+        cur = next;
+      }
+    }
+  }
+
+  // ---- join the waves
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
+  __syncthreads();
+  float *mo = (float *)(lds + wave * kVBytes);
+  float2 *ms = (float2 *)(lds + wave * kVBytes + kRowsQ * kOStride * 4);
+#pragma unroll
+  for (int i = 0; i < 2 * NC; ++i) *(floatx4 *)(mo + r * kOStride + 16 * i + 4 * gq) = o[i];
+  if (gq == 0) ms[r] = make_float2(top, sum);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kRowsQ * (D / 4); e += 64 * kWaves) {
+    const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
+    const int at2 = tile * kRowsQ + rr;
+    const int j2 = (int)g.by_group.div((uint32_t)at2), h2 = kvh * g.group + at2 - j2 * g.group;
+    if (j2 >= count) continue;
+    float m = -INFINITY, l = 0.0f;
+    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    float mw[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      mw[w] = ((const float2 *)(lds + w * kVBytes + kRowsQ * kOStride * 4))[rr].x;
+      m = fmaxf(m, mw[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float by = mw[w] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw[w] - m);
+      // a wave that saw nothing has zeros, unless a score was NaN
+      l += ((const float2 *)(lds + w * kVBytes + kRowsQ * kOStride * 4))[rr].y * (mw[w] == -INFINITY ? 1.0f : by);
+      v += *(const floatx4 *)((const float *)(lds + w * kVBytes) + rr * kOStride + d) * (mw[w] == -INFINITY ? 1.0f : by);
+    }
+    const int64_t orow = start + j2;
+    // a length that the table does not hold
+    if (beyond && length - new_tokens + j2 + 1 > 0) l = nan_f32();
+    if (g.splits > 1) {
+      const int64_t slot = ((int64_t)split * g.tokens + orow) * g.heads + h2;
+      *(floatx4 *)(g.part + slot * D + d) = v;
+      if (d == 0) g.stat[slot] = make_float2(m, l);
+    } else {
+      const float w = NV ? *g.v_whole : 1.0f;
+      const float inv = l == 0.0f ? 0.0f : w / l;
+      const int64_t out = orow * g.ldo + (int64_t)h2 * D + d;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (g.o_bf16) ((unsigned short *)g.o)[out + i] = (unsigned short)pack_bf16(v[i] * inv, 0.0f);
+        else ((float *)g.o)[out + i] = v[i] * inv;
+      }
+      if (g.lse && d == 0) g.lse[orow * g.heads + h2] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    }
+  }
+}
+
+// The splits of a row and head joined, in order: one workgroup for each.
+struct JoinArgs {
+  Batch b;
+  int64_t tokens;
+  int heads, dim, splits, max_new;
+  const float *part;
+  const float2 *stat;
+  const float *v_whole;
+  void *o;
+  int64_t ldo;
+  int o_bf16;
+  float *lse;
+};
+__global__ void __launch_bounds__(256) join_kernel(JoinArgs g) {
+  const int h = blockIdx.x % g.heads;
+  const int64_t row = blockIdx.x / g.heads;
+  const int seq = sequence_of(g.b, row);
+  if (seq < 0) return;
+  const int64_t start = g.b.starts ? g.b.starts[seq] : row, stop = g.b.starts ? g.b.starts[seq + 1] : row + 1;
+  if (start < 0 || stop > g.tokens || row - start >= g.max_new) return;
+  float m = -INFINITY;
+  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.stat[((int64_t)s * g.tokens + row) * g.heads + h].x);
+  float l = 0.0f;
+  for (int d = threadIdx.x; d < g.dim; d += blockDim.x) {
+    float v = 0.0f;
+    l = 0.0f;
+    for (int s = 0; s < g.splits; ++s) {
+      const int64_t slot = ((int64_t)s * g.tokens + row) * g.heads + h;
+      const float2 st = g.stat[slot];
+      if (st.x == -INFINITY && st.y == 0.0f) continue;  // nothing seen, and nothing written
+      const float by = st.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.x - m);
+      l += st.y * by;
+      v += g.part[slot * g.dim + d] * by;
+    }
+    const float w = g.v_whole ? *g.v_whole : 1.0f;
+    const float y = l == 0.0f ? 0.0f : v * (w / l);
+    const int64_t out = row * g.ldo + (int64_t)h * g.dim + d;
+    if (g.o_bf16) ((unsigned short *)g.o)[out] = (unsigned short)pack_bf16(y, 0.0f);
+    else ((float *)g.o)[out] = y;
+  }
+  if (g.lse && threadIdx.x == 0) g.lse[row * g.heads + h] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+}
+
+// ------------------------------------------------------------------- host
+metis_status_t check_cache(const metis_kv_cache_t *c, const metis_kv_batch_t *b, bool present) {
+  if (!c || !b || c->pages < 0 || c->page_size < 1 || c->heads < 1 || b->seqs < 0 || b->max_pages < 0) return METIS_ERR_INVALID;
+  if (b->seqs && b->ldt < b->max_pages) return METIS_ERR_INVALID;
+  const metis_fp4_t &k = c->k, &v = c->v;
+  if (k.fmt != METIS_MXFP4 && k.fmt != METIS_NVFP4) return METIS_ERR_INVALID;
+  if (v.fmt != k.fmt || v.cols != k.cols || k.cols < 1 || k.rows != v.rows) return METIS_ERR_INVALID;
+  if (c->pages > kMaxRows || c->heads > kMaxRows || c->page_size > kMaxTokens) return METIS_ERR_UNSUPPORTED;
+  // one factor after the other: each product stays below 2^62
+  const int64_t page_rows = (int64_t)c->heads * c->page_size;
+  if (page_rows > kMaxRows || c->pages * page_rows > kMaxRows) return METIS_ERR_UNSUPPORTED;
+  if (k.rows != c->pages * page_rows) return METIS_ERR_INVALID;
+  if (k.cols % 32 || k.cols > kMaxDim || (int64_t)b->max_pages * c->page_size > kMaxTokens) return METIS_ERR_UNSUPPORTED;
+  if (!present) return METIS_OK;
+  for (const metis_fp4_t *q : {&k, &v}) {
+    if (q->rows && (!q->codes || !q->scales || ((uintptr_t)q->codes & 3))) return METIS_ERR_INVALID;
+    if (k.fmt == METIS_NVFP4 && (!q->tensor_scale || ((uintptr_t)q->tensor_scale & 3))) return METIS_ERR_INVALID;
+  }
+  if (b->seqs && (!b->lengths || ((uintptr_t)b->lengths & 3) || ((uintptr_t)b->starts & 3))) return METIS_ERR_INVALID;
+  if (b->seqs && b->max_pages && (!b->table || ((uintptr_t)b->table & 3))) return METIS_ERR_INVALID;
+  return METIS_OK;
+}
+
+Batch batch_of(const metis_kv_batch_t *b) {
+  return {b->table, b->lengths, b->starts, b->ldt, b->seqs, b->max_pages};
+}
+Pages pages_of(const metis_kv_cache_t *c) {
+  Pages p = {};
+  p.pages = (int)c->pages;
+  p.page_size = c->page_size;
+  p.heads = c->heads;
+  p.by_page.set((uint32_t)c->page_size);
+  return p;
+}
+void batch_in(Operands &o, const metis_kv_batch_t *b) {
+  o.in(b->max_pages ? b->table : nullptr, b->seqs, b->max_pages, b->ldt, 4);
+  o.in(b->lengths, 1, b->seqs, 0, 4);
+  o.in(b->starts, 1, (int64_t)b->seqs + 1, 0, 4);
+}
+
+// Tokens of a workgroup: as many as leave `kTarget` workgroups, had every
+// sequence the largest length, in whole steps of its waves.
+constexpr int kTarget = 4096, kMaxSplits = 256;
+struct Splits {
+  int splits, chunk;
+};
+Splits splits_of(int64_t work_rows, int64_t max_length) {
+  const int64_t steps = std::max<int64_t>(1, cdiv(max_length, kStepTokens));
+  int64_t per = cdiv(steps * work_rows, kTarget);          // steps of a workgroup
+  per = std::max(per, cdiv(steps, kMaxSplits));
+  per = std::max<int64_t>(1, std::min(per, steps));
+  return {(int)cdiv(steps, per), (int)(per * kStepTokens)};
+}
+
+struct AttendPlan {
+  int tiles;
+  Splits s;
+  float *part;
+  float2 *stat;
+  size_t bytes;
+};
+AttendPlan plan_of(void *ws, int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
+                   const metis_kv_batch_t *b, const metis_kv_cache_t *c) {
+  AttendPlan p = {};
+  const int64_t capacity = (int64_t)b->max_pages * c->page_size;  // longer sequences are not worked on
+  p.tiles = (int)cdiv((int64_t)std::min<int64_t>(max_new, std::max<int64_t>(tokens, 1)) * (heads / c->heads), kRowsQ);
+  p.s = splits_of((int64_t)b->seqs * c->heads * p.tiles, std::max<int64_t>(1, std::min(max_length, capacity)));
+  Carver ws_c(ws);
+  if (p.s.splits > 1) {
+    const size_t n = (size_t)p.s.splits * (size_t)tokens * (size_t)heads;
+    p.part = ws_c.take<float>(n * (size_t)c->k.cols);
+    p.stat = ws_c.take<float2>(n);
+  }
+  p.bytes = ws_c.bytes();
+  return p;
+}
+
+template <bool NV, int PQ, int PP, typename TQ> bool attend_by_dim(const AttendArgs &g, int dim, unsigned grid, hipStream_t stream) {
+#define METIS_CASE(NC)                                                                  \
+  case NC: attend_kernel<NV, NC, PQ, PP, TQ><<<grid, 64 * kWaves, 0, stream>>>(g); return true;
+  switch (dim / 32) {
+    METIS_CASE(1) METIS_CASE(2) METIS_CASE(3) METIS_CASE(4) METIS_CASE(5) METIS_CASE(6) METIS_CASE(7) METIS_CASE(8)
+  }
+#undef METIS_CASE
+  return false;
+}
+
+metis_status_t check_attention(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
+                               const metis_kv_batch_t *b, const metis_kv_cache_t *c, bool present) {
+  const metis_status_t ok = check_cache(c, b, present);
+  if (ok != METIS_OK) return ok;
+  if (tokens < 0 || heads < 1 || heads % c->heads || max_new < 1 || max_length < 1) return METIS_ERR_INVALID;
+  if (!b->starts && max_new != 1) return METIS_ERR_INVALID;
+  if (tokens > kMaxRows || tokens * heads >= (int64_t)1 << 24) return METIS_ERR_UNSUPPORTED;  // workgroups of the join
+  return METIS_OK;
+}
+
+}  // namespace
+
+extern "C" metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, metis_dtype_t dt,
+                                          int64_t tokens, const metis_kv_batch_t *batch, const float *rope,
+                                          int64_t rope_rows, int32_t rot_dim, metis_rope_t pairs,
+                                          const metis_kv_cache_t *cache, hipStream_t stream) {
+  const metis_status_t ok = check_cache(cache, batch, tokens > 0);
+  if (ok != METIS_OK) return ok;
+  if (tokens < 0 || !dtype_ok(dt) || rope_rows < 0 || rot_dim < 0 || rot_dim % 2 || rot_dim > cache->k.cols)
+    return METIS_ERR_INVALID;
+  if (pairs != METIS_ROPE_HALVES && pairs != METIS_ROPE_NEIGHBOURS) return METIS_ERR_INVALID;
+  if (rot_dim && ((!rope && rope_rows) || ((uintptr_t)rope & 3))) return METIS_ERR_INVALID;
+  const int64_t n = cache->heads * cache->k.cols;
+  if (ldk < n || ldv < n) return METIS_ERR_INVALID;
+  if (tokens > kMaxRows) return METIS_ERR_UNSUPPORTED;
+  if (tokens == 0 || batch->seqs == 0 || cache->pages == 0 || batch->max_pages == 0) return METIS_OK;
+  if (!dense_ok(k, dt, n, ldk) || !dense_ok(v, dt, n, ldv)) return METIS_ERR_INVALID;
+  const bool nv = cache->k.fmt == METIS_NVFP4;
+  Operands o;
+  const int64_t rows = cache->k.rows, block = nv ? 16 : 32;
+  for (const metis_fp4_t *q : {&cache->k, &cache->v}) {
+    o.out(q->codes, 1, rows * (q->cols / 2), 0, 1);
+    o.out(q->scales, 1, rows * (q->cols / block), 0, 1);
+    if (nv) o.in(q->tensor_scale, 1, 1, 0, 4);
+  }
+  o.in(k, tokens, n, ldk, elem_bytes(dt));
+  o.in(v, tokens, n, ldv, elem_bytes(dt));
+  if (rot_dim) o.in(rope, 1, rope_rows * rot_dim, 0, 4);
+  batch_in(o, batch);
+  if (!o.distinct()) return METIS_ERR_INVALID;
+  AppendArgs g = {};
+  g.x[0] = k;
+  g.x[1] = v;
+  g.ldx[0] = ldk;
+  g.ldx[1] = ldv;
+  g.b = batch_of(batch);
+  g.p = pages_of(cache);
+  g.rope = rope;
+  g.rope_rows = rope_rows;
+  g.rot = rot_dim;
+  g.neighbours = pairs == METIS_ROPE_NEIGHBOURS;
+  g.tokens = tokens;
+  g.codes[0] = cache->k.codes;
+  g.codes[1] = cache->v.codes;
+  g.scales[0] = cache->k.scales;
+  g.scales[1] = cache->v.scales;
+  g.whole[0] = cache->k.tensor_scale;
+  g.whole[1] = cache->v.tensor_scale;
+  g.dim = (int)cache->k.cols;
+  const int64_t lanes = 2 * n / 8;
+  const unsigned threads = (unsigned)std::min<int64_t>(256, round_up(lanes, 64));
+  constexpr int64_t kSlab = 1 << 23;  // workgroups of a launch: below 2^32 threads
+  for (int64_t t0 = 0; t0 < tokens; t0 += kSlab) {
+    g.first = t0;
+    const unsigned grid = (unsigned)std::min(kSlab, tokens - t0);
+    if (dt == METIS_F32) {
+      if (nv) append_kernel<float, true><<<grid, threads, 0, stream>>>(g);
+      else append_kernel<float, false><<<grid, threads, 0, stream>>>(g);
+    } else {
+      if (nv) append_kernel<unsigned short, true><<<grid, threads, 0, stream>>>(g);
+      else append_kernel<unsigned short, false><<<grid, threads, 0, stream>>>(g);
+    }
+  }
+  METIS_LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+extern "C" size_t metis_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
+                                                     const metis_kv_batch_t *batch, const metis_kv_cache_t *cache) {
+  if (check_attention(tokens, heads, max_new, max_length, batch, cache, false) != METIS_OK || tokens == 0) return 0;
+  return plan_of(nullptr, tokens, heads, max_new, max_length, batch, cache).bytes;
+}
+
+extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, int64_t tokens, int64_t ldq,
+                                             int32_t heads, const metis_kv_batch_t *batch,
+                                             const metis_kv_cache_t *cache, int32_t max_new, int64_t max_length,
+                                             float scale, int64_t window, void *o, metis_dtype_t odt, int64_t ldo,
+                                             float *lse, void *ws, size_t ws_bytes, hipStream_t stream) {
+  const metis_status_t ok = check_attention(tokens, heads, max_new, max_length, batch, cache, tokens > 0);
+  if (ok != METIS_OK) return ok;
+  if (!dtype_ok(dt) || !dtype_ok(odt) || window < 0 || !(scale - scale == 0.0f)) return METIS_ERR_INVALID;
+  const int64_t n = heads * cache->k.cols;
+  if (ldq < n || ldo < n || ((uintptr_t)lse & 3)) return METIS_ERR_INVALID;
+  if (tokens == 0 || batch->seqs == 0) return METIS_OK;
+  if (!dense_ok(q, dt, n, ldq) || !dense_ok(o, odt, n, ldo)) return METIS_ERR_INVALID;
+  const AttendPlan p = plan_of(ws, tokens, heads, max_new, max_length, batch, cache);
+  if (p.bytes && (!ws || ws_bytes < p.bytes)) return METIS_ERR_WORKSPACE;
+  if (p.bytes && ((uintptr_t)ws & 255)) return METIS_ERR_INVALID;
+  if ((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits >= (int64_t)1 << 24) return METIS_ERR_UNSUPPORTED;
+  Operands all;
+  all.out(o, tokens, n, ldo, elem_bytes(odt));
+  all.out(lse, 1, tokens * heads, 0, 4);
+  if (p.bytes) all.out(ws, 1, (int64_t)p.bytes, 0, 1);
+  all.in(q, tokens, n, ldq, elem_bytes(dt));
+  all.in(cache->k);
+  all.in(cache->v);
+  batch_in(all, batch);
+  if (!all.distinct()) return METIS_ERR_INVALID;
+  const bool nv = cache->k.fmt == METIS_NVFP4;
+  AttendArgs g = {};
+  g.q = q;
+  g.ldq = ldq;
+  g.b = batch_of(batch);
+  g.p = pages_of(cache);
+  g.kc = cache->k.codes;
+  g.ks = cache->k.scales;
+  g.vc = cache->v.codes;
+  g.vs = cache->v.scales;
+  g.k_whole = cache->k.tensor_scale;
+  g.v_whole = cache->v.tensor_scale;
+  g.tokens = tokens;
+  g.heads = heads;
+  g.group = heads / cache->heads;
+  g.by_group.set((uint32_t)g.group);
+  g.tiles = p.tiles;
+  g.splits = p.s.splits;
+  g.chunk = p.s.chunk;
+  g.max_new = max_new;
+  g.scale = scale * 1.44269504f;
+  g.window = window;
+  g.o = o;
+  g.ldo = ldo;
+  g.o_bf16 = odt == METIS_BF16;
+  g.lse = lse;
+  g.part = p.part;
+  g.stat = p.stat;
+  const unsigned grid = (unsigned)((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits);
+  const int dim = (int)cache->k.cols;
+  if (dt == METIS_BF16 && odt == METIS_BF16) {
+    nv ? attend_by_dim<true, 1, 2, unsigned short>(g, dim, grid, stream)
+       : attend_by_dim<false, 1, 2, unsigned short>(g, dim, grid, stream);
+  } else if (dt == METIS_BF16) {
+    nv ? attend_by_dim<true, 1, 3, unsigned short>(g, dim, grid, stream)
+       : attend_by_dim<false, 1, 3, unsigned short>(g, dim, grid, stream);
+  } else {
+    nv ? attend_by_dim<true, 3, 3, float>(g, dim, grid, stream) : attend_by_dim<false, 3, 3, float>(g, dim, grid, stream);
+  }
+  if (p.s.splits > 1) {
+    JoinArgs jn = {};
+    jn.b = g.b;
+    jn.tokens = tokens;
+    jn.heads = heads;
+    jn.dim = dim;
+    jn.splits = p.s.splits;
+    jn.max_new = max_new;
+    jn.part = p.part;
+    jn.stat = p.stat;
+    jn.v_whole = nv ? g.v_whole : nullptr;
+    jn.o = o;
+    jn.ldo = ldo;
+    jn.o_bf16 = g.o_bf16;
+    jn.lse = lse;
+    join_kernel<<<(unsigned)(tokens * heads), dim > 64 ? (dim > 128 ? 256 : 128) : 64, 0, stream>>>(jn);
+  }
+  METIS_LAUNCH_CHECK();
+  return METIS_OK;
+}

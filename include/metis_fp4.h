@@ -374,7 +374,11 @@ metis_status_t act8_block_dequant(const metis_act8_t *in, void *y, metis_dtype_t
  * that number gives NaN). At the other end, squares below 1e-38 lose bits,
  * which shows where eps is no larger; with eps = 0 a row whose squares are all
  * 0 has rstd = infinity and y = NaN. */
-typedef enum { METIS_NORM_LAYER = 0, METIS_NORM_RMS = 1 } metis_norm_t;
+typedef enum {
+  METIS_NORM_LAYER = 0,
+  METIS_NORM_RMS = 1,
+  METIS_NORM_NONE = 2 /* metis_qk_norm_rope_* only */
+} metis_norm_t;
 metis_status_t metis_norm_fwd(const void *x, metis_dtype_t dt, int64_t rows, int64_t cols, int64_t ldx, const void *w,
                               const void *b, metis_dtype_t wdt, metis_norm_t kind, float eps, void *y,
                               metis_dtype_t ydt, int64_t ldy, float *mean, float *rstd, metis_act8_t *stored,
@@ -437,6 +441,163 @@ metis_status_t metis_swiglu_bwd(const void *dh, metis_dtype_t dhdt, int64_t lddh
                                 const void *b, int64_t ldb, metis_dtype_t dt, const metis_act8_t *qa,
                                 const metis_act8_t *qb, int64_t rows, int64_t cols, void *da, int64_t ldda, void *db,
                                 int64_t lddb, void *h, int64_t ldh, metis_dtype_t odt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass: what stands between the query / key projection and attention.
+ * A token's row of q holds q_heads heads of head_dim elements side by side, a
+ * row of k k_heads of them. For each head x of n = head_dim elements
+ *   LAYER: xh = (x - mean) rstd,  RMS: xh = x rstd  (as metis_norm_fwd, no
+ *   bias),  NONE: xh = x,
+ *   u = xh w  (w = wq or wk, shared by the heads; NULL: 1),
+ * and of the first rot_dim elements each pair (a, b) is turned by its angle:
+ *   y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin.
+ * Pair i (of rot_dim / 2) is (i, i + rot_dim / 2) with METIS_ROPE_HALVES and
+ * (2 i, 2 i + 1) with METIS_ROPE_NEIGHBOURS; the elements behind rot_dim are
+ * left as they are.
+ *  q, k:      tokens x (heads * head_dim) of type dt, ldq / ldk at least that
+ *             wide (also parts of one matrix). k_heads = 0: no k, wk, ko.
+ *  positions: int32 of tokens elements: the row of `rope` for each token.
+ *  rope:      fp32, rope_rows x rot_dim, tightly packed: the cosines of a
+ *             position's rot_dim / 2 angles, then their sines. A position
+ *             outside [0, rope_rows) makes the token's rotated elements NaN
+ *             (its gradient and dw too), never an out-of-bounds read. rot_dim = 0:
+ *             positions and rope are not read.
+ *  qo, ko:    tokens x (heads * head_dim) of type odt, rounded once from fp32.
+ *  1 <= head_dim <= 512, 0 <= rot_dim <= head_dim, rot_dim even, at most 65536
+ * heads (head_dim or heads beyond: METIS_ERR_UNSUPPORTED). No output may share
+ * memory with an input or another output; the sums' range is as for
+ * metis_norm_fwd. */
+typedef enum { METIS_ROPE_HALVES = 0, METIS_ROPE_NEIGHBOURS = 1 } metis_rope_t;
+metis_status_t metis_qk_norm_rope_fwd(const void *q, int64_t ldq, int32_t q_heads, const void *k, int64_t ldk,
+                                      int32_t k_heads, metis_dtype_t dt, int64_t tokens, int32_t head_dim,
+                                      const void *wq, const void *wk, metis_dtype_t wdt, metis_norm_t kind, float eps,
+                                      const int32_t *positions, const float *rope, int64_t rope_rows, int32_t rot_dim,
+                                      metis_rope_t pairs, void *qo, int64_t ldqo, void *ko, int64_t ldko,
+                                      metis_dtype_t odt, hipStream_t stream);
+
+/* Its gradients. With g = dy turned back by the same angles and u = g w:
+ *   dx = rstd (u - [LAYER: sum(u) / n] - xh sum(u xh) / n),  NONE: dx = u,
+ *   dw = sum over tokens and heads of g xh.
+ *  dq, dk: tokens x (heads * head_dim) of type dydt: the gradients of qo, ko.
+ *  q, k:   the forward's inputs (xh is formed again from them, nothing is
+ *          kept); not read with METIS_NORM_NONE, where they may be NULL.
+ *  dqi, dki: gradients of q and k, type dxdt, rounded once from fp32.
+ *  dwq, dwk: optional fp32 of head_dim elements, stored (accumulate == 0) or
+ *          added to what is there (accumulate != 0); NULL with NONE. With no
+ *          tokens they are zero (stored) or kept (added).
+ *  ws:     metis_qk_norm_rope_bwd_workspace_bytes() bytes, 256-byte aligned;
+ *          may be NULL without dwq and dwk.
+ * Sums run in a fixed order: bitwise reproducible. */
+size_t metis_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+metis_status_t metis_qk_norm_rope_bwd(const void *dq, int64_t lddq, const void *dk, int64_t lddk, metis_dtype_t dydt,
+                                      const void *q, int64_t ldq, int32_t q_heads, const void *k, int64_t ldk,
+                                      int32_t k_heads, metis_dtype_t dt, int64_t tokens, int32_t head_dim,
+                                      const void *wq, const void *wk, metis_dtype_t wdt, metis_norm_t kind, float eps,
+                                      const int32_t *positions, const float *rope, int64_t rope_rows, int32_t rot_dim,
+                                      metis_rope_t pairs, void *dqi, int64_t lddqi, void *dki, int64_t lddki,
+                                      metis_dtype_t dxdt, float *dwq, float *dwk, int32_t accumulate, void *ws,
+                                      size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The linear layer for a few tokens: y = x W_hat^T with x dense (not
+ * quantized) and W_hat the FP4 weight of spectral_fp4_linear_fwd,
+ *   y[t, i] = sum_j R_hat[i, j] x[t, j]
+ *           + sum_r U_hat[i, r] S_r sum_j V_hat[j, r] x[t, j],
+ * each codes-times-scales value exact, products and sums in fp32.
+ *  x:  tokens x W->n of type dt, ldx >= W->n >= 1.
+ *  W:  R_q set (codes and scales 4-byte aligned), with k > 0 also S, Ut_q and
+ *      Vt_q; U, V and Rt_q are not read. Unsplit (k == 0) weights may have any
+ *      number of rows and any multiple of the block (32 or 16) of columns.
+ *  y:  tokens x W->m of type ydt, rounded once from fp32.
+ *  ws: metis_fp4_gemv_workspace_bytes() bytes, 256-byte aligned; NULL is fine
+ *      where that is 0 (bf16 x and k == 0).
+ * Any number of tokens is taken, 64 at a time: W is read once for each 64, so
+ * that beyond a few hundred tokens quantizing x for spectral_fp4_linear_fwd is
+ * faster. Values below 2^-126 may be taken as 0. A NaN or an infinity in x
+ * spoils its own token. Bitwise reproducible. */
+size_t metis_fp4_gemv_workspace_bytes(int64_t tokens, metis_dtype_t dt, const metis_split_t *W);
+metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_t tokens, int64_t ldx, const metis_split_t *W,
+                              void *y, metis_dtype_t ydt, int64_t ldy, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged FP4 cache of keys and values. k and v are two FP4 matrices of
+ * pages * heads * page_size rows and head_dim columns (k.cols == v.cols): the
+ * row of place s in page p for head h is (p * heads + h) * page_size + s.
+ *  head_dim: a multiple of 32, at most 256 (beyond: METIS_ERR_UNSUPPORTED), in
+ *      both formats; at most 2^31 - 1 rows. page_size may be any number >= 1.
+ *  NVFP4: the tensor scales are the caller's and are read only: tensor_scale
+ *      of k and v has to be set before anything is stored (largest magnitude
+ *      expected / 2688); larger values saturate. */
+typedef struct {
+  int64_t pages;
+  int32_t page_size, heads;
+  metis_fp4_t k, v;
+} metis_kv_cache_t;
+
+/* A batch of sequences that new tokens belong to (device arrays).
+ *  table:   int32, seqs x max_pages, leading dimension ldt: the pages of each
+ *           sequence in order; entries behind its last page are not read.
+ *  lengths: int32[seqs]: tokens of each sequence with its new ones. 0 or less:
+ *           the sequence is not in use.
+ *  starts:  int32[seqs + 1]: the new tokens of sequence s are the rows
+ *           starts[s] .. starts[s + 1] - 1, its last ones in order; NULL: one
+ *           new token each, row s of sequence s. Rows outside belong to none.
+ * A new token i of n of a sequence of length L is at position L - n + i;
+ * negative positions are no tokens. A sequence whose rows reach outside the
+ * call's tokens is left out. max_pages * page_size <= 2^29. */
+typedef struct {
+  const int32_t *table, *lengths, *starts;
+  int64_t ldt;
+  int32_t seqs, max_pages;
+} metis_kv_batch_t;
+
+/* Stores new tokens' keys and values into the cache, the keys turned by the
+ * angles of their positions on the way.
+ *  k, v:  tokens x (heads * head_dim) of type dt.
+ *  rope, rope_rows, rot_dim, pairs: as for metis_qk_norm_rope_fwd; NULL with
+ *         rot_dim = 0 stores the keys as they are. The rotation is formed in
+ *         fp64 and rounded once to fp32.
+ * Each row of a head is then quantized as fp4_block_quant does with the
+ * cache's tensor scale. A row that belongs to no sequence, and a token whose
+ * position is outside the table or the rope, or whose page is outside
+ * [0, pages), is not stored; nothing else in the cache changes. Pages that a
+ * call writes to have to belong to one sequence each. */
+metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, metis_dtype_t dt,
+                               int64_t tokens, const metis_kv_batch_t *batch, const float *rope, int64_t rope_rows,
+                               int32_t rot_dim, metis_rope_t pairs, const metis_kv_cache_t *cache, hipStream_t stream);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * stored already): for the query at position p of a sequence
+ *   o = sum_t softmax_t(scale q . k_t) v_t,  t in (p - window, p]  (window 0:
+ *   all t <= p).
+ *  q:      tokens x (heads * head_dim) of type dt, tokens * heads < 2^24;
+ *          heads a multiple of the cache's: query head h reads head h / (heads / cache->heads).
+ *  o:      tokens x (heads * head_dim) of type odt, rounded once from fp32. A
+ *          new token that sees nothing (a sequence not in use, a negative
+ *          position) gives zeros; rows that belong to no sequence are left as
+ *          they were. A page outside [0, pages) below a query's position, or a
+ *          length beyond the table, makes its output NaN, never an
+ *          out-of-bounds read.
+ *  lse:    optional fp32, tokens x heads: log sum_t exp(scale q . k_t), -inf
+ *          where nothing is seen (to join with attention over other tokens).
+ *  max_new: an upper bound of the new tokens of any sequence (1 without
+ *          starts); those beyond it are left as they were.
+ *  max_length: about the largest length, which the work is divided by (any
+ *          value >= 1 gives the same result but for rounding; the true one the
+ *          best speed). The lengths themselves stay on the device.
+ *  ws:     metis_kv_attention_workspace_bytes() bytes, 256-byte aligned.
+ * Queries and keys enter the products as they are (fp32 queries as three bf16
+ * parts), the weights exp(score - max) as two bf16 parts, three where q or o is
+ * fp32; scores, sums and o in fp32. Bitwise reproducible. A NaN or an infinity
+ * in q spoils its own row; one in the cache every new token's of its sequence
+ * and head, in the rows that the kernel works on with it. */
+size_t metis_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
+                                          const metis_kv_batch_t *batch, const metis_kv_cache_t *cache);
+metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, int64_t tokens, int64_t ldq, int32_t heads,
+                                  const metis_kv_batch_t *batch, const metis_kv_cache_t *cache, int32_t max_new,
+                                  int64_t max_length, float scale, int64_t window, void *o, metis_dtype_t odt,
+                                  int64_t ldo, float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
