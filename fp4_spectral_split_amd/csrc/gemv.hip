@@ -15,6 +15,7 @@
 // fp32 x enters as three bf16 parts (exact), z likewise; these and z come from
 // launches of their own ahead of the main one.
 #include <algorithm>
+#include <type_traits>
 
 #include "decode4.hpp"
 
@@ -28,6 +29,7 @@ constexpr int kStep = 128;      // columns of a wave's step
 constexpr int kTokens = 64;     // tokens of a pass over W
 constexpr int kMaxRank = 96;
 constexpr int kMaxWaves = 16;
+constexpr int kManyRows = 12288;
 
 struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` columns
   const uint8_t *codes, *scales;
@@ -64,18 +66,20 @@ template <bool NV, bool EDGE>
 __device__ __forceinline__ void load_codes(const Weight &w, bool there, int64_t row, int c, Codes &r) {
   const uint8_t *p = w.codes + row * (w.cols / 2) + c / 2;
   const uint8_t *s = w.scales + row * (w.cols / kBlock4<NV>) + c / kBlock4<NV>;
-  r.w[0] = r.w[1] = r.w[2] = r.w[3] = r.scale = 0u;
   if (!EDGE || (there && c + 32 <= w.cols)) {
     const u32x4_a1 v = *(const u32x4_a1 *)p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.w[i] = v[i];
     r.scale = s[0];
     if (NV) r.scale |= (uint32_t)s[1] << 8;
-  } else if (NV && there && c < w.cols) {  // the last sixteen columns
-    const u32x2_a1 v = *(const u32x2_a1 *)p;
-    r.w[0] = v[0];
-    r.w[1] = v[1];
-    r.scale = s[0];
+  } else {
+    r.w[0] = r.w[1] = r.w[2] = r.w[3] = r.scale = 0u;
+    if (NV && there && c < w.cols) {  // the last sixteen columns
+      const u32x2_a1 v = *(const u32x2_a1 *)p;
+      r.w[0] = v[0];
+      r.w[1] = v[1];
+      r.scale = s[0];
+    }
   }
 }
 
@@ -84,116 +88,184 @@ template <bool NV> __device__ __forceinline__ void scales_of(const Codes &c, flo
   s[1] = NV ? scale4<NV>(c.scale >> 8) : s[0];
 }
 
-// P: bf16 parts of x. NT: sixteens of tokens. Z: the launch that forms z.
-template <bool NV, int P, int NT, bool Z>
+// 32 of the rank's terms for sixteen rows, as loaded.
+struct Low {
+  uint32_t code[8], scale[8];
+  u32x4_a1 z[3];
+};
+template <bool NV>
+__device__ __forceinline__ void load_low(const MainArgs &g, int64_t row, int k0, Low &w) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t k = min(k0 + j, g.rank - 1);
+    w.code[j] = g.u.codes[k * (g.u.cols / 2) + row / 2];
+    w.scale[j] = g.u.scales[k * (g.u.cols / kBlock4<NV>) + row / kBlock4<NV>];
+  }
+}
+__device__ __forceinline__ void load_z(const MainArgs &g, int token, int k0, Low &w) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    w.z[p] = u32x4_a1{0u, 0u, 0u, 0u};
+    if (token < g.tokens) w.z[p] = *(const u32x4_a1 *)(g.z + ((int64_t)p * kTokens + token) * rank_pad(g.rank) + k0);
+  }
+}
+// Their eight elements of U in a lane. Terms behind the rank are zero.
+template <bool NV> __device__ __forceinline__ ushortx8 low_rows(const MainArgs &g, const Low &w, int64_t row, int k0) {
+  uint32_t word = 0u, a[4];
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    word |= ((w.code[j] >> (4 * (row & 1))) & 15u) << (4 * j);
+    s[j] = k0 + j < g.rank ? scale4<NV>(w.scale[j]) : 0.0f;
+  }
+#define METIS_PAIR(J)                                                                            \
+  {                                                                                              \
+    const floatx2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, J);                   \
+    a[J] = upper_halves(__float_as_uint(v[0] * s[2 * J]), __float_as_uint(v[1] * s[2 * J + 1])); \
+  }
+  METIS_PAIR(0) METIS_PAIR(1) METIS_PAIR(2) METIS_PAIR(3)
+#undef METIS_PAIR
+  const intx4 v = {(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
+  return __builtin_bit_cast(ushortx8, v);
+}
+
+// P: bf16 parts of x. NT: sixteens of tokens. RT: sixteens of rows. Z: the
+// launch that forms z.
+template <bool NV, int P, int NT, int RT, bool Z>
 __global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
-  extern __shared__ float sums[];  // waves x NT x 16 tokens x 16 rows
+  extern __shared__ float sums[];  // waves x RT x NT x 16 tokens x 16 rows
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int row0 = blockIdx.x * kRows, cols = g.w.cols;
-  const bool there = row0 + r < g.w.rows;
-  const int64_t row = there ? row0 + r : g.w.rows - 1;
-  floatx4 acc[NT];
+  const int row0 = blockIdx.x * kRows * RT, cols = g.w.cols;
+  int64_t row[RT];  // rows behind the last one: its codes again, not stored
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < RT; ++t) row[t] = min(row0 + 16 * t + r, g.w.rows - 1);
+  floatx4 acc[RT][NT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[t][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto work = [&](const Codes &c, int at) {
-    float s[2];
-    scales_of<NV>(c, s);
+  // the rank's terms: 32 of them for sixteen rows are a task, under way from
+  // the start (what a wave has beyond one task, at its end)
+  const int chunks = Z ? 0 : (g.rank + 31) / 32, tasks = chunks * RT;
+  Low low = {};
+  if (!Z && wave < tasks) {
+    load_low<NV>(g, min((int64_t)row0 + 16 * (wave / chunks) + r, (int64_t)g.w.rows - 1), 32 * (wave % chunks) + 8 * q, low);
+    if (NT == 1) load_z(g, r, 32 * (wave % chunks) + 8 * q, low);
+  }
+
+  // N steps of 128 columns, `waves` apart: all their codes are asked for before
+  // the first of them is used, x (which the L2 holds) for XU units of eight
+  // columns at a time, as many as registers allow
+  constexpr int kX = 16 / (NT * P);
+  auto run = [&](auto count, auto edge, int st) {
+    constexpr int N = decltype(count)::value;
+    constexpr bool EDGE = decltype(edge)::value;
+    constexpr int XU = kX >= 8 ? (N > 1 ? 8 : 4) : kX >= 4 ? 4 : kX >= 2 ? 2 : 1;
+    Codes c[N][RT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const ushortx8 a = decode4<NV>(c.w[i], s[i / 2]);
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) load_codes<NV, EDGE>(g.w, true, row[t], (st + i * waves) * kStep + 32 * q, c[i][t]);
+#pragma unroll
+    for (int u0 = 0; u0 < 4 * N; u0 += XU) {
+      u32x4_a1 x[XU][NT][P];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int token = 16 * n + r;
+        const unsigned short *p = g.x + (int64_t)token * g.ldx + 32 * q;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          u32x4_a1 b = {0u, 0u, 0u, 0u};
-          if (token < g.tokens && at + 8 * i < cols)
-            b = *(const u32x4_a1 *)(g.x + p * g.plane + (int64_t)token * g.ldx + at + 8 * i);
-          acc[n] = mfma16_bf16(a, __builtin_bit_cast(ushortx8, b), acc[n]);
+        for (int u = 0; u < XU; ++u)
+#pragma unroll
+          for (int k = 0; k < P; ++k) x[u][n][k] = u32x4_a1{0u, 0u, 0u, 0u};
+        if (token < g.tokens) {
+#pragma unroll
+          for (int u = 0; u < XU; ++u) {
+            const int at = (st + (u0 + u) / 4 * waves) * kStep + 8 * ((u0 + u) % 4);
+            if (!EDGE || at + 32 * q < cols) {
+#pragma unroll
+              for (int k = 0; k < P; ++k) x[u][n][k] = *(const u32x4_a1 *)(p + k * g.plane + at);
+            }
+          }
         }
       }
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int u = 0; u < XU; ++u) {
+          const int i = (u0 + u) / 4, e = (u0 + u) % 4;
+          float s[2];
+          scales_of<NV>(c[i][t], s);
+          const ushortx8 a = decode4<NV>(c[i][t].w[e], s[e / 2]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+              acc[t][n] = mfma16_bf16(a, __builtin_bit_cast(ushortx8, x[u][n][k]), acc[t][n]);
+        }
     }
   };
-
-  // steps of 128 columns, dealt to the waves in turn; the last one may end early
+  // the steps are dealt to the waves in turn; the last one may end early
   const int steps = (cols + kStep - 1) / kStep, whole = cols / kStep;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = RT == 1 && NT * P == 1 ? 4 : 2;
   int st = wave;
-  for (; st + (kAhead - 1) * waves < whole; st += kAhead * waves) {
-    Codes c[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_codes<NV, false>(g.w, there, row, (st + i * waves) * kStep + 32 * q, c[i]);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) work(c[i], (st + i * waves) * kStep + 32 * q);
+  for (; st + (kAhead - 1) * waves < whole; st += kAhead * waves)
+    run(std::integral_constant<int, kAhead>(), std::false_type(), st);
+  if (kAhead == 4 && st + waves < whole) {
+    run(std::integral_constant<int, 2>(), std::false_type(), st);
+    st += 2 * waves;
   }
-  for (; st < steps; st += waves) {
-    Codes c;
-    load_codes<NV, true>(g.w, there, row, st * kStep + 32 * q, c);
-    work(c, st * kStep + 32 * q);
-  }
+  for (; st < steps; st += waves) run(std::integral_constant<int, 1>(), std::true_type(), st);
   if (NV) {
     const float whole_scale = *g.w.whole;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] *= whole_scale;
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[t][n] *= whole_scale;
   }
 
-  // 32 of the rank's terms to each of the first waves
-  if (!Z && 32 * wave < g.rank) {
-    floatx4 low[NT];
+  if (!Z) {
+    const float whole_scale = NV && tasks ? *g.u.whole : 1.0f;
+    for (int task = wave; task < tasks; task += waves) {
+      const int at = task / chunks, k0 = 32 * (task % chunks) + 8 * q;
+      const int64_t i = min((int64_t)row0 + 16 * at + r, (int64_t)g.w.rows - 1);
+      if (task != wave) load_low<NV>(g, i, k0, low);
+      const ushortx8 a = low_rows<NV>(g, low, i, k0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) low[n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int k0 = 32 * wave + 8 * q;
-    uint32_t word = 0u;
-    float s[8];
+      for (int n = 0; n < NT; ++n) {
+        if (NT > 1 || task != wave) load_z(g, 16 * n + r, k0, low);
+        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t k = min(k0 + j, g.rank - 1);
-      const uint32_t byte = g.u.codes[k * (g.u.cols / 2) + row / 2];
-      word |= ((byte >> (4 * (row & 1))) & 15u) << (4 * j);
-      s[j] = k0 + j < g.rank ? scale4<NV>(g.u.scales[k * (g.u.cols / kBlock4<NV>) + row / kBlock4<NV>]) : 0.0f;
+        for (int p = 2; p >= 0; --p) v = mfma16_bf16(a, __builtin_bit_cast(ushortx8, low.z[p]), v);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          if (t == at) acc[t][n] += v * whole_scale;
+      }
     }
-    uint32_t a[4];
-#define METIS_PAIR(J)                                                                                       \
-  {                                                                                                         \
-    const floatx2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, J);                              \
-    a[J] = upper_halves(__float_as_uint(v[0] * s[2 * J]), __float_as_uint(v[1] * s[2 * J + 1]));            \
   }
-    METIS_PAIR(0) METIS_PAIR(1) METIS_PAIR(2) METIS_PAIR(3)
-#undef METIS_PAIR
-    const intx4 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
-    const int pad = rank_pad(g.rank);
+
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        u32x4_a1 b = {0u, 0u, 0u, 0u};
-        if (16 * n + r < g.tokens) b = *(const u32x4_a1 *)(g.z + ((int64_t)p * kTokens + 16 * n + r) * pad + k0);
-        low[n] = mfma16_bf16(__builtin_bit_cast(ushortx8, av), __builtin_bit_cast(ushortx8, b), low[n]);
-      }
-    const float whole_scale = NV ? *g.u.whole : 1.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] += low[n] * whole_scale;
-  }
-
-#pragma unroll
-  for (int n = 0; n < NT; ++n) *(floatx4 *)(sums + (((wave * NT + n) * 16 + r) * 16 + 4 * q)) = acc[n];
+      *(floatx4 *)(sums + ((((wave * RT + t) * NT + n) * 16 + r) * 16 + 4 * q)) = acc[t][n];
   __syncthreads();
-  for (int e = threadIdx.x; e < NT * 256; e += blockDim.x) {
-    const int token = e >> 4, i = row0 + (e & 15);
-    if (token >= g.tokens) break;
+  for (int e = threadIdx.x; e < RT * NT * 256; e += blockDim.x) {
+    const int t = e / (NT * 256), token = (e >> 4) % (NT * 16), i = row0 + 16 * t + (e & 15);
+    if (token >= g.tokens) continue;
     float v = 0.0f;
-    for (int k = 0; k < waves; ++k) v += sums[k * NT * 256 + e];
+#pragma unroll 4
+    for (int k = 0; k < waves; ++k) v += sums[k * RT * NT * 256 + e];
     if (Z) {
       const int pad = rank_pad(g.w.rows);
       if (i < pad) {  // three bf16 parts; zeros behind the rank
-        float t = i < g.w.rows ? v * g.s[i] : 0.0f;
+        float z = i < g.w.rows ? v * g.s[i] : 0.0f;
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-          const uint32_t cut = p < 2 ? __float_as_uint(t) & 0xFFFF0000u : pack_bf16(0.0f, t);
+          const uint32_t cut = p < 2 ? __float_as_uint(z) & 0xFFFF0000u : pack_bf16(0.0f, z);
           g.z_out[((int64_t)p * kTokens + token) * pad + i] = (unsigned short)(cut >> 16);
-          t -= __uint_as_float(cut);
+          z -= __uint_as_float(cut);
         }
       }
     } else if (i < g.w.rows) {
@@ -223,14 +295,24 @@ __global__ void __launch_bounds__(256) parts_kernel(const float *x, int64_t ldx,
 }
 
 // ------------------------------------------------------------------- host
-template <bool NV, int P, int NT, bool Z> void launch_tokens(const MainArgs &g, int waves, hipStream_t stream) {
-  gemv_kernel<NV, P, NT, Z><<<(unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows), 64 * waves,
-                              (size_t)waves * NT * 1024, stream>>>(g);
+template <bool NV, int P, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, int waves, hipStream_t stream) {
+  gemv_kernel<NV, P, NT, RT, Z><<<(unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows * RT), 64 * waves,
+                                  (size_t)waves * RT * NT * 1024, stream>>>(g);
 }
+// Rows of a workgroup: x is read once for each workgroup, so that many rows are
+// better, as long as there are workgroups for every CU.
 template <bool NV, int P, bool Z> void launch_parts(const MainArgs &g, int waves, hipStream_t stream) {
-  if (g.tokens <= 16) launch_tokens<NV, P, 1, Z>(g, waves, stream);
-  else if (g.tokens <= 32) launch_tokens<NV, P, 2, Z>(g, std::min(waves, 8), stream);
-  else launch_tokens<NV, P, 4, Z>(g, std::min(waves, 8), stream);
+  const bool many = !Z && g.w.rows >= kManyRows;
+  if (g.tokens <= 16) {
+    if (many) launch_rows<NV, P, 1, Z ? 1 : 2, Z>(g, waves, stream);
+    else launch_rows<NV, P, 1, 1, Z>(g, waves, stream);
+  } else if (g.tokens <= 32) {
+    if (many) launch_rows<NV, P, 2, Z ? 1 : 2, Z>(g, std::min(waves, 8), stream);
+    else launch_rows<NV, P, 2, 1, Z>(g, std::min(waves, 8), stream);
+  } else {
+    if (many) launch_rows<NV, P, 4, Z ? 1 : 2, Z>(g, std::min(waves, 8), stream);
+    else launch_rows<NV, P, 4, 1, Z>(g, std::min(waves, 8), stream);
+  }
 }
 template <bool Z> void launch(const MainArgs &g, bool nv, bool f32, int waves, hipStream_t stream) {
   if (nv) {
@@ -333,7 +415,7 @@ extern "C" metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_
     g.y = ydt == METIS_F32 ? (void *)((float *)y + t0 * ldy) : (void *)((unsigned short *)y + t0 * ldy);
     g.ldy = ldy;
     g.y_bf16 = ydt == METIS_BF16;
-    launch<false>(g, nv, f32, waves_for(K, 8), stream);
+    launch<false>(g, nv, f32, waves_for(K, K > 8192 ? 16 : 8), stream);
   }
   METIS_LAUNCH_CHECK();
   return METIS_OK;

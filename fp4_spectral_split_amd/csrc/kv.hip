@@ -36,7 +36,7 @@ using namespace metis_host;
 namespace {
 
 constexpr int kMaxDim = 256;
-constexpr int64_t kMaxTokens = (int64_t)1 << 29;  // max_pages * page_size
+constexpr int64_t kMaxTokens = (int64_t)1 << 28;  // max_pages * page_size; divisions are exact below 2^29
 
 struct Batch {
   const int32_t *table, *lengths, *starts;
@@ -126,6 +126,19 @@ __device__ __forceinline__ void turned(const AppendArgs &g, const T *head, int d
 
 template <typename T, bool NV> __global__ void __launch_bounds__(256) append_kernel(AppendArgs g) {
   const int64_t t = g.first + blockIdx.x;
+  const int per_head = g.dim / 8, per_side = g.p.heads * per_head;
+  auto source = [&](int u, int &side, int &head, int &d) -> const T * {
+    side = u >= per_side;
+    const int w = side ? u - per_side : u;
+    head = w / per_head;
+    d = (w - head * per_head) * 8;
+    return (const T *)(side ? g.x[1] : g.x[0]) + t * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.dim;
+  };
+  // the elements are under way while their place is looked up
+  int side, head, d;
+  const T *x = source(min((int)threadIdx.x, 2 * per_side - 1), side, head, d);
+  Raw<T> raw;
+  load_all(x + d, raw);
   const int seq = sequence_of(g.b, t);
   if (seq < 0) return;  // the same for the whole workgroup, as are the ways out below
   const int64_t end = g.b.starts ? g.b.starts[seq + 1] : t + 1;
@@ -137,13 +150,13 @@ template <typename T, bool NV> __global__ void __launch_bounds__(256) append_ker
   const int page = g.b.table[seq * g.b.ldt + at];
   if (page < 0 || page >= g.p.pages) return;
   const int place = (int)((uint32_t)position - at * g.p.by_page.d);
-  const int per_head = g.dim / 8, per_side = g.p.heads * per_head;
   for (int u = threadIdx.x; u < 2 * per_side; u += blockDim.x) {  // whole quads: per_head is a multiple of four
-    const int side = u >= per_side, w = side ? u - per_side : u;
-    const int head = w / per_head, d = (w - head * per_head) * 8;
-    const T *x = (const T *)(side ? g.x[1] : g.x[0]) + t * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.dim;
+    if (u != (int)threadIdx.x) {
+      x = source(u, side, head, d);
+      load_all(x + d, raw);
+    }
     float v[8];
-    load8(x + d, v);
+    to_f32(raw, v);
     if (!side && g.rot) turned(g, x, d, position, v);
     float top = 0.0f;
 #pragma unroll
@@ -178,6 +191,7 @@ constexpr int kWaves = 4;
 constexpr int kTile = 32;  // tokens of a wave's step
 constexpr int kStepTokens = kWaves * kTile;
 constexpr int kRowsQ = 16;
+constexpr int kMaxSplits = 256;  // a thread of the join for each
 
 struct AttendArgs {
   const void *q;
@@ -202,7 +216,6 @@ struct AttendArgs {
 };
 
 constexpr float kLn2 = 0.693147181f;
-constexpr uint32_t kNoRow = 0xFFFFFFFFu, kBadRow = 0xFFFFFFFEu;
 
 __device__ __forceinline__ float nan_f32() { return __uint_as_float(0x7FC00000u); }
 
@@ -225,16 +238,39 @@ template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, ui
   }
 }
 
+// Maximum and sum over the four lanes that share lane % 16.
+__device__ __forceinline__ float quarter_max(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Where the 32 tokens of a step are in the cache. Whole pages of a multiple of
+// sixteen places (HALVES): each half of them lies in one page, so the entries
+// are the wave's. Any other page size: an entry to a lane, token lane % 32.
+template <bool HALVES> struct Place {
+  int page[2];      // as in the table
+  uint32_t row[2];  // of the half's first token; row[0]: of token lane % 32
+  bool bad[2];      // a page outside the cache
+};
+
 // NC: head size / 32. PQ, PP: bf16 parts of q and of the weights.
-template <bool NV, int NC, int PQ, int PP, typename TQ>
-__global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
+template <bool NV, int NC, int PQ, int PP, typename TQ, bool HALVES>
+__global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) attend_kernel(AttendArgs g) {
   constexpr int D = 32 * NC;
-  constexpr int kUnitsPerScale = NV ? 2 : 4;                      // units of eight elements under one scale
-  constexpr bool kEven = NC % kUnitsPerScale == 0 || kUnitsPerScale % NC == 0;  // a lane's key units fill whole scales, or share one
-  constexpr int kKeyScales = NC % kUnitsPerScale == 0 ? NC / kUnitsPerScale : (kUnitsPerScale % NC == 0 ? 1 : NC);
-  constexpr int kV = (NC + 1) / 2;                                // 32-element pieces of values in a lane
-  constexpr int kStride = D + 16;                                 // bf16 elements of a row of v in LDS
-  constexpr int kVBytes = kTile * kStride * 2;
+  constexpr int kPerScale = NV ? 2 : 4;  // units of eight elements under one scale
+  // scales of a lane's NC units of a key: whole ones, one that it shares, or one for each unit
+  constexpr int kKeyScales = NC % kPerScale == 0 ? NC / kPerScale : (kPerScale % NC == 0 ? 1 : NC);
+  constexpr int kV = (NC + 1) / 2;     // 32-element pieces of values in a lane
+  constexpr int kStride = 2 * D + 32;  // bytes of a row of v in LDS
+  constexpr int kVBytes = kTile * kStride;
   constexpr int kOStride = D + 4;
   static_assert(kRowsQ * kOStride * 4 + kRowsQ * 8 <= kVBytes, "the join fits where v was");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kVBytes];
@@ -248,113 +284,126 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
   id /= g.tiles;
   const int kvh = id % g.p.heads, seq = id / g.p.heads;
 
-  const int64_t start = g.b.starts ? g.b.starts[seq] : seq, stop = g.b.starts ? g.b.starts[seq + 1] : seq + 1;
+  const int start = __builtin_amdgcn_readfirstlane(g.b.starts ? g.b.starts[seq] : seq);
+  const int stop = __builtin_amdgcn_readfirstlane(g.b.starts ? g.b.starts[seq + 1] : seq + 1);
   if (start < 0 || stop > g.tokens || start >= stop) return;
-  const int new_tokens = (int)(stop - start), count = min(new_tokens, g.max_new);
+  const int new_tokens = stop - start, count = min(new_tokens, g.max_new);
   if (tile * kRowsQ >= count * (int64_t)g.group) return;
-  const int64_t length = max(g.b.lengths[seq], 0);
+  const int length = max(__builtin_amdgcn_readfirstlane(g.b.lengths[seq]), 0);
   // this lane's query row
   const int at = tile * kRowsQ + r;
   const int j = (int)g.by_group.div((uint32_t)at), h = kvh * g.group + at - j * g.group;
   const bool row_there = j < count;
   const int64_t row = start + j;
-  const int64_t capacity = (int64_t)g.b.max_pages * g.p.page_size;
-  const bool beyond = length > capacity;
-  const int64_t end_row = row_there ? max((int64_t)0, length - new_tokens + j + 1) : 0;  // tokens below it are seen
-  const int64_t end = beyond ? 0 : end_row;
-  const int64_t begin = g.window > 0 ? max((int64_t)0, end - g.window) : 0;
+  // a length that the table does not hold, or no cache at all: nothing is read, and what sees a token is NaN
+  const bool beyond = length > g.b.max_pages * (int64_t)g.p.page_size || g.p.pages == 0;
+  const int end_row = row_there ? max(0, length - new_tokens + j + 1) : 0;  // tokens below it are seen
+  const int end = beyond ? 0 : end_row;
+  const int begin = (int)(g.window > 0 ? max((int64_t)0, end - g.window) : 0);
   // tokens that any row of the tile sees
   const int j0 = (int)g.by_group.div((uint32_t)(tile * kRowsQ));
   const int j1 = min(count - 1, (int)g.by_group.div((uint32_t)(tile * kRowsQ + kRowsQ - 1)));
-  int64_t hi = beyond ? 0 : max((int64_t)0, length - new_tokens + j1 + 1);
-  int64_t lo = g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0;
-  lo = lo / kTile * kTile;
+  const int hi = beyond ? 0 : max(0, length - new_tokens + j1 + 1);
+  const int lo = (int)(g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0) / kTile * kTile;
   // all of it, whatever the length that the launch was made for
-  const int64_t each = (hi - lo + g.splits - 1) / g.splits;
-  const int64_t chunk = max((int64_t)g.chunk, (each + kStepTokens - 1) / kStepTokens * kStepTokens);
-  const int64_t from = lo + split * chunk, to = min(hi, from + chunk);
-  if (g.splits > 1 && from >= to) {  // nothing here; the join skips (-inf, 0)
+  const int each = (max(hi - lo, 0) + g.splits - 1) / g.splits;
+  const int chunk = max(g.chunk, (each + kStepTokens - 1) / kStepTokens * kStepTokens);
+  const int64_t from64 = lo + split * (int64_t)chunk;
+  if (g.splits > 1 && from64 >= hi) {  // nothing here; the join skips (-inf, 0)
     if (threadIdx.x < kRowsQ && row_there)
       g.stat[((int64_t)split * g.tokens + row) * g.heads + h] = make_float2(-INFINITY, beyond && end_row > 0 ? nan_f32() : 0.0f);
     return;
   }
+  const int from = (int)from64, to = min(hi, (int)min((int64_t)INT32_MAX, from64 + chunk));
 
   floatx4 o[2 * NC];
 #pragma unroll
   for (int i = 0; i < 2 * NC; ++i) o[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   float top = -INFINITY, sum = 0.0f;  // sum: this lane's tokens only
 
-  if (from < to) {
-    // q: element 8 i of this lane's quarter of the head, as B operands
+  if (from + wave * kTile < to) {
+    const int32_t *table = g.b.table + seq * g.b.ldt;
+    // table entries of the tokens from base on (page 0 behind the last one)
+    auto find = [&](int base, Place<HALVES> &p) {
+#pragma unroll
+      for (int s = 0; s < (HALVES ? 2 : 1); ++s) {
+        const int t = HALVES ? base + 16 * s : base + (lane & 31);
+        p.page[s] = 0;
+        if (t < to) p.page[s] = table[g.p.by_page.div((uint32_t)t)];
+      }
+    };
+    // their rows. Tokens behind the last one and pages outside the cache are
+    // read at page 0: neither counts
+    auto place = [&](int base, Place<HALVES> &p) {
+#pragma unroll
+      for (int s = 0; s < (HALVES ? 2 : 1); ++s) {
+        const int t = HALVES ? base + 16 * s : base + (lane & 31);
+        const int page = HALVES ? __builtin_amdgcn_readfirstlane(p.page[s]) : p.page[s];
+        p.bad[s] = page < 0 || page >= g.p.pages;
+        const uint32_t in_page = (uint32_t)t - g.p.by_page.div((uint32_t)t) * g.p.by_page.d;
+        p.row[s] = ((uint32_t)(p.bad[s] ? 0 : page) * g.p.heads + kvh) * g.p.page_size + in_page;
+      }
+    };
+    struct Tile {
+      uint32_t k[2][NC], ks[2][kKeyScales];
+      uint32_t v[kV][4], vs[kV];
+    };
+    auto row_at = [&](const Place<HALVES> &p, int token) -> uint32_t {  // token of the step
+      if (HALVES) return (token < 16 ? p.row[0] : p.row[1]) + (token & 15);
+      return __shfl(p.row[0], token, 64);
+    };
+    auto load = [&](const Place<HALVES> &p, Tile &t) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint64_t kr = row_at(p, 16 * s + r);
+        load_words<NC>(g.kc + kr * (D / 2) + gq * (D / 8), t.k[s]);
+        const uint8_t *q = g.ks + kr * (D / kBlock4<NV>);
+#pragma unroll
+        for (int i = 0; i < kKeyScales; ++i)
+          t.ks[s][i] = q[kKeyScales == NC ? (gq * NC + i) / kPerScale
+                                          : (NC % kPerScale == 0 ? gq * kKeyScales + i : gq * NC / kPerScale)];
+      }
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        const int piece = min(lane + 64 * x, kTile * NC - 1), token = piece / NC, c = piece - token * NC;
+        const uint64_t vr = row_at(p, token);
+        load_words<4>(g.vc + vr * (D / 2) + 16 * c, t.v[x]);
+        const uint8_t *q = g.vs + vr * (D / kBlock4<NV>);
+        t.vs[x] = NV ? (uint32_t)q[2 * c] | (uint32_t)q[2 * c + 1] << 8 : q[c];
+      }
+    };
+
+    // q: this lane's quarter of the head, as B operands
     ushortx8 qf[NC][PQ];
+    Place<HALVES> now, next;
+    find(from + wave * kTile, now);
     {
-      const TQ *p = (const TQ *)g.q + row * g.ldq + (int64_t)h * D + gq * (D / 4);
+      const TQ *p = (const TQ *)g.q + (row_there ? row * g.ldq + (int64_t)h * D : start * g.ldq) + gq * (D / 4);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (row_there) load8(p + 8 * i, v);
+        float v[8];
+        load8(p + 8 * i, v);
         parts_bf16<PQ>(v, qf[i]);
       }
     }
     const float scale = NV ? g.scale * *g.k_whole : g.scale;
     uint8_t *mine = lds + wave * kVBytes;
-    const int32_t *table = g.b.table + seq * g.b.ldt;
-
-    // row of the cache of token (tile base + lane % 32)
-    auto row_of = [&](int64_t base) -> uint32_t {
-      const int64_t t = base + (lane & 31);
-      if (t >= to) return kNoRow;
-      const uint32_t pg = g.p.by_page.div((uint32_t)t);
-      const int page = table[pg];
-      if (page < 0 || page >= g.p.pages) return kBadRow;
-      return ((uint32_t)page * g.p.heads + kvh) * g.p.page_size + ((uint32_t)t - pg * g.p.by_page.d);
-    };
-    struct Tile {
-      uint32_t k[2][NC], ks[2][kKeyScales];
-      uint32_t v[kV][4], vs[kV];
-      uint32_t row;
-    };
-    auto load = [&](uint32_t row32, Tile &t) {
-      t.row = row32;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t kr = __shfl(row32, 16 * s + r, 64);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) t.k[s][i] = 0u;
-#pragma unroll
-        for (int i = 0; i < kKeyScales; ++i) t.ks[s][i] = 0u;
-        if (kr < kBadRow) {
-          load_words<NC>(g.kc + (int64_t)kr * (D / 2) + gq * (D / 8), t.k[s]);
-          const uint8_t *p = g.ks + (int64_t)kr * (D / kBlock4<NV>);
-#pragma unroll
-          for (int i = 0; i < kKeyScales; ++i)
-            t.ks[s][i] = p[kKeyScales == NC ? (gq * NC + i) / kUnitsPerScale
-                                            : (NC % kUnitsPerScale == 0 ? gq * kKeyScales + i : gq * NC / kUnitsPerScale)];
-        }
-      }
+    int base = from + wave * kTile;
+    Tile t;
+    place(base, now);
+    find(base + kStepTokens, next);
+    load(now, t);
+    for (; base < to; base += kStepTokens) {
+      const bool bad0 = now.bad[0], bad1 = now.bad[HALVES ? 1 : 0];
+      // v to LDS as bf16; behind the last token, where the cache may hold
+      // anything, the scale of zero (mxfp4: 2^-127): finite, and times p = 0
 #pragma unroll
       for (int x = 0; x < kV; ++x) {
         const int piece = lane + 64 * x, token = piece / NC, c = piece - token * NC;
-        const uint32_t vr = __shfl(row32, token & 31, 64);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t.v[x][i] = 0u;
-        t.vs[x] = 0u;
-        if (piece < kTile * NC && vr < kBadRow) {
-          load_words<4>(g.vc + (int64_t)vr * (D / 2) + 16 * c, t.v[x]);
-          const uint8_t *p = g.vs + (int64_t)vr * (D / kBlock4<NV>);
-          t.vs[x] = NV ? (uint32_t)p[2 * c] | (uint32_t)p[2 * c + 1] << 8 : p[c];
-        }
-      }
-    };
-
-    auto compute = [&](const Tile &t, int64_t base) {
-      // v to LDS as bf16
-#pragma unroll
-      for (int x = 0; x < kV; ++x) {
-        const int piece = lane + 64 * x, token = piece / NC, c = piece - token * NC;
-        if (piece < kTile * NC) {
-          const float s0 = scale4<NV>(t.vs[x] & 255u), s1 = NV ? scale4<NV>(t.vs[x] >> 8) : s0;
-          ushortx8 *dst = (ushortx8 *)(mine + token * (kStride * 2) + c * 64);
+        const uint32_t byte = base + token < to ? t.vs[x] : 0u;
+        const float s0 = scale4<NV>(byte & 255u), s1 = NV ? scale4<NV>(byte >> 8) : s0;
+        ushortx8 *dst = (ushortx8 *)(mine + token * kStride + c * 64);
+        if (kTile * NC % 64 == 0 || piece < kTile * NC) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = decode4<NV>(t.v[x][i], i < 2 ? s0 : s1);
         }
@@ -366,7 +415,7 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
         floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          const int k = kKeyScales == NC ? i : (NC % kUnitsPerScale == 0 ? i / kUnitsPerScale : 0);
+          const int k = kKeyScales == NC ? i : (NC % kPerScale == 0 ? i / kPerScale : 0);
           const ushortx8 a = decode4<NV>(t.k[s][i], scale4<NV>(t.ks[s][k]));
 #pragma unroll
           for (int part = PQ - 1; part >= 0; --part) acc = mfma16_bf16(a, qf[i][part], acc);
@@ -374,26 +423,30 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[4 * s + i] = acc[i] * scale;
       }
-      if (base < begin || base + kTile > end) {
+      // the codes are used up: the next ones are under way during the rest,
+      // and the entries of those after them
+      place(base + kStepTokens, next);
+      const Place<HALVES> was = now;
+      now = next;
+      find(base + 2 * kStepTokens, next);
+      load(now, t);
+
+      if (__ballot(base < begin || base + kTile > end)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int64_t token = base + 16 * (i / 4) + 4 * gq + i % 4;
+          const int token = base + 16 * (i / 4) + 4 * gq + i % 4;
           p[i] = token >= begin && token < end ? p[i] : -INFINITY;
         }
       }
-      if (__ballot(t.row == kBadRow)) {  // a page outside the cache: its tokens have no scores
+      if (__ballot(bad0 || bad1)) {  // a page outside the cache: its tokens have no scores
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t there = __shfl(t.row, 16 * (i / 4) + 4 * gq + i % 4, 64);
-          p[i] = there == kBadRow && p[i] != -INFINITY ? nan_f32() : p[i];
+          const bool bad = HALVES ? was.bad[i / 4] : __shfl((int)was.bad[0], 16 * (i / 4) + 4 * gq + i % 4, 64) != 0;
+          p[i] = bad && p[i] != -INFINITY ? nan_f32() : p[i];
         }
       }
-      float m = p[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, p[i]);
-      m = fmaxf(m, __shfl_xor(m, 16, 64));
-      m = fmaxf(m, __shfl_xor(m, 32, 64));
-      m = fmaxf(m, top);
+      float m = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+      m = fmaxf(quarter_max(m), top);
       if (__ballot(m != top)) {
         // nothing seen before: O is zero, and exp2(-inf) leaves it so
         const float by = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - m);
@@ -418,9 +471,9 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
       for (int i = 0; i < 2 * NC; ++i) {
         typedef short shortx4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) shortx4 *lds_ptr;
-        const uint8_t *src = mine + (4 * gq + r / 4) * (kStride * 2) + 32 * i + 8 * (r & 3);
+        const uint8_t *src = mine + (4 * gq + r / 4) * kStride + 32 * i + 8 * (r & 3);
         const shortx4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)src);
-        const shortx4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(src + 16 * (kStride * 2)));
+        const shortx4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(src + 16 * kStride));
         ushortx8 a;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -433,26 +486,11 @@ __global__ void __launch_bounds__(64 * kWaves) attend_kernel(AttendArgs g) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    };
-
-    constexpr int64_t kNext = kStepTokens;
-    int64_t base = from + (int64_t)wave * kTile;
-    if (base < to) {
-      Tile cur, next;
-      load(row_of(base), cur);
-      uint32_t ahead = row_of(base + kNext);
-      for (; base < to; base += kNext) {
-        load(ahead, next);
-        ahead = row_of(base + 2 * kNext);
-        compute(cur, base);
-        cur = next;
-      }
     }
   }
 
   // ---- join the waves
-  sum += __shfl_xor(sum, 16, 64);
-  sum += __shfl_xor(sum, 32, 64);
+  sum = quarter_sum(sum);
   __syncthreads();
   float *mo = (float *)(lds + wave * kVBytes);
   float2 *ms = (float2 *)(lds + wave * kVBytes + kRowsQ * kOStride * 4);
@@ -514,34 +552,71 @@ struct JoinArgs {
   int o_bf16;
   float *lse;
 };
-__global__ void __launch_bounds__(256) join_kernel(JoinArgs g) {
-  const int h = blockIdx.x % g.heads;
+// Four elements a thread, as many splits at once as the workgroup has threads
+// for; their weights are formed first, one split to a thread.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs g) {
+  __shared__ float weight[kMaxSplits];
+  __shared__ float2 wave_stat[kJoinThreads / 64];
+  __shared__ int wave_last[kJoinThreads / 64];
+  __shared__ floatx4 sums[kJoinThreads];
+  const int h = blockIdx.x % g.heads, t = threadIdx.x;
   const int64_t row = blockIdx.x / g.heads;
   const int seq = sequence_of(g.b, row);
   if (seq < 0) return;
   const int64_t start = g.b.starts ? g.b.starts[seq] : row, stop = g.b.starts ? g.b.starts[seq + 1] : row + 1;
   if (start < 0 || stop > g.tokens || row - start >= g.max_new) return;
-  float m = -INFINITY;
-  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.stat[((int64_t)s * g.tokens + row) * g.heads + h].x);
-  float l = 0.0f;
-  for (int d = threadIdx.x; d < g.dim; d += blockDim.x) {
-    float v = 0.0f;
-    l = 0.0f;
-    for (int s = 0; s < g.splits; ++s) {
-      const int64_t slot = ((int64_t)s * g.tokens + row) * g.heads + h;
-      const float2 st = g.stat[slot];
-      if (st.x == -INFINITY && st.y == 0.0f) continue;  // nothing seen, and nothing written
-      const float by = st.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.x - m);
-      l += st.y * by;
-      v += g.part[slot * g.dim + d] * by;
-    }
-    const float w = g.v_whole ? *g.v_whole : 1.0f;
-    const float y = l == 0.0f ? 0.0f : v * (w / l);
-    const int64_t out = row * g.ldo + (int64_t)h * g.dim + d;
-    if (g.o_bf16) ((unsigned short *)g.o)[out] = (unsigned short)pack_bf16(y, 0.0f);
-    else ((float *)g.o)[out] = y;
+  const int64_t step = g.tokens * g.heads, slot = row * g.heads + h;
+  // (-inf, 0): nothing seen. Splits that wrote nothing follow the others, so
+  // all up to the last one that saw something have been written.
+  const float2 st = t < g.splits ? g.stat[t * step + slot] : make_float2(-INFINITY, 0.0f);
+  float m = st.x;
+  int last = st.x == -INFINITY && st.y == 0.0f ? 0 : t + 1;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    last = max(last, __shfl_xor(last, o, 64));
   }
-  if (g.lse && threadIdx.x == 0) g.lse[row * g.heads + h] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+  if ((t & 63) == 0) {
+    wave_stat[t >> 6].x = m;
+    wave_last[t >> 6] = last;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) {
+    m = fmaxf(m, wave_stat[w].x);
+    last = max(last, wave_last[w]);
+  }
+  const float by = st.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.x - m);
+  weight[t] = by;
+  float l = st.y * by;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, 64);
+  if ((t & 63) == 0) wave_stat[t >> 6].y = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) l += wave_stat[w].y;
+  const int cols = g.dim / 4, groups = kJoinThreads / cols, grp = t / cols, d = (t - grp * cols) * 4;
+  floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (grp < groups) {
+    const float *p = g.part + slot * g.dim + d;
+#pragma unroll 4
+    for (int s = grp; s < last; s += groups) v += *(const floatx4 *)(p + s * step * g.dim) * weight[s];
+  }
+  sums[t] = v;
+  __syncthreads();
+  if (grp) return;
+  for (int k = 1; k < groups; ++k) v += sums[k * cols + t];
+  const float w = g.v_whole ? *g.v_whole : 1.0f;
+  const float inv = l == 0.0f ? 0.0f : w / l;
+  const int64_t out = row * g.ldo + (int64_t)h * g.dim + d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (g.o_bf16) ((unsigned short *)g.o)[out + i] = (unsigned short)pack_bf16(v[i] * inv, 0.0f);
+    else ((float *)g.o)[out + i] = v[i] * inv;
+  }
+  if (g.lse && t == 0) g.lse[slot] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // ------------------------------------------------------------------- host
@@ -586,7 +661,7 @@ void batch_in(Operands &o, const metis_kv_batch_t *b) {
 
 // Tokens of a workgroup: as many as leave `kTarget` workgroups, had every
 // sequence the largest length, in whole steps of its waves.
-constexpr int kTarget = 4096, kMaxSplits = 256;
+constexpr int kTarget = 4096;
 struct Splits {
   int splits, chunk;
 };
@@ -621,14 +696,21 @@ AttendPlan plan_of(void *ws, int64_t tokens, int32_t heads, int32_t max_new, int
   return p;
 }
 
-template <bool NV, int PQ, int PP, typename TQ> bool attend_by_dim(const AttendArgs &g, int dim, unsigned grid, hipStream_t stream) {
-#define METIS_CASE(NC)                                                                  \
-  case NC: attend_kernel<NV, NC, PQ, PP, TQ><<<grid, 64 * kWaves, 0, stream>>>(g); return true;
+template <bool NV, int PQ, int PP, typename TQ, bool HALVES>
+void attend_by_dim(const AttendArgs &g, int dim, unsigned grid, hipStream_t stream) {
+#define METIS_CASE(NC)                                                                             \
+  case NC: attend_kernel<NV, NC, PQ, PP, TQ, HALVES><<<grid, 64 * kWaves, 0, stream>>>(g); break;
   switch (dim / 32) {
     METIS_CASE(1) METIS_CASE(2) METIS_CASE(3) METIS_CASE(4) METIS_CASE(5) METIS_CASE(6) METIS_CASE(7) METIS_CASE(8)
   }
 #undef METIS_CASE
-  return false;
+}
+template <int PQ, int PP, typename TQ> void attend(const AttendArgs &g, bool nv, int dim, unsigned grid, hipStream_t stream) {
+  if (g.p.page_size % 16 == 0) {
+    nv ? attend_by_dim<true, PQ, PP, TQ, true>(g, dim, grid, stream) : attend_by_dim<false, PQ, PP, TQ, true>(g, dim, grid, stream);
+  } else {
+    nv ? attend_by_dim<true, PQ, PP, TQ, false>(g, dim, grid, stream) : attend_by_dim<false, PQ, PP, TQ, false>(g, dim, grid, stream);
+  }
 }
 
 metis_status_t check_attention(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
@@ -769,15 +851,9 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
   g.stat = p.stat;
   const unsigned grid = (unsigned)((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits);
   const int dim = (int)cache->k.cols;
-  if (dt == METIS_BF16 && odt == METIS_BF16) {
-    nv ? attend_by_dim<true, 1, 2, unsigned short>(g, dim, grid, stream)
-       : attend_by_dim<false, 1, 2, unsigned short>(g, dim, grid, stream);
-  } else if (dt == METIS_BF16) {
-    nv ? attend_by_dim<true, 1, 3, unsigned short>(g, dim, grid, stream)
-       : attend_by_dim<false, 1, 3, unsigned short>(g, dim, grid, stream);
-  } else {
-    nv ? attend_by_dim<true, 3, 3, float>(g, dim, grid, stream) : attend_by_dim<false, 3, 3, float>(g, dim, grid, stream);
-  }
+  if (dt == METIS_F32) attend<3, 3, float>(g, nv, dim, grid, stream);
+  else if (odt == METIS_F32) attend<1, 3, unsigned short>(g, nv, dim, grid, stream);
+  else attend<1, 2, unsigned short>(g, nv, dim, grid, stream);
   if (p.s.splits > 1) {
     JoinArgs jn = {};
     jn.b = g.b;
@@ -793,7 +869,7 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
     jn.ldo = ldo;
     jn.o_bf16 = g.o_bf16;
     jn.lse = lse;
-    join_kernel<<<(unsigned)(tokens * heads), dim > 64 ? (dim > 128 ? 256 : 128) : 64, 0, stream>>>(jn);
+    join_kernel<<<(unsigned)(tokens * heads), kJoinThreads, 0, stream>>>(jn);
   }
   METIS_LAUNCH_CHECK();
   return METIS_OK;

@@ -545,7 +545,7 @@ typedef struct {
  *           new token each, row s of sequence s. Rows outside belong to none.
  * A new token i of n of a sequence of length L is at position L - n + i;
  * negative positions are no tokens. A sequence whose rows reach outside the
- * call's tokens is left out. max_pages * page_size <= 2^29. */
+ * call's tokens is left out. max_pages * page_size <= 2^28. */
 typedef struct {
   const int32_t *table, *lengths, *starts;
   int64_t ldt;
