@@ -26,9 +26,10 @@ namespace {
 
 constexpr int kRows = 16;       // rows of W in a workgroup
 constexpr int kStep = 128;      // columns of a wave's step
-constexpr int kTokens = 64;     // tokens of a pass over W
+constexpr int kHeldGrid = 512;  // workgroups that take several tiles of rows
 constexpr int kMaxRank = 96;
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 16, kHeldWaves = 12;
+constexpr int kSlices = 8;      // workgroups that share the columns of z's sums
 constexpr int kManyRows = 12288;
 
 struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` columns
@@ -39,74 +40,94 @@ struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` column
 
 struct MainArgs {
   Weight w;
-  const unsigned short *x;  // P planes of tokens x cols bf16
-  int64_t ldx, plane;
-  int tokens;
+  const unsigned short *x;  // bf16, a row for each column of the products
+  int64_t ldx;
+  int tokens, parts;  // a token's bf16 parts are `parts` rows of x in a row
   void *y;
   int64_t ldy;
   int y_bf16;
-  // low-rank term: U^T (rank x rows), z as three bf16 parts of 64 x rank_pad
+  // low-rank term: U^T (rank x rows); z as kSlices sums over columns, each
+  // tokens x rank_pad, their factors S not yet in
   Weight u;
-  const unsigned short *z;
-  int rank;
-  // what a launch that forms z multiplies its sums by, and where it puts them
+  float *z;
   const float *s;
-  unsigned short *z_out;
+  int rank;
+  int tiles;  // sixteens of rows (held): workgroup b has tiles b, b + gridDim.x, ...
+  __host__ __device__ int columns() const { return tokens * parts; }
 };
 
-// z is kept as three planes of kTokens rows.
 __host__ __device__ inline int rank_pad(int rank) { return (rank + 31) / 32 * 32; }
 
-// The 32 elements of row `row` from column c on, as loaded.
-struct Codes {
+// A step of one row: 128 columns of which a lane loads the 32 from 32 q on, and
+// the scales of all of them.
+template <bool NV> struct Codes {
   uint32_t w[4];
-  uint32_t scale;  // MXFP4: one byte; NVFP4: two
+  uint32_t scale[NV ? 2 : 1];  // four blocks of 32 or eight of 16
 };
 template <bool NV, bool EDGE>
-__device__ __forceinline__ void load_codes(const Weight &w, bool there, int64_t row, int c, Codes &r) {
-  const uint8_t *p = w.codes + row * (w.cols / 2) + c / 2;
-  const uint8_t *s = w.scales + row * (w.cols / kBlock4<NV>) + c / kBlock4<NV>;
-  if (!EDGE || (there && c + 32 <= w.cols)) {
+__device__ __forceinline__ void load_codes(const Weight &w, int64_t row, int c, int q, Codes<NV> &r) {
+  constexpr int B = kBlock4<NV>;
+  const uint8_t *p = w.codes + row * (w.cols / 2) + c / 2 + 16 * q;
+  const uint8_t *s = w.scales + row * (w.cols / B) + c / B;
+  if (!EDGE) {
     const u32x4_a1 v = *(const u32x4_a1 *)p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.w[i] = v[i];
-    r.scale = s[0];
-    if (NV) r.scale |= (uint32_t)s[1] << 8;
-  } else {
-    r.w[0] = r.w[1] = r.w[2] = r.w[3] = r.scale = 0u;
-    if (NV && there && c < w.cols) {  // the last sixteen columns
+    if (NV) {
+      const u32x2_a1 t = *(const u32x2_a1 *)s;
+      r.scale[0] = t[0];
+      r.scale[NV] = t[1];
+    } else {
+      typedef uint32_t u32_a1 __attribute__((aligned(1)));
+      r.scale[0] = *(const u32_a1 *)s;
+    }
+  } else {  // the row ends here: whole blocks of it are left
+    r.w[0] = r.w[1] = r.w[2] = r.w[3] = r.scale[0] = r.scale[NV] = 0u;
+    if (c + 32 * q + 32 <= w.cols) {
+      const u32x4_a1 v = *(const u32x4_a1 *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[i] = v[i];
+    } else if (NV && c + 32 * q < w.cols) {
       const u32x2_a1 v = *(const u32x2_a1 *)p;
       r.w[0] = v[0];
       r.w[1] = v[1];
-      r.scale = s[0];
     }
+#pragma unroll
+    for (int i = 0; i < kStep / B; ++i)
+      if (c + B * i < w.cols) r.scale[i / 4] |= (uint32_t)s[i] << (8 * (i % 4));
   }
 }
 
-template <bool NV> __device__ __forceinline__ void scales_of(const Codes &c, float (&s)[2]) {
-  s[0] = scale4<NV>(c.scale & 255u);
-  s[1] = NV ? scale4<NV>(c.scale >> 8) : s[0];
+// Word u of lane q to word q of lane u (of the four lanes that share a row):
+// a lane then has columns 32 u + 8 q .. + 7 as word u, so that the four lanes'
+// pieces of x are 64 bytes in a row. (With x read where the codes lie, sixteen
+// bytes of every 64, 16 tokens x 4096 -> 14336 took 21.6 us.)
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  w[0] = c[0];
+  w[1] = c[1];
+  w[2] = d[0];
+  w[3] = d[1];
+}
+// The scale of word u after that, in lane q.
+template <bool NV> __device__ __forceinline__ float scale_of(const Codes<NV> &c, int u, int q) {
+  if (NV) return scale4<NV>((c.scale[u / 2] >> (16 * (u % 2) + 8 * (q >> 1))) & 255u);
+  return scale4<NV>((c.scale[0] >> (8 * u)) & 255u);
 }
 
 // 32 of the rank's terms for sixteen rows, as loaded.
 struct Low {
   uint32_t code[8], scale[8];
-  u32x4_a1 z[3];
 };
-template <bool NV>
-__device__ __forceinline__ void load_low(const MainArgs &g, int64_t row, int k0, Low &w) {
+template <bool NV> __device__ __forceinline__ void load_low(const MainArgs &g, int64_t row, int k0, Low &w) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t k = min(k0 + j, g.rank - 1);
     w.code[j] = g.u.codes[k * (g.u.cols / 2) + row / 2];
     w.scale[j] = g.u.scales[k * (g.u.cols / kBlock4<NV>) + row / kBlock4<NV>];
-  }
-}
-__device__ __forceinline__ void load_z(const MainArgs &g, int token, int k0, Low &w) {
-#pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    w.z[p] = u32x4_a1{0u, 0u, 0u, 0u};
-    if (token < g.tokens) w.z[p] = *(const u32x4_a1 *)(g.z + ((int64_t)p * kTokens + token) * rank_pad(g.rank) + k0);
   }
 }
 // Their eight elements of U in a lane. Terms behind the rank are zero.
@@ -128,146 +149,50 @@ template <bool NV> __device__ __forceinline__ ushortx8 low_rows(const MainArgs &
   const intx4 v = {(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
   return __builtin_bit_cast(ushortx8, v);
 }
-
-// P: bf16 parts of x. NT: sixteens of tokens. RT: sixteens of rows. Z: the
-// launch that forms z.
-template <bool NV, int P, int NT, int RT, bool Z>
-__global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
-  extern __shared__ float sums[];  // waves x RT x NT x 16 tokens x 16 rows
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int row0 = blockIdx.x * kRows * RT, cols = g.w.cols;
-  int64_t row[RT];  // rows behind the last one: its codes again, not stored
+// z[k0 .. k0 + 7] of the token whose first part is column c of the products, its
+// slices joined in order, as three bf16 parts. The columns of its other parts
+// get none.
+__device__ __forceinline__ void load_z(const MainArgs &g, int c, int k0, ushortx8 (&part)[3]) {
+  const int pad = rank_pad(g.rank), token = c / g.parts;
+  const bool there = token * g.parts == c && token < g.tokens;
+  const float *p = g.z + (int64_t)min(token, g.tokens - 1) * pad + k0;
+  floatx4 a[kSlices], b[kSlices];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) row[t] = min(row0 + 16 * t + r, g.w.rows - 1);
-  floatx4 acc[RT][NT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[t][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  // the rank's terms: 32 of them for sixteen rows are a task, under way from
-  // the start (what a wave has beyond one task, at its end)
-  const int chunks = Z ? 0 : (g.rank + 31) / 32, tasks = chunks * RT;
-  Low low = {};
-  if (!Z && wave < tasks) {
-    load_low<NV>(g, min((int64_t)row0 + 16 * (wave / chunks) + r, (int64_t)g.w.rows - 1), 32 * (wave % chunks) + 8 * q, low);
-    if (NT == 1) load_z(g, r, 32 * (wave % chunks) + 8 * q, low);
+  for (int i = 0; i < kSlices; ++i) {
+    a[i] = *(const floatx4 *)(p + (int64_t)i * g.tokens * pad);
+    b[i] = *(const floatx4 *)(p + (int64_t)i * g.tokens * pad + 4);
   }
-
-  // N steps of 128 columns, `waves` apart: all their codes are asked for before
-  // the first of them is used, x (which the L2 holds) for XU units of eight
-  // columns at a time, as many as registers allow
-  constexpr int kX = 16 / (NT * P);
-  auto run = [&](auto count, auto edge, int st) {
-    constexpr int N = decltype(count)::value;
-    constexpr bool EDGE = decltype(edge)::value;
-    constexpr int XU = kX >= 8 ? (N > 1 ? 8 : 4) : kX >= 4 ? 4 : kX >= 2 ? 2 : 1;
-    Codes c[N][RT];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int t = 0; t < RT; ++t) load_codes<NV, EDGE>(g.w, true, row[t], (st + i * waves) * kStep + 32 * q, c[i][t]);
-#pragma unroll
-    for (int u0 = 0; u0 < 4 * N; u0 += XU) {
-      u32x4_a1 x[XU][NT][P];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int token = 16 * n + r;
-        const unsigned short *p = g.x + (int64_t)token * g.ldx + 32 * q;
-#pragma unroll
-        for (int u = 0; u < XU; ++u)
-#pragma unroll
-          for (int k = 0; k < P; ++k) x[u][n][k] = u32x4_a1{0u, 0u, 0u, 0u};
-        if (token < g.tokens) {
-#pragma unroll
-          for (int u = 0; u < XU; ++u) {
-            const int at = (st + (u0 + u) / 4 * waves) * kStep + 8 * ((u0 + u) % 4);
-            if (!EDGE || at + 32 * q < cols) {
-#pragma unroll
-              for (int k = 0; k < P; ++k) x[u][n][k] = *(const u32x4_a1 *)(p + k * g.plane + at);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int u = 0; u < XU; ++u) {
-          const int i = (u0 + u) / 4, e = (u0 + u) % 4;
-          float s[2];
-          scales_of<NV>(c[i][t], s);
-          const ushortx8 a = decode4<NV>(c[i][t].w[e], s[e / 2]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < P; ++k)
-              acc[t][n] = mfma16_bf16(a, __builtin_bit_cast(ushortx8, x[u][n][k]), acc[t][n]);
-        }
-    }
-  };
-  // the steps are dealt to the waves in turn; the last one may end early
-  const int steps = (cols + kStep - 1) / kStep, whole = cols / kStep;
-  constexpr int kAhead = RT == 1 && NT * P == 1 ? 4 : 2;
-  int st = wave;
-  for (; st + (kAhead - 1) * waves < whole; st += kAhead * waves)
-    run(std::integral_constant<int, kAhead>(), std::false_type(), st);
-  if (kAhead == 4 && st + waves < whole) {
-    run(std::integral_constant<int, 2>(), std::false_type(), st);
-    st += 2 * waves;
+  for (int i = 1; i < kSlices; ++i) {
+    a[0] += a[i];
+    b[0] += b[i];
   }
-  for (; st < steps; st += waves) run(std::integral_constant<int, 1>(), std::true_type(), st);
-  if (NV) {
-    const float whole_scale = *g.w.whole;
+  float v[8];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[t][n] *= whole_scale;
-  }
+  for (int i = 0; i < 8; ++i) v[i] = there ? (i < 4 ? a[0][i % 4] : b[0][i % 4]) * g.s[min(k0 + i, g.rank - 1)] : 0.0f;
+  parts_bf16<3>(v, part);
+}
 
-  if (!Z) {
-    const float whole_scale = NV && tasks ? *g.u.whole : 1.0f;
-    for (int task = wave; task < tasks; task += waves) {
-      const int at = task / chunks, k0 = 32 * (task % chunks) + 8 * q;
-      const int64_t i = min((int64_t)row0 + 16 * at + r, (int64_t)g.w.rows - 1);
-      if (task != wave) load_low<NV>(g, i, k0, low);
-      const ushortx8 a = low_rows<NV>(g, low, i, k0);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (NT > 1 || task != wave) load_z(g, 16 * n + r, k0, low);
-        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int p = 2; p >= 0; --p) v = mfma16_bf16(a, __builtin_bit_cast(ushortx8, low.z[p]), v);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          if (t == at) acc[t][n] += v * whole_scale;
-      }
-    }
-  }
+// x for column c of the products (behind the last one: it again), from column
+// 8 q of W on.
+__device__ __forceinline__ const unsigned short *x_row(const MainArgs &g, int c, int q) {
+  return g.x + (int64_t)min(c, g.columns() - 1) * g.ldx + 8 * q;
+}
 
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *(floatx4 *)(sums + ((((wave * RT + t) * NT + n) * 16 + r) * 16 + 4 * q)) = acc[t][n];
-  __syncthreads();
-  for (int e = threadIdx.x; e < RT * NT * 256; e += blockDim.x) {
-    const int t = e / (NT * 256), token = (e >> 4) % (NT * 16), i = row0 + 16 * t + (e & 15);
-    if (token >= g.tokens) continue;
+// The sum over waves and over a token's parts: rows row0 .. + 15 of W, `sums`
+// being waves x (16 NT columns x 16 rows), `stride` floats from wave to wave.
+template <bool Z>
+__device__ __forceinline__ void join_waves(const MainArgs &g, const float *sums, int waves, int stride, int row0) {
+  for (int e = threadIdx.x; e < g.tokens * 16; e += blockDim.x) {
+    const int token = e >> 4, i = row0 + (e & 15);
     float v = 0.0f;
+    for (int p = 0; p < g.parts; ++p) {
+      const float *s = sums + (token * g.parts + p) * 16 + (e & 15);
 #pragma unroll 4
-    for (int k = 0; k < waves; ++k) v += sums[k * RT * NT * 256 + e];
-    if (Z) {
-      const int pad = rank_pad(g.w.rows);
-      if (i < pad) {  // three bf16 parts; zeros behind the rank
-        float z = i < g.w.rows ? v * g.s[i] : 0.0f;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const uint32_t cut = p < 2 ? __float_as_uint(z) & 0xFFFF0000u : pack_bf16(0.0f, z);
-          g.z_out[((int64_t)p * kTokens + token) * pad + i] = (unsigned short)(cut >> 16);
-          z -= __uint_as_float(cut);
-        }
-      }
+      for (int k = 0; k < waves; ++k) v += s[k * stride];
+    }
+    if (Z) {  // rows behind the rank hold the last one's sum; their U is zero
+      g.z[((int64_t)blockIdx.y * g.tokens + token) * rank_pad(g.w.rows) + i] = v;
     } else if (i < g.w.rows) {
       const int64_t at = (int64_t)token * g.ldy + i;
       if (g.y_bf16) ((unsigned short *)g.y)[at] = (unsigned short)pack_bf16(v, 0.0f);
@@ -276,58 +201,258 @@ __global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
   }
 }
 
-// fp32 x as three planes of bf16 parts.
-__global__ void __launch_bounds__(256) parts_kernel(const float *x, int64_t ldx, int cols, unsigned short *out, int64_t plane) {
+// Columns of the products belong to one token and rows to one row of W, so what
+// a lane computes for columns and rows behind the last ones is not masked (it
+// loads the last one again), only not stored.
+
+// ---- few columns of W, up to sixteen columns of the products: x stays in
+// registers, S steps of a wave, while the workgroup goes through its tiles of
+// sixteen rows; the next tile's codes are under way while one is worked on.
+template <bool NV, int S> struct Held {
+  Codes<NV> c[S];
+};
+template <bool NV, int S>
+__global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) {
+  __shared__ float sums[2][kHeldWaves][256];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all_waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, cols = g.w.cols;
+  const int chunks = (g.rank + 31) / 32, waves = all_waves - chunks;  // the last waves have the rank's terms
+  const int steps = (cols + kStep - 1) / kStep, first = wave * S;
+  auto row_of = [&](int tile) { return (int64_t)min(tile * kRows + r, g.w.rows - 1); };
+  if (wave < waves) {
+    // a wave whose last step ends early, or whose steps are fewer, takes zeros
+    // for the codes; x is then the last eight columns again
+    const bool edge = (first + S) * kStep > cols;
+    auto load = [&](int tile, Held<NV, S> &h) {
+      const int64_t row = row_of(tile);
+      if (!edge) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) load_codes<NV, false>(g.w, row, (first + i) * kStep, q, h.c[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) load_codes<NV, true>(g.w, row, (first + i) * kStep, q, h.c[i]);
+      }
+    };
+    Held<NV, S> h, next;
+    load(blockIdx.x, h);
+    ushortx8 x[S][4];
+    const unsigned short *p = x_row(g, r, q);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        x[i][u] = __builtin_bit_cast(ushortx8, *(const u32x4_a1 *)(p + min((first + i) * kStep + 32 * u, cols - 8 - 8 * q)));
+    const float whole = NV ? *g.w.whole : 1.0f;
+    int buf = 0;
+    for (int tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+      const bool more = tile + (int)gridDim.x < g.tiles;
+      if (more) load(tile + gridDim.x, next);
+      floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        transpose4(h.c[i].w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc = mfma16_bf16(decode4<NV>(h.c[i].w[u], scale_of<NV>(h.c[i], u, q)), x[i][u], acc);
+      }
+      if (NV) acc *= whole;
+      *(floatx4 *)&sums[buf][wave][16 * r + 4 * q] = acc;
+      __syncthreads();
+      join_waves<false>(g, sums[buf][0], all_waves, 256, tile * kRows);
+      buf ^= 1;
+      h = next;
+    }
+  } else {
+    const int k0 = 32 * (wave - waves) + 8 * q;
+    Low low, next;
+    load_low<NV>(g, row_of(blockIdx.x), k0, low);
+    ushortx8 z[3];
+    load_z(g, r, k0, z);
+    const float whole = NV ? *g.u.whole : 1.0f;
+    int buf = 0;
+    for (int tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+      const bool more = tile + (int)gridDim.x < g.tiles;
+      if (more) load_low<NV>(g, row_of(tile + gridDim.x), k0, next);
+      const ushortx8 a = low_rows<NV>(g, low, row_of(tile), k0);
+      floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 2; i >= 0; --i) acc = mfma16_bf16(a, z[i], acc);
+      if (NV) acc *= whole;
+      *(floatx4 *)&sums[buf][wave][16 * r + 4 * q] = acc;
+      __syncthreads();
+      join_waves<false>(g, sums[buf][0], all_waves, 256, tile * kRows);
+      buf ^= 1;
+      low = next;
+    }
+  }
+}
+
+// ---- any number of columns of W: x is read along with the codes.
+// The sums over a wave's columns. NT: sixteens of columns of the products. RT:
+// sixteens of rows. Z: the launch that forms z.
+template <bool NV, int NT, int RT, bool Z>
+__device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, int waves, int r, int q,
+                                        floatx4 (&acc)[RT][NT]) {
+  const int cols = g.w.cols;
+  int64_t row[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) row[t] = min(row0 + 16 * t + r, g.w.rows - 1);
+  const unsigned short *x_of[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x_of[n] = x_row(g, 16 * n + r, q);
+
+  // N steps of 128 columns in a row: all their codes are asked for before the
+  // first of them is used, x (which the L2 holds) XU units of 32 columns at a
+  // time, as many as registers allow
+  constexpr int kX = 16 / NT;
+  auto run = [&](auto count, auto edge, int st) {
+    constexpr int N = decltype(count)::value;
+    constexpr bool EDGE = decltype(edge)::value;
+    constexpr int XU = kX >= 8 ? (N > 1 ? 8 : 4) : kX >= 4 ? 4 : kX >= 2 ? 2 : 1;
+    Codes<NV> c[N][RT];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) load_codes<NV, EDGE>(g.w, row[t], (st + i) * kStep, q, c[i][t]);
+#pragma unroll
+    for (int u0 = 0; u0 < 4 * N; u0 += XU) {
+      u32x4_a1 x[XU][NT];
+#pragma unroll
+      for (int u = 0; u < XU; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int at = (st + (u0 + u) / 4) * kStep + 32 * ((u0 + u) % 4);
+          // behind the last column the codes are zeros: x there is the last eight again
+          x[u][n] = *(const u32x4_a1 *)(x_of[n] + (EDGE ? min(at, cols - 8 - 8 * q) : at));
+        }
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int u = 0; u < XU; ++u) {
+          const int i = (u0 + u) / 4, e = (u0 + u) % 4;
+          if (e == 0) transpose4(c[i][t].w);
+          const ushortx8 a = decode4<NV>(c[i][t].w[e], scale_of<NV>(c[i][t], e, q));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[t][n] = mfma16_bf16(a, __builtin_bit_cast(ushortx8, x[u][n]), acc[t][n]);
+        }
+    }
+  };
+  // groups of kAhead steps are dealt to the waves (and workgroups) in turn; what
+  // is left of whole steps likewise, and the last one, which may end early
+  constexpr int kAhead = NT == 1 ? 4 : 2;
+  const int whole = cols / kStep, groups = whole / kAhead;
+  const int me = Z ? wave + waves * (int)blockIdx.y : wave, all = Z ? waves * kSlices : waves;
+  for (int k = me; k < groups; k += all) run(std::integral_constant<int, kAhead>(), std::false_type(), k * kAhead);
+  // the waves that had fewer groups come first
+  const int spare = (me + all - groups % all) % all;
+  for (int st = groups * kAhead + spare; st < whole; st += all)
+    run(std::integral_constant<int, 1>(), std::false_type(), st);
+  if (whole * kStep < cols && spare == (whole - groups * kAhead) % all)
+    run(std::integral_constant<int, 1>(), std::true_type(), whole);
+  if (NV) {
+    const float whole_scale = *g.w.whole;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[t][n] *= whole_scale;
+  }
+}
+
+template <bool NV, int NT, int RT, bool Z>
+__global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
+  extern __shared__ float sums[];  // waves x RT x 16 NT columns x 16 rows
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all_waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int row0 = blockIdx.x * kRows * RT;
+  // the last waves have the rank's terms: 32 of them for sixteen rows each
+  const int chunks = Z ? 0 : (g.rank + 31) / 32, waves = all_waves - chunks * RT;
+  floatx4 acc[RT][NT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[t][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (!Z && wave >= waves) {
+    const int task = wave - waves, at = task / chunks, k0 = 32 * (task - at * chunks) + 8 * q;
+    const int64_t i = min((int64_t)row0 + 16 * at + r, (int64_t)g.w.rows - 1);
+    Low low;
+    load_low<NV>(g, i, k0, low);
+    const float whole_scale = NV ? *g.u.whole : 1.0f;
+    const ushortx8 a = low_rows<NV>(g, low, i, k0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      ushortx8 z[3];
+      load_z(g, 16 * n + r, k0, z);
+      floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 2; p >= 0; --p) v = mfma16_bf16(a, z[p], v);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        if (t == at) acc[t][n] = v * whole_scale;
+    }
+  } else {
+    columns<NV, NT, RT, Z>(g, row0, wave, waves, r, q, acc);
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *(floatx4 *)(sums + ((((wave * RT + t) * NT + n) * 16 + r) * 16 + 4 * q)) = acc[t][n];
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < RT; ++t) join_waves<Z>(g, sums + t * NT * 256, all_waves, RT * NT * 256, row0 + 16 * t);
+}
+
+// fp32 x as three rows of bf16 parts for each of its own.
+__global__ void __launch_bounds__(256) parts_kernel(const float *x, int64_t ldx, int cols, unsigned short *out) {
   const int c = (blockIdx.x * 256 + threadIdx.x) * 8, t = blockIdx.y;
   if (c >= cols) return;  // cols is a multiple of eight
-  const float *p = x + (int64_t)t * ldx + c;
-  const u32x4_a1 a = *(const u32x4_a1 *)p, b = *(const u32x4_a1 *)(p + 4);
   float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __uint_as_float(a[i]);
-    v[4 + i] = __uint_as_float(b[i]);
-  }
+  Raw<float> raw;
+  load_all(x + (int64_t)t * ldx + c, raw);
+  to_f32(raw, v);
   ushortx8 part[3];
   parts_bf16<3>(v, part);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) *(ushortx8 *)(out + k * plane + (int64_t)t * cols + c) = part[k];
+  for (int k = 0; k < 3; ++k) *(ushortx8 *)(out + ((int64_t)t * 3 + k) * cols + c) = part[k];
 }
 
 // ------------------------------------------------------------------- host
-template <bool NV, int P, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, int waves, hipStream_t stream) {
-  gemv_kernel<NV, P, NT, RT, Z><<<(unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows * RT), 64 * waves,
-                                  (size_t)waves * RT * NT * 1024, stream>>>(g);
-}
-// Rows of a workgroup: x is read once for each workgroup, so that many rows are
-// better, as long as there are workgroups for every CU.
-template <bool NV, int P, bool Z> void launch_parts(const MainArgs &g, int waves, hipStream_t stream) {
-  const bool many = !Z && g.w.rows >= kManyRows;
-  if (g.tokens <= 16) {
-    if (many) launch_rows<NV, P, 1, Z ? 1 : 2, Z>(g, waves, stream);
-    else launch_rows<NV, P, 1, 1, Z>(g, waves, stream);
-  } else if (g.tokens <= 32) {
-    if (many) launch_rows<NV, P, 2, Z ? 1 : 2, Z>(g, std::min(waves, 8), stream);
-    else launch_rows<NV, P, 2, 1, Z>(g, std::min(waves, 8), stream);
-  } else {
-    if (many) launch_rows<NV, P, 4, Z ? 1 : 2, Z>(g, std::min(waves, 8), stream);
-    else launch_rows<NV, P, 4, 1, Z>(g, std::min(waves, 8), stream);
-  }
-}
-template <bool Z> void launch(const MainArgs &g, bool nv, bool f32, int waves, hipStream_t stream) {
-  if (nv) {
-    if (f32) launch_parts<true, 3, Z>(g, waves, stream);
-    else launch_parts<true, 1, Z>(g, waves, stream);
-  } else {
-    if (f32) launch_parts<false, 3, Z>(g, waves, stream);
-    else launch_parts<false, 1, Z>(g, waves, stream);
-  }
+template <bool NV, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, int waves, hipStream_t stream) {
+  const dim3 grid((unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows * RT), Z ? kSlices : 1);
+  const int low = Z ? 0 : (int)cdiv(g.rank, 32) * RT;
+  waves = std::min(waves, std::min(kMaxWaves, 64 / (NT * RT)) - low) + low;  // of LDS: 1 KB for a sixteen by sixteen
+  gemv_kernel<NV, NT, RT, Z><<<grid, 64 * waves, (size_t)waves * RT * NT * 1024, stream>>>(g);
 }
 
-int waves_for(int64_t cols, int most) {
-  int w = 4;
-  while (w < most && cols > (int64_t)w * kStep) w *= 2;
-  return w;
+template <bool NV> void launch(MainArgs g, hipStream_t stream) {
+  const int n = g.columns(), cols = g.w.cols, steps = (int)cdiv(cols, kStep), low = (int)cdiv(g.rank, 32);
+  if (n <= 16 && steps <= 32) {
+    const int s = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, waves = std::max(1, (int)cdiv(steps, s));
+    g.tiles = (int)cdiv(g.w.rows, kRows);
+    const unsigned grid = (unsigned)cdiv(g.tiles, cdiv(g.tiles, kHeldGrid));
+    if (s == 1) gemv_held_kernel<NV, 1><<<grid, 64 * (waves + low), 0, stream>>>(g);
+    else if (s == 2) gemv_held_kernel<NV, 2><<<grid, 64 * (waves + low), 0, stream>>>(g);
+    else gemv_held_kernel<NV, 4><<<grid, 64 * (waves + low), 0, stream>>>(g);
+    return;
+  }
+  // rows of a workgroup: x is read once for each, so that many rows are better,
+  // as long as there are workgroups for every CU
+  const bool many = g.w.rows >= kManyRows;
+  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(4, cdiv(steps, NV ? 4 : 4)));
+  if (n <= 16) {
+    if (many) launch_rows<NV, 1, 2, false>(g, waves, stream);
+    else launch_rows<NV, 1, 1, false>(g, waves, stream);
+  } else if (n <= 32) {
+    if (many) launch_rows<NV, 2, 2, false>(g, waves, stream);
+    else launch_rows<NV, 2, 1, false>(g, waves, stream);
+  } else {
+    launch_rows<NV, 4, 1, false>(g, waves, stream);
+  }
+}
+template <bool NV> void launch_z(const MainArgs &g, hipStream_t stream) {
+  const int n = g.columns();
+  if (n <= 16) launch_rows<NV, 1, 1, true>(g, 4, stream);
+  else if (n <= 32) launch_rows<NV, 2, 1, true>(g, 4, stream);
+  else launch_rows<NV, 4, 1, true>(g, 4, stream);
 }
 
 bool fp4_ok(const metis_fp4_t &q, int fmt, int64_t rows, int64_t cols) {
@@ -337,15 +462,19 @@ bool fp4_ok(const metis_fp4_t &q, int fmt, int64_t rows, int64_t cols) {
 
 Weight weight_of(const metis_fp4_t &q) { return {q.codes, q.scales, q.tensor_scale, (int)q.rows, (int)q.cols}; }
 
+// Tokens of a pass over W: 64 columns of the products.
+int64_t pass_tokens(bool f32) { return f32 ? 21 : 64; }
+
 struct Plan {
-  unsigned short *z, *x;
+  float *z;
+  unsigned short *x;
   size_t bytes;
 };
 Plan plan_of(void *ws, int64_t tokens, bool f32, int64_t cols, int rank) {
-  const int64_t n = std::min<int64_t>(tokens, kTokens);
+  const int64_t n = std::min<int64_t>(tokens, pass_tokens(f32));
   Carver c(ws);
   Plan p = {};
-  if (rank) p.z = c.take<unsigned short>((size_t)3 * kTokens * rank_pad(rank));
+  if (rank) p.z = c.take<float>((size_t)(kSlices * n * rank_pad(rank)));
   if (f32) p.x = c.take<unsigned short>((size_t)(3 * n * cols));
   p.bytes = c.bytes();
   return p;
@@ -388,15 +517,16 @@ extern "C" metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_
     o.in(W->Vt_q);
   }
   if (!o.distinct()) return METIS_ERR_INVALID;
-  for (int64_t t0 = 0; t0 < tokens; t0 += kTokens) {
+  const int64_t pass = pass_tokens(f32);
+  for (int64_t t0 = 0; t0 < tokens; t0 += pass) {
     MainArgs g = {};
-    g.tokens = (int)std::min<int64_t>(kTokens, tokens - t0);
+    g.tokens = (int)std::min<int64_t>(pass, tokens - t0);
+    g.parts = f32 ? 3 : 1;
     if (f32) {
       g.x = p.x;
       g.ldx = K;
-      g.plane = (int64_t)std::min<int64_t>(tokens, kTokens) * K;
-      parts_kernel<<<dim3((unsigned)cdiv(K / 8, 256), (unsigned)g.tokens), 256, 0, stream>>>(
-          (const float *)x + t0 * ldx, ldx, (int)K, p.x, g.plane);
+      parts_kernel<<<dim3((unsigned)cdiv(K / 8, 256), (unsigned)g.tokens), 256, 0, stream>>>((const float *)x + t0 * ldx,
+                                                                                             ldx, (int)K, p.x);
     } else {
       g.x = (const unsigned short *)x + t0 * ldx;
       g.ldx = ldx;
@@ -404,18 +534,18 @@ extern "C" metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_
     if (k) {
       MainArgs z = g;
       z.w = weight_of(W->Vt_q);
-      z.s = W->S;
-      z.z_out = p.z;
-      launch<true>(z, nv, f32, waves_for(K, 16), stream);
+      z.z = p.z;
+      nv ? launch_z<true>(z, stream) : launch_z<false>(z, stream);
       g.u = weight_of(W->Ut_q);
       g.z = p.z;
+      g.s = W->S;
       g.rank = k;
     }
     g.w = weight_of(W->R_q);
     g.y = ydt == METIS_F32 ? (void *)((float *)y + t0 * ldy) : (void *)((unsigned short *)y + t0 * ldy);
     g.ldy = ldy;
     g.y_bf16 = ydt == METIS_BF16;
-    launch<false>(g, nv, f32, waves_for(K, K > 8192 ? 16 : 8), stream);
+    nv ? launch<true>(g, stream) : launch<false>(g, stream);
   }
   METIS_LAUNCH_CHECK();
   return METIS_OK;

@@ -35,7 +35,7 @@ using namespace metis_host;
 
 namespace {
 
-constexpr int kMaxDim = 256;
+constexpr int kMaxDim = 256, kMaxHeads = 65536;
 constexpr int64_t kMaxTokens = (int64_t)1 << 28;  // max_pages * page_size; divisions are exact below 2^29
 
 struct Batch {
@@ -62,7 +62,10 @@ struct AppendArgs {
   const float *whole[2];
   int dim;
   int64_t first;  // row of this launch's first workgroup
+  int each;       // tokens of a workgroup, at most kAppendTokens
+  FastDiv by_token, by_head;  // chunks of a token, and of a head
 };
+constexpr int kAppendTokens = 64, kAppendGrid = 2048;
 
 // The sequence that row t belongs to, -1 if to none.
 __device__ __forceinline__ int sequence_of(const Batch &b, int64_t t) {
@@ -88,14 +91,30 @@ __device__ __forceinline__ void turned(const AppendArgs &g, const T *head, int d
   const int half = g.rot / 2;
   const float *cs = g.rope + position * g.rot, *sn = cs + half;
   if (g.neighbours) {
+    if (d >= g.rot) return;
+    float cv[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (d + 8 <= g.rot) {
+      const u32x4_a1 c4 = *(const u32x4_a1 *)(cs + d / 2), s4 = *(const u32x4_a1 *)(sn + d / 2);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      if (d + i < g.rot) {
-        const double c = cs[(d + i) / 2], s = sn[(d + i) / 2], a = v[i], b = v[i + 1];
-        v[i] = (float)(a * c - b * s);
-        v[i + 1] = (float)(b * c + a * s);
+      for (int i = 0; i < 4; ++i) {
+        cv[i] = __uint_as_float(c4[i]);
+        sv[i] = __uint_as_float(s4[i]);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (d + 2 * i < g.rot) {
+          cv[i] = cs[d / 2 + i];
+          sv[i] = sn[d / 2 + i];
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (d + 2 * i < g.rot) {
+        const double c = cv[i], s = sv[i], a = v[2 * i], b = v[2 * i + 1];
+        v[2 * i] = (float)(a * c - b * s);
+        v[2 * i + 1] = (float)(b * c + a * s);
+      }
   } else if (half % 8 == 0) {  // the chunk's partners are a chunk too
     if (d < g.rot) {
       const bool first = d < half;
@@ -124,39 +143,67 @@ __device__ __forceinline__ void turned(const AppendArgs &g, const T *head, int d
   }
 }
 
+// E4M3 byte of a value >= 0, to nearest even, at most 448.
+__device__ __forceinline__ uint32_t e4m3_of(float v) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(v, 448.0f), 0.0f, 0, false) & 255u;
+}
+
 template <typename T, bool NV> __global__ void __launch_bounds__(256) append_kernel(AppendArgs g) {
-  const int64_t t = g.first + blockIdx.x;
-  const int per_head = g.dim / 8, per_side = g.p.heads * per_head;
-  auto source = [&](int u, int &side, int &head, int &d) -> const T * {
-    side = u >= per_side;
-    const int w = side ? u - per_side : u;
-    head = w / per_head;
-    d = (w - head * per_head) * 8;
-    return (const T *)(side ? g.x[1] : g.x[0]) + t * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.dim;
+  __shared__ int64_t places[kAppendTokens];  // row of a token's first head, -1: not stored
+  __shared__ int positions[kAppendTokens];
+  const int64_t t0 = g.first + (int64_t)blockIdx.x * g.each;
+  const int tokens = (int)min((int64_t)g.each, g.tokens - t0);
+  const int per_side = g.p.heads * (int)g.by_head.d, chunks = tokens * (int)g.by_token.d;
+  // chunk u of the workgroup's: a token's keys, then its values
+  struct Chunk8 {
+    int token, side, head, d;
+    const T *x;
   };
-  // the elements are under way while their place is looked up
-  int side, head, d;
-  const T *x = source(min((int)threadIdx.x, 2 * per_side - 1), side, head, d);
+  auto chunk_of = [&](int u) {
+    Chunk8 c;
+    c.token = (int)g.by_token.div((uint32_t)u);
+    const int in_token = u - c.token * (int)g.by_token.d;
+    c.side = in_token >= per_side;
+    const int w = c.side ? in_token - per_side : in_token;
+    c.head = (int)g.by_head.div((uint32_t)w);
+    c.d = (w - c.head * (int)g.by_head.d) * 8;
+    c.x = (const T *)(c.side ? g.x[1] : g.x[0]) + (t0 + c.token) * (c.side ? g.ldx[1] : g.ldx[0]) + (int64_t)c.head * g.dim;
+    return c;
+  };
+  // the first elements are under way while their places are looked up
+  Chunk8 c = chunk_of(min((int)threadIdx.x, chunks - 1));
   Raw<T> raw;
-  load_all(x + d, raw);
-  const int seq = sequence_of(g.b, t);
-  if (seq < 0) return;  // the same for the whole workgroup, as are the ways out below
-  const int64_t end = g.b.starts ? g.b.starts[seq + 1] : t + 1;
-  if (end > g.tokens || (g.b.starts && g.b.starts[seq] < 0)) return;
-  const int64_t position = g.b.lengths[seq] - (end - t);
-  if (position < 0 || position >= (int64_t)g.b.max_pages * g.p.page_size) return;
-  if (g.rot && position >= g.rope_rows) return;
-  const uint32_t at = g.p.by_page.div((uint32_t)position);
-  const int page = g.b.table[seq * g.b.ldt + at];
-  if (page < 0 || page >= g.p.pages) return;
-  const int place = (int)((uint32_t)position - at * g.p.by_page.d);
-  for (int u = threadIdx.x; u < 2 * per_side; u += blockDim.x) {  // whole quads: per_head is a multiple of four
-    if (u != (int)threadIdx.x) {
-      x = source(u, side, head, d);
-      load_all(x + d, raw);
+  load_all(c.x + c.d, raw);
+  if ((int)threadIdx.x < tokens) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t place = -1, position = -1;
+    const int seq = sequence_of(g.b, t);
+    if (seq >= 0) {
+      const int64_t start = g.b.starts ? g.b.starts[seq] : t, end = g.b.starts ? g.b.starts[seq + 1] : t + 1;
+      if (start >= 0 && end <= g.tokens) position = g.b.lengths[seq] - (end - t);
+      if (position >= 0 && position < (int64_t)g.b.max_pages * g.p.page_size && (!g.rot || position < g.rope_rows)) {
+        const uint32_t at = g.p.by_page.div((uint32_t)position);
+        const int page = g.b.table[seq * g.b.ldt + at];
+        if (page >= 0 && page < g.p.pages)
+          place = (int64_t)page * g.p.heads * g.p.page_size + ((uint32_t)position - at * g.p.by_page.d);
+      }
     }
+    places[threadIdx.x] = place;
+    positions[threadIdx.x] = (int)position;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < chunks; u += blockDim.x) {  // whole quads: a head has a multiple of four chunks
+    const Chunk8 now = c;
     float v[8];
     to_f32(raw, v);
+    if (u + (int)blockDim.x < chunks) {
+      c = chunk_of(u + (int)blockDim.x);
+      load_all(c.x + c.d, raw);
+    }
+    const int side = now.side, head = now.head, d = now.d;
+    const T *x = now.x;
+    const int64_t place = places[now.token], position = positions[now.token];
+    if (place < 0) continue;  // the same for a whole quad
     if (!side && g.rot) turned(g, x, d, position, v);
     float top = 0.0f;
 #pragma unroll
@@ -168,10 +215,22 @@ template <typename T, bool NV> __global__ void __launch_bounds__(256) append_ker
     uint32_t code, byte;
     if (NV) {
       const float whole = *(side ? g.whole[1] : g.whole[0]);
-      byte = e4m3_rne_sat(__fdiv_rn(top, 6.0f * whole));
-      const float by = e4m3_value(byte) * whole;
+      byte = e4m3_of(__fdiv_rn(top, 6.0f * whole));
+      const float by = scale4<true>(byte) * whole;
+      if (by > 0x1p-60f && by < 0x1p60f) {
+        // x / by correctly rounded: 1 / by is, and x q's remainder is exact, so
+        // that the corrected quotient is the rounded one (Markstein). Quotients
+        // too large for it saturate, ones too small for it are codes of zero.
+        const float inv = __fdiv_rn(1.0f, by);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = byte ? __fdiv_rn(v[i], by) : v[i] * 0.0f;
+        for (int i = 0; i < 8; ++i) {
+          const float q = v[i] * inv, c = fmaf(fmaf(-q, by, v[i]), inv, q);
+          v[i] = fabsf(q) < 0x1p20f ? c : q;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = byte ? __fdiv_rn(v[i], by) : v[i] * 0.0f;
+      }
       code = e2m1_pack8(v);
     } else {
       const int e = mx_shared_exponent(top);
@@ -180,7 +239,7 @@ template <typename T, bool NV> __global__ void __launch_bounds__(256) append_ker
       e2m1_pack_scaled<8>(v, pow2_f32(e), packed);
       code = packed[0];
     }
-    const int64_t row = ((int64_t)page * g.p.heads + head) * g.p.page_size + place;
+    const int64_t row = place + (int64_t)head * g.p.page_size;
     *(uint32_t *)((side ? g.codes[1] : g.codes[0]) + row * (g.dim / 2) + d / 2) = code;
     if (d % kBlock4<NV> == 0) (side ? g.scales[1] : g.scales[0])[row * (g.dim / kBlock4<NV>) + d / kBlock4<NV>] = (uint8_t)byte;
   }
@@ -626,7 +685,7 @@ metis_status_t check_cache(const metis_kv_cache_t *c, const metis_kv_batch_t *b,
   const metis_fp4_t &k = c->k, &v = c->v;
   if (k.fmt != METIS_MXFP4 && k.fmt != METIS_NVFP4) return METIS_ERR_INVALID;
   if (v.fmt != k.fmt || v.cols != k.cols || k.cols < 1 || k.rows != v.rows) return METIS_ERR_INVALID;
-  if (c->pages > kMaxRows || c->heads > kMaxRows || c->page_size > kMaxTokens) return METIS_ERR_UNSUPPORTED;
+  if (c->pages > kMaxRows || c->heads > kMaxHeads || c->page_size > kMaxTokens) return METIS_ERR_UNSUPPORTED;
   // one factor after the other: each product stays below 2^62
   const int64_t page_rows = (int64_t)c->heads * c->page_size;
   if (page_rows > kMaxRows || c->pages * page_rows > kMaxRows) return METIS_ERR_UNSUPPORTED;
@@ -772,12 +831,17 @@ extern "C" metis_status_t metis_kv_append(const void *k, int64_t ldk, const void
   g.whole[0] = cache->k.tensor_scale;
   g.whole[1] = cache->v.tensor_scale;
   g.dim = (int)cache->k.cols;
-  const int64_t lanes = 2 * n / 8;
-  const unsigned threads = (unsigned)std::min<int64_t>(256, round_up(lanes, 64));
+  // Tokens of a workgroup: looking a place up takes a handful of dependent
+  // loads, which several tokens of a workgroup share the time of
+  const int64_t chunks = 2 * n / 8;
+  g.each = (int)std::min<int64_t>(kAppendTokens, std::max({(int64_t)1, 256 / chunks, std::min<int64_t>(8, tokens / kAppendGrid)}));
+  g.by_token.set((uint32_t)chunks);
+  g.by_head.set((uint32_t)(g.dim / 8));
   constexpr int64_t kSlab = 1 << 23;  // workgroups of a launch: below 2^32 threads
-  for (int64_t t0 = 0; t0 < tokens; t0 += kSlab) {
+  for (int64_t t0 = 0; t0 < tokens; t0 += kSlab * g.each) {
     g.first = t0;
-    const unsigned grid = (unsigned)std::min(kSlab, tokens - t0);
+    const unsigned threads = (unsigned)std::min<int64_t>(256, round_up(chunks * g.each, 64));
+    const unsigned grid = (unsigned)std::min(kSlab, cdiv(tokens - t0, g.each));
     if (dt == METIS_F32) {
       if (nv) append_kernel<float, true><<<grid, threads, 0, stream>>>(g);
       else append_kernel<float, false><<<grid, threads, 0, stream>>>(g);

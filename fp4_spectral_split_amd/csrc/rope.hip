@@ -24,8 +24,9 @@ using namespace metis_host;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBwdThreads = 512;
 constexpr int kMaxDim = 512, kMaxHeads = 65536;
-constexpr int kParts = 768;  // partial sums of dwq and dwk together, at most
+constexpr int kParts = 512;  // partial sums of dwq and dwk together, at most
 
 template <int CTRL> __device__ __forceinline__ float dpp_f32(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
@@ -141,17 +142,17 @@ template <int W> __device__ __forceinline__ void unpair(const Shape &s, float *a
   }
 }
 
-// Cosines and sines of a unit's pairs for a token.
-template <int W> __device__ __forceinline__ void angles(const Shape &s, const Unit &u, int64_t token, float *c, float *sn) {
+// Cosines and sines of a unit's pairs at position p. (The position is read
+// ahead of x: memory answers in order, and the angles wait for it.)
+template <int W> __device__ __forceinline__ void angles(const Shape &s, const Unit &u, int p, float *c, float *sn) {
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     c[i] = 1.0f;
     sn[i] = 0.0f;
   }
   if (u.angle >= 0) {
-    const int64_t p = s.positions[token];
     if (p >= 0 && p < s.rope_rows) {
-      const float *row = s.rope + p * s.rot + u.angle;
+      const float *row = s.rope + (int64_t)p * s.rot + u.angle;
       load_part<W>(row, c);
       load_part<W>(row + s.rot / 2, sn);
     } else {
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(FwdArgs g) {
   const int h0 = (int)(unit - token * g.by_chunks.d) * H;
   Unit un[U];
   float a[H][U][W], b[H][U][W], c[U][W], sn[U][W];
+  const int position = g.s.positions ? g.s.positions[token] : 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) un[u] = unit_of<W>(g.s, lane + u * G);
 #pragma unroll
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(FwdArgs g) {
     for (int u = 0; u < U; ++u) load_unit<W>(un[u], p, at < g.heads[0] + g.heads[1], a[h][u], b[h][u]);
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], token, c[u], sn[u]);
+  for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], position, c[u], sn[u]);
   float wa[U][W], wb[U][W];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
@@ -296,8 +298,8 @@ struct BwdArgs {
 };
 
 template <typename TD, typename T, typename TO, int W, int G, int U, int H>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(BwdArgs g) {
-  constexpr int kGroups = kThreads / G;
+__global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(BwdArgs g) {
+  constexpr int kGroups = kBwdThreads / G;
   __shared__ float sums[kGroups][2 * W * U * G];
   const int side = (int)blockIdx.x >= g.blocks[0];
   const int block = (int)blockIdx.x - (side ? g.blocks[0] : 0), blocks = side ? g.blocks[1] : g.blocks[0];
@@ -322,6 +324,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(BwdArgs g) {
     const uint32_t token = by.div(unit);
     const int h0 = (int)(unit - token * by.d) * H;
     float ga[H][U][W], gb[H][U][W], a[H][U][W], b[H][U][W], c[U][W], sn[U][W];
+    const int position = g.s.positions ? g.s.positions[token] : 0;
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(BwdArgs g) {
         load_unit<W>(un[u], x + (int64_t)token * ldx + off, !g.s.none && h0 + h < heads, a[h][u], b[h][u]);
       }
 #pragma unroll
-    for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], token, c[u], sn[u]);
+    for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], position, c[u], sn[u]);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       if (h0 + h >= heads) break;
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(BwdArgs g) {
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < dim; e += kThreads) {
+  for (int e = threadIdx.x; e < dim; e += kBwdThreads) {
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) v += sums[k][e];
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(BwdArgs g) {
   }
 }
 
-// dw of one side: sixteen columns a workgroup, sixteen threads on each, in the
+// dw of one side: sixteen columns a workgroup, 64 threads on each, in the
 // order of the partial sums.
 struct FinishArgs {
   const float *part[2];
@@ -409,8 +412,9 @@ struct FinishArgs {
   int parts[2];
   int dim, accumulate;
 };
-__global__ void __launch_bounds__(kThreads) qk_finish_kernel(FinishArgs g) {
-  __shared__ float sums[16][17];
+constexpr int kFinishThreads = 1024, kFinishRows = kFinishThreads / 16;
+__global__ void __launch_bounds__(kFinishThreads) qk_finish_kernel(FinishArgs g) {
+  __shared__ float sums[kFinishRows][17];
   const int side = blockIdx.y, col = threadIdx.x & 15, row = threadIdx.x >> 4;
   float *dw = side ? g.dw[1] : g.dw[0];
   if (!dw) return;
@@ -419,14 +423,14 @@ __global__ void __launch_bounds__(kThreads) qk_finish_kernel(FinishArgs g) {
   float v = 0.0f;
   if (e < g.dim) {
 #pragma unroll 8
-    for (int p = row; p < parts; p += 16) v += part[(int64_t)p * g.dim + e];
+    for (int p = row; p < parts; p += kFinishRows) v += part[(int64_t)p * g.dim + e];
   }
   sums[row][col] = v;
   __syncthreads();
   if (row == 0 && e < g.dim) {
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) t += sums[k][col];
+    for (int k = 0; k < kFinishRows; ++k) t += sums[k][col];
     dw[e] = g.accumulate ? dw[e] + t : t;
   }
 }
@@ -489,12 +493,14 @@ template <typename T, typename TO> void fwd_by_shape(const FwdArgs &g, int64_t t
   }
 }
 
-// Workgroups of one side of the backward pass, each with one partial sum.
+// Workgroups of one side of the backward pass, each with one partial sum: as
+// many as the heads give work to, up to what fills the GPU.
 constexpr int kBwdHeads = 2;
-int bwd_blocks(int64_t tokens, int heads, int all_heads) {
+int bwd_blocks(int64_t tokens, int heads, int all_heads, int dim) {
   if (!heads) return 0;
   const int64_t most = std::max<int64_t>(1, (int64_t)kParts * heads / all_heads);
-  return (int)std::min<int64_t>(most, std::max<int64_t>(1, tokens * cdiv(heads, kBwdHeads)));
+  const int groups = kBwdThreads / (dim <= 64 ? 8 : dim <= 128 ? 16 : dim <= 256 ? 32 : 64);
+  return (int)std::min<int64_t>(most, cdiv(tokens * cdiv(heads, kBwdHeads), std::max(1, groups / 4)));
 }
 
 template <typename TD, typename T, typename TO, int W, int G, int U>
@@ -504,7 +510,7 @@ void bwd_launch(BwdArgs g, int64_t tokens, hipStream_t stream) {
     g.units[s] = (uint32_t)(tokens * chunks);
     g.by_chunks[s].set((uint32_t)std::max(1, chunks));
   }
-  qk_bwd_kernel<TD, T, TO, W, G, U, kBwdHeads><<<g.blocks[0] + g.blocks[1], kThreads, 0, stream>>>(g);
+  qk_bwd_kernel<TD, T, TO, W, G, U, kBwdHeads><<<g.blocks[0] + g.blocks[1], kBwdThreads, 0, stream>>>(g);
 }
 
 template <typename TD, typename T, typename TO> void bwd_by_shape(const BwdArgs &g, int64_t tokens, hipStream_t stream) {
@@ -564,7 +570,7 @@ Shape shape_of(int32_t head_dim, int kind, float eps, const int32_t *positions, 
 }
 
 void finish_launch(const FinishArgs &f, hipStream_t stream) {
-  qk_finish_kernel<<<dim3((unsigned)cdiv(f.dim, 16), 2), kThreads, 0, stream>>>(f);
+  qk_finish_kernel<<<dim3((unsigned)cdiv(f.dim, 16), 2), kFinishThreads, 0, stream>>>(f);
 }
 
 }  // namespace
@@ -632,8 +638,8 @@ extern "C" size_t metis_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t
       head_dim < 1 || head_dim > kMaxDim)
     return 0;
   Carver ws(nullptr);
-  ws.take<float>((size_t)bwd_blocks(tokens, q_heads, q_heads + k_heads) * head_dim);
-  ws.take<float>((size_t)bwd_blocks(tokens, k_heads, q_heads + k_heads) * head_dim);
+  ws.take<float>((size_t)bwd_blocks(tokens, q_heads, q_heads + k_heads, head_dim) * head_dim);
+  ws.take<float>((size_t)bwd_blocks(tokens, k_heads, q_heads + k_heads, head_dim) * head_dim);
   return ws.bytes();
 }
 
@@ -698,8 +704,8 @@ extern "C" metis_status_t metis_qk_norm_rope_bwd(const void *dq, int64_t lddq, c
   if (!o.distinct()) return METIS_ERR_INVALID;
   BwdArgs g = {};
   g.s = shape_of(head_dim, kind, eps, positions, rope, rope_rows, rot_dim, pairs);
-  g.blocks[0] = bwd_blocks(tokens, q_heads, q_heads + k_heads);
-  g.blocks[1] = bwd_blocks(tokens, k_heads, q_heads + k_heads);
+  g.blocks[0] = bwd_blocks(tokens, q_heads, q_heads + k_heads, head_dim);
+  g.blocks[1] = bwd_blocks(tokens, k_heads, q_heads + k_heads, head_dim);
   Carver carve(ws);
   float *pq = carve.take<float>((size_t)g.blocks[0] * head_dim), *pk = carve.take<float>((size_t)g.blocks[1] * head_dim);
   g.dy[0] = dq;
