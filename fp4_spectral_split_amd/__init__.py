@@ -28,6 +28,7 @@ Calls (same names as the C ABI in include/metis_fp4.h):
   metis_kv_attention(q, batch, cache)          -> (o, log-sum-exp)
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass, field
 from typing import Optional
@@ -249,7 +250,9 @@ class Fp4Tensor:
                          torch.empty(1, dtype=torch.float32, device=device) if fmt == NVFP4 else None)
 
     def c(self):
-        return _Fp4(self.fmt, 0, self.rows, self.cols, _ptr(self.codes), _ptr(self.scales), _ptr(self.tensor_scale))
+        t = self.tensor_scale
+        return _Fp4(self.fmt, 0, self.rows, self.cols, None if self.codes is None else self.codes.data_ptr(),
+                    None if self.scales is None else self.scales.data_ptr(), None if t is None else t.data_ptr())
 
     @property
     def fmt_name(self):
@@ -279,11 +282,10 @@ def fp4_block_quant(x, fmt="mxfp4", transpose=False, out=None):
 
 
 def fp4_block_dequant(q, out=None):
-    L = load()
+    dev = q.codes.device
     if out is None:
-        out = torch.empty(q.rows, q.cols, dtype=torch.float32, device=q.codes.device)
-    c = q.c()
-    _check(L.fp4_block_dequant(ctypes.byref(c), _ptr(out), out.stride(0), _stream(out.device)))
+        out = torch.empty((q.rows, q.cols), dtype=torch.float32, device=dev)
+    _run(out.device, load().fp4_block_dequant, q.c(), out.data_ptr(), out.stride(0))
     return out
 
 
@@ -977,52 +979,71 @@ def metis_qk_norm_rope_bwd(dq, dk, q, k, positions, rope, head_dim, weight_q=Non
     return out_q, out_k, dweight_q if want_q else None, dweight_k if want_k else None
 
 
-def _fp4_buffers(q, name, rows, cols, device, fmt=None):
-    """Checks an Fp4Tensor: its buffers hold the matrix it says, on the device."""
+def _fp4_buffers(q, name, rows, cols, index, fmt=None):
+    """Checks an Fp4Tensor: its buffers hold the matrix it says, on device
+    `index`; returns its C record."""
     if not isinstance(q, Fp4Tensor) or q.fmt not in _FMT_NAME or (fmt is not None and q.fmt != fmt):
         raise MetisError("%s must be an Fp4Tensor%s" % (name, "" if fmt is None else " in " + _FMT_NAME[fmt]))
     if q.rows != rows or q.cols != cols:
         raise MetisError("%s must be %d x %d, got %d x %d" % (name, rows, cols, q.rows, q.cols))
-    sizes = [(q.codes, rows * cols // 2, torch.uint8), (q.scales, rows * (cols // BLOCK[q.fmt]), torch.uint8)]
-    if q.fmt == NVFP4:
-        sizes.append((q.tensor_scale, 1, torch.float32))
-    for buf, n, dtype in sizes:
-        if (not isinstance(buf, torch.Tensor) or buf.dtype != dtype or buf.numel() != n or not buf.is_contiguous()
-                or not buf.is_cuda):
-            raise MetisError("%s needs contiguous CUDA codes and scales of its size" % name)
-        if buf.device != device:
-            raise MetisError("%s is on %s, the other operands on %s" % (name, buf.device, device))
+    codes, scales, whole = q.codes, q.scales, q.tensor_scale
+    try:
+        ok = (codes.dtype == scales.dtype == torch.uint8 and codes.numel() == rows * cols // 2
+              and scales.numel() == rows * (cols // BLOCK[q.fmt]) and codes.is_contiguous() and scales.is_contiguous())
+        there = codes.get_device() == scales.get_device() == index >= 0
+        if q.fmt == NVFP4:
+            ok = ok and whole.dtype == torch.float32 and whole.numel() == 1
+            there = there and whole.get_device() == index
+    except AttributeError:  # something else than a tensor
+        ok = there = False
+    if not ok:
+        raise MetisError("%s needs contiguous CUDA codes and scales of its size" % name)
+    if not there:
+        raise MetisError("%s is not on the device of the other operands" % name)
+    return _Fp4(q.fmt, 0, rows, cols, codes.data_ptr(), scales.data_ptr(),
+                whole.data_ptr() if q.fmt == NVFP4 else None)
+
+
+@functools.lru_cache(maxsize=1024)
+def _gemv_workspace(tokens, dt, m, n, k):
+    s = _Split()
+    s.m, s.n, s.k = m, n, k
+    return load().metis_fp4_gemv_workspace_bytes(tokens, dt, s)
 
 
 def metis_fp4_gemv(x, W, dtype=None, out=None):
     """y = x W_hat^T of a few tokens: x a 2-D fp32/bf16 CUDA tensor (tokens x
     W.n, not quantized), W a SplitRecord (split or plain) with its R_q; y is
     tokens x W.m of type `dtype` (default: x's). W is read once for each 64
-    tokens: many tokens are better quantized for spectral_fp4_linear_fwd."""
+    tokens of bf16 or 21 of fp32: many tokens are better quantized for
+    spectral_fp4_linear_fwd."""
     if not isinstance(W, SplitRecord) or W.R_q is None:
         raise MetisError("W must be a SplitRecord with R_q")
     ldx = _matrix(x, "x")
-    dev, tokens, dt = x.device, x.shape[0], _code(x.dtype)
-    if x.shape[1] != W.n:
-        raise MetisError("x must have %d columns, got %d" % (W.n, x.shape[1]))
-    _fp4_buffers(W.R_q, "R_q", W.m, W.n, dev, W.fmt)
-    if W.k:
-        _fp4_buffers(W.Ut_q, "Ut_q", W.k, W.m, dev, W.fmt)
-        _fp4_buffers(W.Vt_q, "Vt_q", W.k, W.n, dev, W.fmt)
-        if _vector(W.S, "S", W.k, dev, torch.float32) is None:
+    (tokens, cols), m, n, k, fmt = x.shape, W.m, W.n, W.k, W.fmt
+    dt, index = _code(x.dtype), x.get_device()
+    if cols != n:
+        raise MetisError("x must have %d columns, got %d" % (n, cols))
+    w = _Split()
+    w.m, w.n, w.k = m, n, k
+    w.R_q = _fp4_buffers(W.R_q, "R_q", m, n, index, fmt)
+    if k:
+        w.Ut_q = _fp4_buffers(W.Ut_q, "Ut_q", k, m, index, fmt)
+        w.Vt_q = _fp4_buffers(W.Vt_q, "Vt_q", k, n, index, fmt)
+        w.S = _vector(W.S, "S", k, x.device, torch.float32)
+        if not w.S:
             raise MetisError("a split weight needs its S")
     dtype = x.dtype if dtype is None else dtype
     ydt = _code(dtype)
     if out is None:
-        out, ldy = x.new_empty((tokens, W.m), dtype=dtype), W.m
+        out, ldy = x.new_empty((tokens, m), dtype=dtype), m
     else:
-        ldy = _matrix(out, "out", (tokens, W.m), dev)
+        ldy = _matrix(out, "out", (tokens, m), x.device)
         if out.dtype != dtype:
             raise MetisError("out must be %s" % dtype)
-    L, w = load(), W.c()
-    nws = L.metis_fp4_gemv_workspace_bytes(tokens, dt, w)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _run(dev, L.metis_fp4_gemv, x.data_ptr(), dt, tokens, ldx, w, out.data_ptr(), ydt, ldy,
+    nws = _gemv_workspace(tokens, dt, m, n, k)
+    ws = x.new_empty(nws, dtype=torch.uint8) if nws else None  # of its own per call, as in metis_norm_bwd
+    _run(x.device, load().metis_fp4_gemv, x.data_ptr(), dt, tokens, ldx, w, out.data_ptr(), ydt, ldy,
          ws.data_ptr() if nws else None, nws)
     return out
 
@@ -1070,7 +1091,7 @@ class KvCache:
             raise MetisError("FP4 format must be mxfp4 or nvfp4, got %r" % (fmt,))
         rows = pages * heads * page_size
         c = KvCache(pages, page_size, heads, Fp4Tensor(f, rows, head_dim, *keys), Fp4Tensor(f, rows, head_dim, *values))
-        _cache(c, c.k.codes.device if isinstance(c.k.codes, torch.Tensor) else None)
+        _cache(c, c.k.codes.get_device() if isinstance(c.k.codes, torch.Tensor) else -1)
         return c
 
     @property
@@ -1097,16 +1118,18 @@ class KvBatch:
     max_length: Optional[int] = None
 
 
-def _cache(cache, device):
+def _cache(cache, index):
+    """Checks a KvCache; returns its C record."""
     if not isinstance(cache, KvCache):
         raise MetisError("cache must be a KvCache")
     rows, cols = cache.pages * cache.heads * cache.page_size, getattr(cache.k, "cols", 0)
-    _fp4_buffers(cache.k, "the cache's k", rows, cols, device)
-    _fp4_buffers(cache.v, "the cache's v", rows, cols, device, cache.k.fmt)
-    return cache.c()
+    k = _fp4_buffers(cache.k, "the cache's k", rows, cols, index)
+    return _KvCache(cache.pages, cache.page_size, cache.heads, k,
+                    _fp4_buffers(cache.v, "the cache's v", rows, cols, index, k.fmt))
 
 
 def _batch(batch, device):
+    """Checks a KvBatch; returns its C record."""
     if not isinstance(batch, KvBatch):
         raise MetisError("batch must be a KvBatch")
     t = batch.table
@@ -1121,6 +1144,15 @@ def _batch(batch, device):
     return _KvBatch(t.data_ptr(), lengths, starts, ldt, seqs, pages)
 
 
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(tokens, heads, max_new, longest, seqs, max_pages, starts, pages, page_size, kv_heads, fmt, dim):
+    rows = pages * kv_heads * page_size
+    q = _Fp4(fmt, 0, rows, dim, None, None, None)
+    b = _KvBatch(None, None, 1 if starts else None, max_pages, seqs, max_pages)
+    return load().metis_kv_attention_workspace_bytes(tokens, heads, max_new, longest, b,
+                                                     _KvCache(pages, page_size, kv_heads, q, q))
+
+
 def metis_kv_append(k, v, batch, cache, rope=None, pairs="halves"):
     """Store the new tokens' keys (turned by their positions' angles where rope
     is given, see metis_qk_norm_rope_fwd) and values in the cache, quantized as
@@ -1129,7 +1161,7 @@ def metis_kv_append(k, v, batch, cache, rope=None, pairs="halves"):
     the rope are not stored; pages written to belong to one sequence each."""
     ldk = _matrix(k, "k")
     dev, dt = k.device, _code(k.dtype)
-    c, b = _cache(cache, dev), _batch(batch, dev)
+    c, b = _cache(cache, k.get_device()), _batch(batch, dev)
     n = cache.heads * cache.head_dim
     if k.shape[1] != n:
         raise MetisError("k must have %d columns, got %d" % (n, k.shape[1]))
@@ -1148,7 +1180,7 @@ def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=No
     sees the tokens up to its own position, of them the last `window` (0: all).
     scale: default 1 / sqrt(head_dim). o is of type `dtype` (default: q's).
     Rows outside the batch keep what `out` holds (a new output: zeros)."""
-    c = _cache(cache, q.device if isinstance(q, torch.Tensor) else None)
+    c = _cache(cache, q.get_device() if isinstance(q, torch.Tensor) else -1)
     ldq, heads = _heads(q, "q", cache.head_dim)
     dev, tokens, dt = q.device, q.shape[0], _code(q.dtype)
     b = _batch(batch, dev)
@@ -1165,11 +1197,11 @@ def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=No
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
         if not every:
             lse.fill_(float("-inf"))
-    L = load()
     longest = max(1, int(batch.max_length) if batch.max_length is not None else b.max_pages * cache.page_size)
-    nws = L.metis_kv_attention_workspace_bytes(tokens, heads, batch.max_new, longest, b, c)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _run(dev, L.metis_kv_attention, q.data_ptr(), dt, tokens, ldq, heads, b, c, batch.max_new, longest,
+    nws = _attention_workspace(tokens, heads, batch.max_new, longest, b.seqs, b.max_pages, batch.starts is not None,
+                               cache.pages, cache.page_size, cache.heads, c.k.fmt, cache.head_dim)
+    ws = q.new_empty(nws, dtype=torch.uint8) if nws else None  # of its own per call, as in metis_norm_bwd
+    _run(dev, load().metis_kv_attention, q.data_ptr(), dt, tokens, ldq, heads, b, c, batch.max_new, longest,
          cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), odt, ldo,
          None if lse is None else lse.data_ptr(), ws.data_ptr() if nws else None, nws)
     return out, lse

@@ -58,15 +58,20 @@ struct MainArgs {
 
 __host__ __device__ inline int rank_pad(int rank) { return (rank + 31) / 32 * 32; }
 
-// A step of one row: 128 columns of which a lane loads the 32 from 32 q on, and
-// the scales of all of them.
+// A step of sixteen rows, 128 columns of each, as loaded: lane l has the 32
+// columns from 32 (l % 4) on of row l / 4, and the scales of all of that row's, so
+// that four neighbouring lanes read 64 bytes in a row. (With lane l at row
+// l % 16, as the products want it, every lane was an access of its own to the
+// cache's tags: four times as many.)
 template <bool NV> struct Codes {
   uint32_t w[4];
   uint32_t scale[NV ? 2 : 1];  // four blocks of 32 or eight of 16
 };
 template <bool NV, bool EDGE>
-__device__ __forceinline__ void load_codes(const Weight &w, int64_t row, int c, int q, Codes<NV> &r) {
+__device__ __forceinline__ void load_codes(const Weight &w, int row0, int c, int lane, Codes<NV> &r) {
   constexpr int B = kBlock4<NV>;
+  const int64_t row = min(row0 + (lane >> 2), w.rows - 1);  // behind the last row: it again, not stored
+  const int q = lane & 3;
   const uint8_t *p = w.codes + row * (w.cols / 2) + c / 2 + 16 * q;
   const uint8_t *s = w.scales + row * (w.cols / B) + c / B;
   if (!EDGE) {
@@ -98,6 +103,15 @@ __device__ __forceinline__ void load_codes(const Weight &w, int64_t row, int c, 
   }
 }
 
+// Sixteen bytes from lane 4 r + q to lane 16 q + r, through a kilobyte of LDS
+// that is the wave's own (its accesses take place in order). The sixteen-byte
+// pieces of a row change places with r / 4, so that neither side meets a bank twice.
+__device__ __forceinline__ u32x4_a1 spread(const u32x4_a1 &v, uint8_t *mine, int lane) {
+  const int r = lane & 15, q = lane >> 4;
+  *(intx4 *)(mine + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) * 16)) = __builtin_bit_cast(intx4, v);
+  return __builtin_bit_cast(u32x4_a1, *(const intx4 *)(mine + r * 64 + ((q ^ (r >> 2)) * 16)));
+}
+
 // Word u of lane q to word q of lane u (of the four lanes that share a row):
 // a lane then has columns 32 u + 8 q .. + 7 as word u, so that the four lanes'
 // pieces of x are 64 bytes in a row. (With x read where the codes lie, sixteen
@@ -112,7 +126,17 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
   w[2] = d[0];
   w[3] = d[1];
 }
-// The scale of word u after that, in lane q.
+// Codes as the products want them: lane 16 q + r has row r, and of it columns
+// 32 u + 8 q .. + 7 as word u.
+template <bool NV> __device__ __forceinline__ void arrange(Codes<NV> &c, uint8_t *mine, int lane) {
+  const u32x4_a1 v = spread(u32x4_a1{c.w[0], c.w[1], c.w[2], c.w[3]}, mine, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.w[i] = v[i];
+  transpose4(c.w);
+#pragma unroll
+  for (int i = 0; i <= NV; ++i) c.scale[i] = __shfl(c.scale[i], 4 * (lane & 15), 64);
+}
+// The scale of word u after that, in lane 16 q + r.
 template <bool NV> __device__ __forceinline__ float scale_of(const Codes<NV> &c, int u, int q) {
   if (NV) return scale4<NV>((c.scale[u / 2] >> (16 * (u % 2) + 8 * (q >> 1))) & 255u);
   return scale4<NV>((c.scale[0] >> (8 * u)) & 255u);
@@ -173,10 +197,10 @@ __device__ __forceinline__ void load_z(const MainArgs &g, int c, int k0, ushortx
   parts_bf16<3>(v, part);
 }
 
-// x for column c of the products (behind the last one: it again), from column
-// 8 q of W on.
-__device__ __forceinline__ const unsigned short *x_row(const MainArgs &g, int c, int q) {
-  return g.x + (int64_t)min(c, g.columns() - 1) * g.ldx + 8 * q;
+// Row of x that a lane loads for the sixteen columns of the products from c0 on
+// (behind the last one: it again), its columns from 8 (lane % 4) on.
+__device__ __forceinline__ const unsigned short *x_row(const MainArgs &g, int c0, int lane) {
+  return g.x + (int64_t)min(c0 + (lane >> 2), g.columns() - 1) * g.ldx + 8 * (lane & 3);
 }
 
 // The sum over waves and over a token's parts: rows row0 .. + 15 of W, `sums`
@@ -214,6 +238,7 @@ template <bool NV, int S> struct Held {
 template <bool NV, int S>
 __global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) {
   __shared__ float sums[2][kHeldWaves][256];
+  __shared__ __attribute__((aligned(16))) uint8_t pieces[kHeldWaves][1024];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all_waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, cols = g.w.cols;
   const int chunks = (g.rank + 31) / 32, waves = all_waves - chunks;  // the last waves have the rank's terms
@@ -224,24 +249,28 @@ __global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) 
     // for the codes; x is then the last eight columns again
     const bool edge = (first + S) * kStep > cols;
     auto load = [&](int tile, Held<NV, S> &h) {
-      const int64_t row = row_of(tile);
       if (!edge) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) load_codes<NV, false>(g.w, row, (first + i) * kStep, q, h.c[i]);
+        for (int i = 0; i < S; ++i) load_codes<NV, false>(g.w, tile * kRows, (first + i) * kStep, lane, h.c[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < S; ++i) load_codes<NV, true>(g.w, row, (first + i) * kStep, q, h.c[i]);
+        for (int i = 0; i < S; ++i) load_codes<NV, true>(g.w, tile * kRows, (first + i) * kStep, lane, h.c[i]);
       }
     };
     Held<NV, S> h, next;
     load(blockIdx.x, h);
-    ushortx8 x[S][4];
-    const unsigned short *p = x_row(g, r, q);
+    u32x4_a1 x[S][4];
+    const unsigned short *p = x_row(g, 0, lane);
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        x[i][u] = __builtin_bit_cast(ushortx8, *(const u32x4_a1 *)(p + min((first + i) * kStep + 32 * u, cols - 8 - 8 * q)));
+        x[i][u] = *(const u32x4_a1 *)(p + min((first + i) * kStep + 32 * u, cols - 8 - 8 * (lane & 3)));
+    uint8_t *mine = pieces[wave];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[i][u] = spread(x[i][u], mine, lane);
     const float whole = NV ? *g.w.whole : 1.0f;
     int buf = 0;
     for (int tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
@@ -250,9 +279,10 @@ __global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) 
       floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        transpose4(h.c[i].w);
+        arrange<NV>(h.c[i], mine, lane);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) acc = mfma16_bf16(decode4<NV>(h.c[i].w[u], scale_of<NV>(h.c[i], u, q)), x[i][u], acc);
+        for (int u = 0; u < 4; ++u)
+          acc = mfma16_bf16(decode4<NV>(h.c[i].w[u], scale_of<NV>(h.c[i], u, q)), __builtin_bit_cast(ushortx8, x[i][u]), acc);
       }
       if (NV) acc *= whole;
       *(floatx4 *)&sums[buf][wave][16 * r + 4 * q] = acc;
@@ -290,15 +320,12 @@ __global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) 
 // The sums over a wave's columns. NT: sixteens of columns of the products. RT:
 // sixteens of rows. Z: the launch that forms z.
 template <bool NV, int NT, int RT, bool Z>
-__device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, int waves, int r, int q,
+__device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, int waves, int lane, uint8_t *mine,
                                         floatx4 (&acc)[RT][NT]) {
-  const int cols = g.w.cols;
-  int64_t row[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) row[t] = min(row0 + 16 * t + r, g.w.rows - 1);
+  const int cols = g.w.cols, q = lane >> 4;
   const unsigned short *x_of[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x_of[n] = x_row(g, 16 * n + r, q);
+  for (int n = 0; n < NT; ++n) x_of[n] = x_row(g, 16 * n, lane);
 
   // N steps of 128 columns in a row: all their codes are asked for before the
   // first of them is used, x (which the L2 holds) XU units of 32 columns at a
@@ -312,7 +339,7 @@ __device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, i
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) load_codes<NV, EDGE>(g.w, row[t], (st + i) * kStep, q, c[i][t]);
+      for (int t = 0; t < RT; ++t) load_codes<NV, EDGE>(g.w, row0 + 16 * t, (st + i) * kStep, lane, c[i][t]);
 #pragma unroll
     for (int u0 = 0; u0 < 4 * N; u0 += XU) {
       u32x4_a1 x[XU][NT];
@@ -322,14 +349,18 @@ __device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, i
         for (int n = 0; n < NT; ++n) {
           const int at = (st + (u0 + u) / 4) * kStep + 32 * ((u0 + u) % 4);
           // behind the last column the codes are zeros: x there is the last eight again
-          x[u][n] = *(const u32x4_a1 *)(x_of[n] + (EDGE ? min(at, cols - 8 - 8 * q) : at));
+          x[u][n] = *(const u32x4_a1 *)(x_of[n] + (EDGE ? min(at, cols - 8 - 8 * (lane & 3)) : at));
         }
+#pragma unroll
+      for (int u = 0; u < XU; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[u][n] = spread(x[u][n], mine, lane);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int u = 0; u < XU; ++u) {
           const int i = (u0 + u) / 4, e = (u0 + u) % 4;
-          if (e == 0) transpose4(c[i][t].w);
+          if (e == 0) arrange<NV>(c[i][t], mine, lane);
           const ushortx8 a = decode4<NV>(c[i][t].w[e], scale_of<NV>(c[i][t], e, q));
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[t][n] = mfma16_bf16(a, __builtin_bit_cast(ushortx8, x[u][n]), acc[t][n]);
@@ -389,7 +420,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
         if (t == at) acc[t][n] = v * whole_scale;
     }
   } else {
-    columns<NV, NT, RT, Z>(g, row0, wave, waves, r, q, acc);
+    columns<NV, NT, RT, Z>(g, row0, wave, waves, lane, (uint8_t *)(sums + wave * RT * NT * 256), acc);
   }
 #pragma unroll
   for (int t = 0; t < RT; ++t)
