@@ -1,0 +1,257 @@
+"""GPU parity of the head norm with rotation and of its gradient with the fp64
+oracle (oracle/attention.py) on the inputs the GPU is given.
+
+Tolerances, u = 2^-24 (half a step of fp32), n = head size. A head's sums are
+formed in a lane (up to 8 terms) and over up to 64 lanes (6 steps), each adding
+u, so a sum of positive terms is within 16 u, with the product by 1 / n and the
+addition of eps within 18 u of the second moment: rstd within 9 u, and 3 u of
+the square root and the quotient: 12 u. A layer norm's mean is within 17 u of
+sum |x| / n =: 17 u a; with d = x - mean, xh is off by 17 u a rstd + 14 u |xh|
+(the shift changes the second moment in the second order only). So with
+e = 14 u |xh| + [layer] 18 u a rstd + and u = xh w one step more,
+  y:  |c| e_a + |s| e_b + 2 u (|u_a c| + |u_b s|) + hs |y|,
+hs the output's half step. Backward: g = turned back, 2 u (|dy_a c| + |dy_b s|),
+u = g w one more; the two sums over the head 17 u of their magnitudes and what
+their terms are off by; dx = rstd (u - su - xh sx) adds 4 u of its terms, 12 u
+of rstd and hs. dw: its terms are off by |g| e + |xh| e_g + u |g xh|, and sums
+over groups, workgroups and parts add at most 200 + items u of sum |g xh|."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as O
+from tests import _attn as A
+from tests import _ffn as H
+
+pytestmark = pytest.mark.gpu
+
+import fp4_spectral_split_amd as M
+
+U = H.U32
+EPS = 1e-5
+# tokens, query heads, key heads, head size, turned elements
+SHAPES = [(1, 32, 8, 128, 128), (1, 1, 0, 64, 64), (3, 5, 2, 96, 48), (7, 4, 1, 256, 256), (2, 3, 3, 512, 64), (5, 2, 1, 90, 30),
+          (4, 3, 2, 33, 32), (6, 2, 1, 1, 0), (5, 2, 2, 7, 2), (9, 2, 1, 200, 12), (3, 2, 2, 511, 510), (300, 36, 4, 64, 64),
+          (130, 9, 3, 80, 80), (64, 2, 2, 160, 0)]
+
+
+def _inputs(shape, seed):
+    T, hq, hk, D, rot = shape
+    g = H.rng(seed)
+    x = g.standard_normal((T, hq + hk, D)) * np.exp(0.4 * g.standard_normal((1, 1, D))) + 0.2
+    table = A.angles(T + 50, rot)
+    pos = g.permutation(T + 50)[:T].astype(np.int32)
+    return (x[:, :hq].reshape(T, -1), x[:, hq:].reshape(T, -1), table, pos, 1.0 + 0.3 * g.standard_normal((2, D)),
+            1e-2 * g.standard_normal((T, hq * D)), 1e-2 * g.standard_normal((T, hk * D)))
+
+
+def _terms(x, w, rows, kind, pairs):
+    """(xh, rstd, error of xh)."""
+    d, rstd = O.head_stats(x, kind, EPS)
+    xh = d * rstd
+    e = 0.0 * xh if kind is None else 14 * U * np.abs(xh)
+    if kind == "layer":
+        e = e + 18 * U * np.abs(x).mean(-1, keepdims=True) * rstd
+    return xh, rstd, e
+
+
+def _turned_size(a, rows, pairs):
+    """|a| |c| + |b| |s| for the pairs, |.| for the others."""
+    big = np.concatenate([np.abs(rows[:, :rows.shape[1] // 2]), -np.abs(rows[:, rows.shape[1] // 2:])], axis=1)
+    out = np.abs(a).copy()
+    if rows.shape[1]:
+        ia, ib = O.pair_index(rows.shape[1], pairs)
+        c, s = np.abs(rows[:, None, :rows.shape[1] // 2]), np.abs(rows[:, None, rows.shape[1] // 2:])
+        x, y = np.abs(a[..., ia]), np.abs(a[..., ib])
+        out[..., ia], out[..., ib] = x * c + y * s, y * c + x * s
+    del big
+    return out
+
+
+def _check_fwd(y, x, w, rows, kind, pairs, odt, what):
+    D = x.shape[-1]
+    want = O.norm_rope_fwd(x, w, rows, kind, EPS, pairs)
+    xh, _, e = _terms(x, w, rows, kind, pairs)
+    wa = 1.0 if w is None else np.abs(w)
+    tol = _turned_size((e + U * np.abs(xh)) * wa, rows, pairs) + 2 * U * _turned_size(xh * wa, rows, pairs)
+    A.close(H.np64(y).reshape(want.shape), want, tol * 1.01 + H.HALF[odt] * 1.01 * np.abs(want) + 1e-37, what)
+    assert D
+
+
+def _check_bwd(dx, dw, dy, x, w, rows, kind, pairs, odt, what):
+    want, wdw = O.norm_rope_bwd(dy, x, w, rows, kind, EPS, pairs)
+    g = O.turn(dy, rows, pairs, back=True)
+    eg = 2 * U * _turned_size(dy, rows, pairs)
+    tol = eg
+    if kind is not None:
+        xh, rstd, e = _terms(x, w, rows, kind, pairs)
+        wa = 1.0 if w is None else np.abs(w)
+        u, eu = np.abs(g) * wa, (eg + U * np.abs(g)) * wa
+        n = x.shape[-1]
+        sx = np.abs((g * (1.0 if w is None else w) * xh).mean(-1, keepdims=True))
+        esx = ((u * e + np.abs(xh) * eu).sum(-1, keepdims=True) + 19 * U * (u * np.abs(xh)).sum(-1, keepdims=True)) / n
+        su = esu = 0.0
+        if kind == "layer":
+            su = np.abs((g * (1.0 if w is None else w)).mean(-1, keepdims=True))
+            esu = (eu.sum(-1, keepdims=True) + 18 * U * u.sum(-1, keepdims=True)) / n
+        tol = rstd * (eu + esu + np.abs(xh) * esx + sx * e + 4 * U * (u + su + np.abs(xh) * sx)) + 12 * U * np.abs(want)
+        if dw is not None:
+            items = x.shape[0] * x.shape[1]
+            tw = (np.abs(g) * e + np.abs(xh) * eg).sum((0, 1)) + (200 + items) * U * (np.abs(g) * np.abs(xh)).sum((0, 1))
+            A.close(H.np64(dw), wdw, tw * 1.01 + 1e-37, what + " dw")
+    A.close(H.np64(dx).reshape(want.shape), want, tol * 1.01 + H.HALF[odt] * 1.01 * np.abs(want) + 1e-37, what)
+
+
+def _place(a, dtype, pad, shift):
+    return H.to_dev(a, dtype, pad, shift) if a.shape[1] else None
+
+
+CONFIGS = [("rms", "halves", "f32", "bf16", "f32"), ("layer", "neighbours", "bf16", "f32", "bf16"),
+           (None, "halves", "bf16", "bf16", None), ("rms", "neighbours", "bf16", "bf16", None), ("layer", "halves", "f32", "f32", "f32"),
+           (None, "neighbours", "f32", "f32", None)]
+
+
+@pytest.mark.parametrize("kind,pairs,dtype,odt,wdt", CONFIGS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_gradient(shape, kind, pairs, dtype, odt, wdt):
+    T, hq, hk, D, rot = shape
+    q, k, table, pos, w, dq, dk = _inputs(shape, 71)
+    qd, kd = _place(q, H.T[dtype], 3, 1), _place(k, H.T[dtype], 0, 0)
+    wq = wk = None
+    if wdt:
+        wq, wk = (A.dev(v, H.T[wdt]) for v in w)
+    rope, p = A.dev(table), A.dev(pos)
+    outs = [H.Guard(T, n, H.T[odt], pad=s, shift=s) if n else None for n, s in ((hq * D, 5), (hk * D, 1))]
+    how = dict(kind=kind, eps=EPS, pairs=pairs)
+    print("case qk fwd", shape, kind, pairs, dtype, odt, wdt, flush=True)
+    got = M.metis_qk_norm_rope_fwd(qd, kd, p, rope, D, wq, wk if hk else None, dtype=H.T[odt],
+                                   out_q=outs[0].t, out_k=outs[1].t if hk else None, **how)
+    torch.cuda.synchronize()
+    assert all(o.intact() for o in outs if o)
+    rows = table[pos].astype(np.float64)
+    sides = [(got[0], qd, wq, hq)] + ([(got[1], kd, wk, hk)] if hk else [])
+    for i, (y, x, wt, heads) in enumerate(sides):
+        _check_fwd(y, H.np64(x).reshape(T, heads, D), None if wt is None else H.np64(wt), rows, kind, pairs, H.T[odt], "qk"[i])
+    # the gradient, its dy of the output's type and dx of the input's
+    dqd, dkd = _place(dq, H.T[odt], 2, 1), _place(dk, H.T[odt], 0, 3)
+    outs = [H.Guard(T, n, H.T[dtype], pad=s, shift=s) if n else None for n, s in ((hq * D, 1), (hk * D, 2))]
+    print("case qk bwd", shape, kind, pairs, dtype, odt, wdt, flush=True)
+    back = M.metis_qk_norm_rope_bwd(dqd, dkd, qd, kd, p, rope, D, wq, wk if hk else None, dtype=H.T[dtype],
+                                    need_dweight=kind is not None, out_q=outs[0].t, out_k=outs[1].t if hk else None, **how)
+    torch.cuda.synchronize()
+    assert all(o.intact() for o in outs if o) and (kind is None) == (back[2] is None) and (kind is None or not hk) == (back[3] is None)
+    for i, (y, x, wt, heads) in enumerate(sides):
+        _check_bwd(back[i], back[2 + i], H.np64((dqd, dkd)[i]).reshape(T, heads, D), H.np64(x).reshape(T, heads, D),
+                   None if wt is None else H.np64(wt), rows, kind, pairs, H.T[dtype], "d" + "qk"[i])
+
+
+def test_gradient_against_differences():
+    """The kernel's gradient against differences of the kernel's forward pass in
+    fp32: a step h = 2^-6 is off by h^2 / 6 times the third derivative (below 40
+    for heads of unit scale, as sum |dy| is below 1 here), and 2 x 40 u / 2 h."""
+    T, hq, D, rot = 2, 2, 16, 16
+    q, _, table, pos, w, dq, _ = _inputs((T, hq, 0, D, rot), 72)
+    dq *= 0.5 / np.abs(dq).sum()
+    qd, dy, wq, rope, p = A.dev(q, torch.float32), A.dev(dq, torch.float32), A.dev(w[0], torch.float32), A.dev(table), A.dev(pos)
+    for kind in ("rms", "layer"):
+        f = lambda x, w: float((H.np64(M.metis_qk_norm_rope_fwd(x, None, p, rope, D, w, kind=kind)[0]) * H.np64(dy)).sum())  # noqa: E731
+        dx, _, dw, _ = M.metis_qk_norm_rope_bwd(dy, None, qd, None, p, rope, D, wq, kind=kind)
+        h = 2.0 ** -6
+        tol = h * h / 6 * 40 + 40 * U / h
+        for t, grad, second in ((qd, dx, False), (wq, dw, True)):
+            flat = t.view(-1)
+            for i in range(0, flat.numel(), 3):
+                keep = flat[i].item()
+                flat[i] = keep + h
+                hi, up = f(qd, wq), flat[i].item()
+                flat[i] = keep - h
+                lo, down = f(qd, wq), flat[i].item()
+                flat[i] = keep
+                assert abs((hi - lo) / (up - down) - grad.view(-1)[i].item()) <= tol, (kind, second, i)
+
+
+def test_positions_outside_the_table_and_weights_absent():
+    T, hq, D, rot = 5, 2, 64, 32
+    q, _, table, pos, _, _, _ = _inputs((T, hq, 0, D, rot), 73)
+    pos[1], pos[3] = -1, len(table)
+    y, _ = M.metis_qk_norm_rope_fwd(A.dev(q, torch.float32), None, A.dev(pos), A.dev(table), D)
+    torch.cuda.synchronize()
+    y = H.np64(y).reshape(T, hq, D)
+    assert np.isnan(y[[1, 3], :, :rot]).all() and np.isfinite(y[[1, 3], :, rot:]).all() and np.isfinite(y[[0, 2, 4]]).all()
+    want = O.norm_rope_fwd(q.astype(np.float32).astype(np.float64).reshape(T, hq, D), None, np.zeros((T, 0)), "rms", 1e-6, "halves")
+    assert np.allclose(y[..., rot:], want[..., rot:], rtol=1e-5, atol=1e-6)
+
+
+def test_ends_of_the_range():
+    """A NaN or an infinity spoils its own head; a head of zeros stays zeros;
+    squares past fp32's range give rstd 0, large finite heads a finite mean."""
+    D = 128
+    x = H.rng(74).standard_normal((4, 3 * D)).astype(np.float32)
+    x[0, 5], x[1, D + 7], x[2, :D], x[3, :D] = np.nan, np.inf, 0.0, 3e38
+    y, _ = M.metis_qk_norm_rope_fwd(A.dev(x), None, None, None, D, kind="rms")
+    z, _ = M.metis_qk_norm_rope_fwd(A.dev(x), None, None, None, D, kind="layer")
+    torch.cuda.synchronize()
+    y, z = H.np64(y).reshape(4, 3, D), H.np64(z).reshape(4, 3, D)
+    for a in (y, z):
+        assert np.isnan(a[0, 0]).any() and np.isfinite(a[0, 1:]).all() and not np.isfinite(a[1, 1]).all() and np.isfinite(a[1, [0, 2]]).all()
+        assert np.all(a[2, 0] == 0)
+    assert np.all(y[3, 0] == 0) and np.all(np.abs(z[3, 0]) < 1e35) and np.isfinite(z[3]).all()
+
+
+def test_accumulate_empty_and_same_bits_twice():
+    T, hq, hk, D, rot = 700, 9, 3, 64, 64
+    q, k, table, pos, w, dq, dk = _inputs((T, hq, hk, D, rot), 75)
+    a = [A.dev(v, torch.bfloat16) for v in (dq, dk, q, k)] + [A.dev(pos), A.dev(table), D]
+    wq, wk = (A.dev(v, torch.float32) for v in w)
+    first, second = (M.metis_qk_norm_rope_bwd(*a, wq, wk, dtype=torch.float32) for _ in range(2))
+    assert all(torch.equal(x, y) for x, y in zip(first, second))
+    gq, gk = torch.full((D,), 2.0, device="cuda"), torch.full((D,), -1.0, device="cuda")
+    M.metis_qk_norm_rope_bwd(*a, wq, wk, dweight_q=gq, dweight_k=gk, accumulate=True)
+    assert torch.equal(gq, first[2] + 2.0) and torch.equal(gk, first[3] - 1.0)
+    none = [t[:0] for t in a[:5]] + a[5:]
+    out = M.metis_qk_norm_rope_bwd(*none, wq, wk, dweight_q=gq, dweight_k=gk)
+    torch.cuda.synchronize()
+    assert out[0].shape == (0, hq * D) and not gq.any() and not gk.any()
+    gq.fill_(3.0)
+    M.metis_qk_norm_rope_bwd(*none, wq, wk, dweight_q=gq, dweight_k=gk, accumulate=True)
+    assert torch.equal(gq, torch.full((D,), 3.0, device="cuda"))
+    y, _ = M.metis_qk_norm_rope_fwd(a[2][:0], a[3][:0], a[4][:0], a[5], D)
+    assert y.shape == (0, hq * D)
+
+
+def test_rows_past_32_bit_offsets():
+    """Three tokens 2^31 elements apart, read and written."""
+    D, heads, ld = 64, 2, 1 << 31
+    buf = torch.zeros(2 * ld + heads * D, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, heads * D), (ld, 1))
+    x.copy_(A.dev(H.rng(76).standard_normal((3, heads * D)), torch.bfloat16))
+    table, pos = A.angles(8, D), np.array([7, 0, 3], np.int32)
+    want, _ = M.metis_qk_norm_rope_fwd(x.contiguous(), None, A.dev(pos), A.dev(table), D)
+    got, _ = M.metis_qk_norm_rope_fwd(x, None, A.dev(pos), A.dev(table), D)
+    out = buf.as_strided((3, heads * D), (ld, 1), 0)[:, :]
+    assert torch.equal(got, want)
+    src = x.contiguous()
+    M.metis_qk_norm_rope_fwd(src, None, A.dev(pos), A.dev(table), D, out_q=out)
+    dx = M.metis_qk_norm_rope_bwd(out, None, out, None, A.dev(pos), A.dev(table), D)[0]
+    ref = M.metis_qk_norm_rope_bwd(want, None, want, None, A.dev(pos), A.dev(table), D)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(dx, ref)
+    del buf, x, out
+
+
+def test_refusals():
+    q, p, r = torch.zeros(4, 256, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(9, 64, device="cuda")
+    w = torch.ones(128, device="cuda")
+    f = M.metis_qk_norm_rope_fwd
+    for call in (lambda: f(q, None, p, r, 100), lambda: f(q, q[:3], p, r, 128), lambda: f(q, q.bfloat16(), p, r, 128),
+                 lambda: f(q, None, p.long(), r, 128), lambda: f(q, None, p[:3], r, 128), lambda: f(q, None, None, r, 128),
+                 lambda: f(q, None, p, r.double(), 128), lambda: f(q, None, p, r[:, ::2], 128), lambda: f(q, None, p, r, 32),
+                 lambda: f(q, None, p, r, 128, w[:64]), lambda: f(q, None, p, r, 128, w, w), lambda: f(q, None, p, r, 128, w, kind=None),
+                 lambda: f(q, q, p, r, 128, w, w.bfloat16()), lambda: f(q, None, p, r, 128, kind="batch"),
+                 lambda: f(q, None, p, r, 128, pairs="thirds"), lambda: f(q, None, p, r, 128, out_q=q),
+                 lambda: f(q.half(), None, p, r, 128), lambda: f(q, None, p, r, 128, eps=-1.0),
+                 lambda: M.metis_qk_norm_rope_bwd(q, None, None, None, p, r, 128),
+                 lambda: M.metis_qk_norm_rope_bwd(q, None, q, None, p, r, 128, w, accumulate=True),
+                 lambda: M.metis_qk_norm_rope_bwd(q, q, q, None, p, r, 128)):
+        with pytest.raises(M.MetisError):
+            call()
