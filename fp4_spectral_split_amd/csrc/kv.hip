@@ -225,7 +225,7 @@ template <typename T, bool NV> __global__ void __launch_bounds__(256) append_ker
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float q = v[i] * inv, c = fmaf(fmaf(-q, by, v[i]), inv, q);
-          v[i] = fabsf(q) < 0x1p20f ? c : q;
+          v[i] = fabsf(q) < 0x1p20f ? copysignf(c, q) : q;  // (a zero's remainder has lost its sign)
         }
       } else {
 #pragma unroll
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
   const int j0 = (int)g.by_group.div((uint32_t)(tile * kRowsQ));
   const int j1 = min(count - 1, (int)g.by_group.div((uint32_t)(tile * kRowsQ + kRowsQ - 1)));
   const int hi = beyond ? 0 : max(0, length - new_tokens + j1 + 1);
-  const int lo = (int)(g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0) / kTile * kTile;
+  const int first = (int)(g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0);
+  const int lo = first / kTile * kTile;
   // all of it, whatever the length that the launch was made for
   const int each = (max(hi - lo, 0) + g.splits - 1) / g.splits;
   const int chunk = max(g.chunk, (each + kStepTokens - 1) / kStepTokens * kStepTokens);
@@ -458,12 +459,16 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
     load(now, t);
     for (; base < to; base += kStepTokens) {
       const bool bad0 = now.bad[0], bad1 = now.bad[HALVES ? 1 : 0];
-      // v to LDS as bf16; behind the last token, where the cache may hold
-      // anything, the scale of zero (mxfp4: 2^-127): finite, and times p = 0
+      // v to LDS as bf16; where no row looks (before the window, behind the last
+      // token, in pages outside the cache) there may be anything: there the scale
+      // byte of zero (mxfp4: 2^-127), finite, and times p = 0
+      const bool any_bad = __ballot(bad0 || bad1) != 0;
 #pragma unroll
       for (int x = 0; x < kV; ++x) {
         const int piece = lane + 64 * x, token = piece / NC, c = piece - token * NC;
-        const uint32_t byte = base + token < to ? t.vs[x] : 0u;
+        bool seen = (unsigned)(base + token - first) < (unsigned)(to - first);
+        if (any_bad) seen = seen && !(HALVES ? (token < 16 ? bad0 : bad1) : __shfl((int)bad0, token & 31, 64) != 0);
+        const uint32_t byte = seen ? t.vs[x] : 0u;
         const float s0 = scale4<NV>(byte & 255u), s1 = NV ? scale4<NV>(byte >> 8) : s0;
         ushortx8 *dst = (ushortx8 *)(mine + token * kStride + c * 64);
         if (kTile * NC % 64 == 0 || piece < kTile * NC) {
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
           p[i] = token >= begin && token < end ? p[i] : -INFINITY;
         }
       }
-      if (__ballot(bad0 || bad1)) {  // a page outside the cache: its tokens have no scores
+      if (any_bad) {  // a page outside the cache: its tokens have no scores
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool bad = HALVES ? was.bad[i / 4] : __shfl((int)was.bad[0], 16 * (i / 4) + 4 * gq + i % 4, 64) != 0;

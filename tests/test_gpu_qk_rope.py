@@ -57,25 +57,21 @@ def _terms(x, w, rows, kind, pairs):
 
 def _turned_size(a, rows, pairs):
     """|a| |c| + |b| |s| for the pairs, |.| for the others."""
-    big = np.concatenate([np.abs(rows[:, :rows.shape[1] // 2]), -np.abs(rows[:, rows.shape[1] // 2:])], axis=1)
     out = np.abs(a).copy()
     if rows.shape[1]:
         ia, ib = O.pair_index(rows.shape[1], pairs)
         c, s = np.abs(rows[:, None, :rows.shape[1] // 2]), np.abs(rows[:, None, rows.shape[1] // 2:])
         x, y = np.abs(a[..., ia]), np.abs(a[..., ib])
         out[..., ia], out[..., ib] = x * c + y * s, y * c + x * s
-    del big
     return out
 
 
 def _check_fwd(y, x, w, rows, kind, pairs, odt, what):
-    D = x.shape[-1]
     want = O.norm_rope_fwd(x, w, rows, kind, EPS, pairs)
     xh, _, e = _terms(x, w, rows, kind, pairs)
     wa = 1.0 if w is None else np.abs(w)
     tol = _turned_size((e + U * np.abs(xh)) * wa, rows, pairs) + 2 * U * _turned_size(xh * wa, rows, pairs)
     A.close(H.np64(y).reshape(want.shape), want, tol * 1.01 + H.HALF[odt] * 1.01 * np.abs(want) + 1e-37, what)
-    assert D
 
 
 def _check_bwd(dx, dw, dy, x, w, rows, kind, pairs, odt, what):
