@@ -855,38 +855,50 @@ def _pairs(pairs):
     return p
 
 
-def _rope(rope, device):
+def _on(t, name, index, dtype, dim, n):
+    """Address of a contiguous tensor of the given type, number of axes and
+    (with n) elements, on device `index`."""
+    try:
+        if t.dtype is dtype and t.dim() == dim and (n is None or t.numel() == n) and t.is_contiguous():
+            if t.get_device() == index:
+                return t.data_ptr()
+            raise MetisError("%s is not on the device of the other operands" % name)
+    except AttributeError:  # no tensor
+        pass
+    raise MetisError("%s must be a contiguous %d-D CUDA tensor of %s%s" % (name, dim, dtype, "" if n is None else " and %d elements" % n))
+
+
+def _rope(rope, index):
     """Checks an optional table of angles; returns (address, rows, elements
     turned)."""
     if rope is None:
         return None, 0, 0
-    if (not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype != torch.float32
-            or not rope.is_contiguous() or not rope.is_cuda):
-        raise MetisError("rope must be a contiguous 2-D float32 CUDA tensor")
-    if rope.device != device:
-        raise MetisError("rope is on %s, the other operands on %s" % (rope.device, device))
-    return rope.data_ptr(), rope.shape[0], rope.shape[1]
+    p = _on(rope, "rope", index, torch.float32, 2, None)
+    rows, rot = rope.shape
+    return p, rows, rot
 
 
-def _qk_common(q, k, positions, rope, head_dim, weight_q, weight_k, kind, tokens, dev):
+def _qk_common(positions, rope, head_dim, weight_q, weight_k, kind, tokens, keys, index):
     """The arguments that both directions share: (kind, weights' addresses and
     type, position and rope arguments)."""
     kd = NORM_NONE if kind is None else _norm_kind(kind)
-    for w, name in ((weight_q, "weight_q"), (weight_k, "weight_k")):
-        if w is not None and kd == NORM_NONE:
-            raise MetisError("%s needs a norm" % name)
-    if weight_k is not None and k is None:
-        raise MetisError("weight_k without k")
-    wq = _vector(weight_q, "weight_q", head_dim, dev)
-    wk = _vector(weight_k, "weight_k", head_dim, dev, weight_q.dtype if weight_q is not None else None)
-    wt = weight_q if weight_q is not None else weight_k
-    rp, rows, rot = _rope(rope, dev)
-    pos = None
+    wq = wk = pos = None
+    wdt = F32
+    if weight_q is not None or weight_k is not None:
+        if kd == NORM_NONE:
+            raise MetisError("weights need a norm")
+        if weight_k is not None and not keys:
+            raise MetisError("weight_k without k")
+        dtype = (weight_q if weight_q is not None else weight_k).dtype
+        wdt = _code(dtype)
+        if weight_q is not None:
+            wq = _on(weight_q, "weight_q", index, dtype, 1, head_dim)
+        if weight_k is not None:
+            wk = _on(weight_k, "weight_k", index, dtype, 1, head_dim)
+    rp, rows, rot = _rope(rope, index)
     if rope is not None:
-        if positions is None:
-            raise MetisError("the rotation needs positions")
-        pos = _vector(positions, "positions", tokens, dev, torch.int32)
-    return kd, wq, wk, _code(wt.dtype) if wt is not None else F32, pos, rp, rows, rot
+        pos = _on(positions, "positions", index, torch.int32, 1, tokens)
+    return kd, wq, wk, wdt, pos, rp, rows, rot
 
 
 def metis_qk_norm_rope_fwd(q, k, positions, rope, head_dim, weight_q=None, weight_k=None, kind="rms", eps=1e-6,
@@ -908,8 +920,8 @@ def metis_qk_norm_rope_fwd(q, k, positions, rope, head_dim, weight_q=None, weigh
         ldk, hk = _heads(k, "k", head_dim, dev)
         if k.shape[0] != tokens or k.dtype != q.dtype:
             raise MetisError("q and k must be of one type and have one row per token")
-    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(q, k, positions, rope, head_dim, weight_q, weight_k, kind, tokens,
-                                                     dev)
+    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(positions, rope, head_dim, weight_q, weight_k, kind, tokens, hk,
+                                                     q.get_device())
     dtype = q.dtype if dtype is None else dtype
     odt = _code(dtype)
     out_q, ldqo = _out(out_q, "out_q", q, dtype, dev)
@@ -922,6 +934,11 @@ def metis_qk_norm_rope_fwd(q, k, positions, rope, head_dim, weight_q=None, weigh
          tokens, head_dim, wq, wk, wdt, kd, eps, pos, rp, rows, rot, _pairs(pairs), out_q.data_ptr(), ldqo,
          None if k is None else out_k.data_ptr(), ldko, odt)
     return out_q, out_k
+
+
+@functools.lru_cache(maxsize=1024)
+def _qk_workspace(tokens, q_heads, k_heads, head_dim):
+    return load().metis_qk_norm_rope_bwd_workspace_bytes(tokens, q_heads, k_heads, head_dim)
 
 
 def metis_qk_norm_rope_bwd(dq, dk, q, k, positions, rope, head_dim, weight_q=None, weight_k=None, kind="rms", eps=1e-6,
@@ -939,8 +956,8 @@ def metis_qk_norm_rope_bwd(dq, dk, q, k, positions, rope, head_dim, weight_q=Non
         lddk, hk = _heads(dk, "dk", head_dim, dev)
         if dk.shape[0] != tokens or dk.dtype != dq.dtype:
             raise MetisError("dq and dk must be of one type and have one row per token")
-    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(dq, dk, positions, rope, head_dim, weight_q, weight_k, kind,
-                                                     tokens, dev)
+    kd, wq, wk, wdt, pos, rp, rows, rot = _qk_common(positions, rope, head_dim, weight_q, weight_k, kind, tokens, hk,
+                                                     dq.get_device())
     qp = kp = None
     dt = F32
     if kd != NORM_NONE:
@@ -970,8 +987,8 @@ def metis_qk_norm_rope_bwd(dq, dk, q, k, positions, rope, head_dim, weight_q=Non
         dweight_k, wkp = _sum_out(dweight_k, "dweight_k", head_dim, dev)
     L, nws = load(), 0
     if want_q or want_k:  # a buffer of its own per call, as in metis_norm_bwd
-        nws = L.metis_qk_norm_rope_bwd_workspace_bytes(tokens, hq, hk, head_dim)
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        nws = _qk_workspace(tokens, hq, hk, head_dim)
+        ws = dq.new_empty(nws, dtype=torch.uint8)
     _run(dev, L.metis_qk_norm_rope_bwd, dq.data_ptr(), lddq, None if dk is None else dk.data_ptr(), lddk, dydt, qp,
          ldq, hq, kp, ldk, hk, dt, tokens, head_dim, wq, wk, wdt, kd, eps, pos, rp, rows, rot, _pairs(pairs),
          out_q.data_ptr(), lddqi, None if dk is None else out_k.data_ptr(), lddki, dxdt, wqp, wkp,
@@ -1030,9 +1047,7 @@ def metis_fp4_gemv(x, W, dtype=None, out=None):
     if k:
         w.Ut_q = _fp4_buffers(W.Ut_q, "Ut_q", k, m, index, fmt)
         w.Vt_q = _fp4_buffers(W.Vt_q, "Vt_q", k, n, index, fmt)
-        w.S = _vector(W.S, "S", k, x.device, torch.float32)
-        if not w.S:
-            raise MetisError("a split weight needs its S")
+        w.S = _on(W.S, "S", index, torch.float32, 1, k)
     dtype = x.dtype if dtype is None else dtype
     ydt = _code(dtype)
     if out is None:
@@ -1137,10 +1152,9 @@ def _batch(batch, device):
     if t.dtype != torch.int32:
         raise MetisError("table must be int32")
     seqs, pages = t.shape
-    lengths = _vector(batch.lengths, "lengths", seqs, device, torch.int32)
-    if lengths is None:
-        raise MetisError("a batch needs its lengths")
-    starts = _vector(batch.starts, "starts", seqs + 1, device, torch.int32)
+    index = t.get_device()
+    lengths = _on(batch.lengths, "lengths", index, torch.int32, 1, seqs)
+    starts = None if batch.starts is None else _on(batch.starts, "starts", index, torch.int32, 1, seqs + 1)
     return _KvBatch(t.data_ptr(), lengths, starts, ldt, seqs, pages)
 
 
@@ -1168,7 +1182,7 @@ def metis_kv_append(k, v, batch, cache, rope=None, pairs="halves"):
     ldv = _matrix(v, "v", k.shape, dev)
     if v.dtype != k.dtype:
         raise MetisError("k and v must be of one type")
-    rp, rows, rot = _rope(rope, dev)
+    rp, rows, rot = _rope(rope, k.get_device())
     _run(dev, load().metis_kv_append, k.data_ptr(), ldk, v.data_ptr(), ldv, dt, k.shape[0], b, rp, rows, rot,
          _pairs(pairs), c)
     return cache

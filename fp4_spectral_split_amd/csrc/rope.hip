@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBwdThreads = 512;
 constexpr int kMaxDim = 512, kMaxHeads = 65536;
+constexpr int kFwdGrid = 1024;  // workgroups of the forward pass that go through rounds
 constexpr int kParts = 512;  // partial sums of dwq and dwk together, at most
 
 template <int CTRL> __device__ __forceinline__ float dpp_f32(float v) {
@@ -42,24 +43,47 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Four elements at once or one, as fp32.
-template <int W> __device__ __forceinline__ void load_part(const float *p, float *v) {
-  if (W == 4) {
-    const u32x4_a1 r = *(const u32x4_a1 *)p;
+// Four elements or one as loaded, and as fp32.
+template <typename T, int W> struct Part {
+  static constexpr int kWords = W * (int)sizeof(T) >= 4 ? W * (int)sizeof(T) / 4 : 1;
+  uint32_t w[kWords];
+};
+template <int W> __device__ __forceinline__ void load_raw_part(const float *p, Part<float, W> &r) {
+  if constexpr (W == 4) {
+    const u32x4_a1 v = *(const u32x4_a1 *)p;
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 4; ++i) r.w[i] = v[i];
   } else {
-    v[0] = *p;
+    r.w[0] = __float_as_uint(*p);
   }
 }
-template <int W> __device__ __forceinline__ void load_part(const unsigned short *p, float *v) {
-  if (W == 4) {
-    const u32x2_a1 r = *(const u32x2_a1 *)p;
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = __uint_as_float(i % 2 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
+template <int W> __device__ __forceinline__ void load_raw_part(const unsigned short *p, Part<unsigned short, W> &r) {
+  if constexpr (W == 4) {
+    const u32x2_a1 v = *(const u32x2_a1 *)p;
+    r.w[0] = v[0];
+    r.w[1] = v[1];
   } else {
-    v[0] = bf16_to_f32(*p);
+    r.w[0] = *p;
   }
+}
+template <int W> __device__ __forceinline__ void value_of(const Part<float, W> &r, float *v) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+template <int W> __device__ __forceinline__ void value_of(const Part<unsigned short, W> &r, float *v) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = __uint_as_float(i % 2 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+}
+// Zeros where the part does not exist.
+template <int W, typename T> __device__ __forceinline__ void value_of(const Part<T, W> &r, bool there, float *v) {
+  value_of<W>(r, v);
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = there ? v[i] : 0.0f;
+}
+template <int W, typename T> __device__ __forceinline__ void load_part(const T *p, float *v) {
+  Part<T, W> r;
+  load_raw_part<W>(p, r);
+  value_of<W>(r, v);
 }
 template <int W> __device__ __forceinline__ void store_part(float *p, const float *v) {
   if (W == 4) {
@@ -177,14 +201,6 @@ template <int W> __device__ __forceinline__ void weights(const Shape &s, const U
   }
 }
 
-template <int W, typename T>
-__device__ __forceinline__ void load_unit(const Unit &u, const T *head, bool there, float *a, float *b) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) a[i] = b[i] = 0.0f;
-  if (there && u.a) load_part<W>(head + u.oa, a);
-  if (there && u.b) load_part<W>(head + u.ob, b);
-}
-
 // x to its deviation from the mean (layer); the reciprocal deviation. The mean
 // adds x / n, so that a finite head has a finite mean. A sum of squares past
 // fp32's range gives 0, as in the norm of whole rows.
@@ -223,62 +239,90 @@ struct FwdArgs {
   const void *w[2];
   int w_bf16;
   int heads[2];
-  int chunks;  // groups of H heads of a token
-  uint32_t units;
+  uint32_t units;  // H heads of a token each
   FastDiv by_chunks;
 };
 
-template <typename T, typename TO, int W, int G, int U, int H>
+// One round of a group: H heads of a token. ROUNDS: groups go through several,
+// the next one's heads and angles under way while one is worked on.
+template <typename T, typename TO, int W, int G, int U, int H, bool ROUNDS>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(FwdArgs g) {
-  const uint32_t unit = blockIdx.x * (uint32_t)(kThreads / G) + threadIdx.x / G;
-  if (unit >= g.units) return;  // whole groups
-  const int lane = threadIdx.x % G;
-  const uint32_t token = g.by_chunks.div(unit);
-  const int h0 = (int)(unit - token * g.by_chunks.d) * H;
+  const uint32_t first = blockIdx.x * (uint32_t)(kThreads / G) + threadIdx.x / G;
+  if (first >= g.units) return;  // whole groups
+  const uint32_t step = gridDim.x * (uint32_t)(kThreads / G);
+  const int lane = threadIdx.x % G, heads = g.heads[0] + g.heads[1];
   Unit un[U];
-  float a[H][U][W], b[H][U][W], c[U][W], sn[U][W];
-  const int position = g.s.positions ? g.s.positions[token] : 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) un[u] = unit_of<W>(g.s, lane + u * G);
+  struct Round {
+    Part<T, W> a[H][U], b[H][U];
+    float c[U][W], sn[U][W];
+  };
+  auto position_of = [&](uint32_t unit) { return g.s.positions && unit < g.units ? g.s.positions[g.by_chunks.div(unit)] : 0; };
+  auto load = [&](uint32_t unit, int position, Round &r) {
+    const uint32_t token = g.by_chunks.div(unit);
+    const int h0 = (int)(unit - token * g.by_chunks.d) * H;
 #pragma unroll
-  for (int h = 0; h < H; ++h) {
-    const int at = h0 + h, side = at >= g.heads[0];
-    const int head = side ? at - g.heads[0] : at;
-    const T *p = (const T *)(side ? g.x[1] : g.x[0]) + (int64_t)token * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.s.dim;
+    for (int h = 0; h < H; ++h) {
+      const int at = min(h0 + h, heads - 1), side = at >= g.heads[0], head = side ? at - g.heads[0] : at;
+      const T *p = (const T *)(side ? g.x[1] : g.x[0]) + (int64_t)token * (side ? g.ldx[1] : g.ldx[0]) + (int64_t)head * g.s.dim;
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_unit<W>(un[u], p, at < g.heads[0] + g.heads[1], a[h][u], b[h][u]);
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], position, c[u], sn[u]);
-  float wa[U][W], wb[U][W];
-#pragma unroll
-  for (int h = 0; h < H; ++h) {
-    const int at = h0 + h, side = at >= g.heads[0];
-    if (at >= g.heads[0] + g.heads[1]) break;
-    const int head = side ? at - g.heads[0] : at;
-    if (h == 0 || at == g.heads[0]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) weights<W>(g.s, un[u], side ? g.w[1] : g.w[0], g.w_bf16, wa[u], wb[u]);
-    }
-    float rstd = 1.0f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) pair<W>(g.s, a[h][u], b[h][u]);
-    if (!g.s.none) rstd = deviation<W, G, U>(g.s, un, a[h], b[h]);
-    TO *y = (TO *)(side ? g.y[1] : g.y[0]) + (int64_t)token * (side ? g.ldy[1] : g.ldy[0]) + (int64_t)head * g.s.dim;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float ya[W], yb[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float ua = a[h][u][i] * rstd * wa[u][i], ub = b[h][u][i] * rstd * wb[u][i];
-        // an element that is not turned stays itself, whatever stands beside it
-        ya[i] = un[u].angle >= 0 ? fmaf(ua, c[u][i], -(ub * sn[u][i])) : ua;
-        yb[i] = un[u].angle >= 0 ? fmaf(ub, c[u][i], ua * sn[u][i]) : ub;
+      for (int u = 0; u < U; ++u) {
+        if (un[u].a) load_raw_part<W>(p + un[u].oa, r.a[h][u]);
+        if (un[u].b) load_raw_part<W>(p + un[u].ob, r.b[h][u]);
       }
-      unpair<W>(g.s, ya, yb);
-      if (un[u].a) store_part<W>(y + un[u].oa, ya);
-      if (un[u].b) store_part<W>(y + un[u].ob, yb);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], position, r.c[u], r.sn[u]);
+  };
+  Round now = {}, next = {};
+  int position = position_of(first), ahead = ROUNDS ? position_of(first + step) : 0;
+  load(first, position, now);
+  float wa[2][U][W], wb[2][U][W];  // of q and of k
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int u = 0; u < U; ++u) weights<W>(g.s, un[u], g.w[side], g.w_bf16, wa[side][u], wb[side][u]);
+  for (uint32_t unit = first; unit < g.units; unit += step) {
+    if (ROUNDS) {
+      position = ahead;
+      ahead = position_of(unit + 2 * step);
+      if (unit + step < g.units) load(unit + step, position, next);
+    }
+    const uint32_t token = g.by_chunks.div(unit);
+    const int h0 = (int)(unit - token * g.by_chunks.d) * H;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int at = h0 + h, side = at >= g.heads[0];
+      if (at >= heads) break;
+      const int head = side ? at - g.heads[0] : at;
+      float a[U][W], b[U][W], rstd = 1.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        value_of<W>(now.a[h][u], un[u].a, a[u]);
+        value_of<W>(now.b[h][u], un[u].b, b[u]);
+        pair<W>(g.s, a[u], b[u]);
+      }
+      if (!g.s.none) rstd = deviation<W, G, U>(g.s, un, a, b);
+      TO *y = (TO *)(side ? g.y[1] : g.y[0]) + (int64_t)token * (side ? g.ldy[1] : g.ldy[0]) + (int64_t)head * g.s.dim;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float ya[W], yb[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float ua = a[u][i] * rstd * (side ? wa[1][u][i] : wa[0][u][i]);
+          const float ub = b[u][i] * rstd * (side ? wb[1][u][i] : wb[0][u][i]);
+          // an element that is not turned stays itself, whatever stands beside it
+          ya[i] = un[u].angle >= 0 ? fmaf(ua, now.c[u][i], -(ub * now.sn[u][i])) : ua;
+          yb[i] = un[u].angle >= 0 ? fmaf(ub, now.c[u][i], ua * now.sn[u][i]) : ub;
+        }
+        unpair<W>(g.s, ya, yb);
+        if (un[u].a) store_part<W>(y + un[u].oa, ya);
+        if (un[u].b) store_part<W>(y + un[u].ob, yb);
+      }
+    }
+    if (!ROUNDS) break;
+    now = next;
   }
 }
 
@@ -320,21 +364,53 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(BwdArgs g) {
 #pragma unroll
     for (int i = 0; i < W; ++i) da[u][i] = db[u][i] = 0.0f;
   }
-  for (uint32_t unit = block * kGroups + grp; unit < units; unit += blocks * kGroups) {
+  // H heads of a token, as loaded. Those of the next round are asked for before a
+  // round is worked on, its position a round earlier still.
+  struct Round {
+    Part<TD, W> ga[H][U], gb[H][U];
+    Part<T, W> a[H][U], b[H][U];
+  };
+  const uint32_t step = blocks * kGroups;
+  auto load = [&](uint32_t unit, Round &r) {
     const uint32_t token = by.div(unit);
     const int h0 = (int)(unit - token * by.d) * H;
-    float ga[H][U][W], gb[H][U][W], a[H][U][W], b[H][U][W], c[U][W], sn[U][W];
-    const int position = g.s.positions ? g.s.positions[token] : 0;
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t off = (int64_t)(h0 + h) * dim;
-        load_unit<W>(un[u], dy + (int64_t)token * lddy + off, h0 + h < heads, ga[h][u], gb[h][u]);
-        load_unit<W>(un[u], x + (int64_t)token * ldx + off, !g.s.none && h0 + h < heads, a[h][u], b[h][u]);
+        const int64_t off = (int64_t)min(h0 + h, heads - 1) * dim;
+        const TD *pd = dy + (int64_t)token * lddy + off;
+        const T *px = x + (int64_t)token * ldx + off;
+        if (un[u].a) load_raw_part<W>(pd + un[u].oa, r.ga[h][u]);
+        if (un[u].b) load_raw_part<W>(pd + un[u].ob, r.gb[h][u]);
+        if (un[u].a && !g.s.none) load_raw_part<W>(px + un[u].oa, r.a[h][u]);
+        if (un[u].b && !g.s.none) load_raw_part<W>(px + un[u].ob, r.b[h][u]);
       }
+  };
+  auto position_of = [&](uint32_t unit) { return g.s.positions && unit < units ? g.s.positions[by.div(unit)] : 0; };
+  const uint32_t first = block * kGroups + grp;
+  Round now = {}, next = {};
+  int position = position_of(first), ahead = position_of(first + step);
+  if (first < units) load(first, now);
+  for (uint32_t unit = first; unit < units; unit += step) {
+    const uint32_t token = by.div(unit);
+    const int h0 = (int)(unit - token * by.d) * H;
+    float ga[H][U][W], gb[H][U][W], a[H][U][W], b[H][U][W], c[U][W], sn[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u) angles<W>(g.s, un[u], position, c[u], sn[u]);
+    position = ahead;
+    ahead = position_of(unit + 2 * step);
+    if (unit + step < units) load(unit + step, next);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        value_of<W>(now.ga[h][u], un[u].a, ga[h][u]);
+        value_of<W>(now.gb[h][u], un[u].b, gb[h][u]);
+        value_of<W>(now.a[h][u], un[u].a, a[h][u]);
+        value_of<W>(now.b[h][u], un[u].b, b[h][u]);
+      }
+    now = next;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       if (h0 + h >= heads) break;
@@ -449,33 +525,28 @@ Group group_of(int dim, int rot) {
   return {64, n <= 64 ? 1 : n <= 128 ? 2 : 4};
 }
 
-// Heads that a group takes of one token: four together where that still leaves
-// the GPU full.
-int heads_at_once(int64_t tokens, int heads, int most, int groups) {
-  return tokens * cdiv(heads, most) >= 2048 * (int64_t)groups ? most : 1;
-}
-
+// Few heads: one to a group, all at once. Many: two to a group, and rounds.
 template <typename T, typename TO, int W, int G, int U>
 void fwd_launch(FwdArgs g, int64_t tokens, hipStream_t stream) {
   constexpr int kGroups = kThreads / G;
   const int heads = g.heads[0] + g.heads[1];
-  const int at_once = heads_at_once(tokens, heads, 4, kGroups);
-  g.chunks = (int)cdiv(heads, at_once);
-  g.by_chunks.set((uint32_t)g.chunks);
-  const int64_t slab = slab_rows(g.chunks);
+  const bool rounds = tokens * heads >= 2 * kFwdGrid * (int64_t)kGroups;
+  const int chunks = (int)cdiv(heads, rounds ? 2 : 1);
+  g.by_chunks.set((uint32_t)chunks);
+  const int64_t slab = slab_rows(chunks);
   for (int64_t t0 = 0; t0 < tokens; t0 += slab) {
     const int64_t n = std::min(slab, tokens - t0);
     FwdArgs a = g;
-    a.units = (uint32_t)(n * g.chunks);
+    a.units = (uint32_t)(n * chunks);
     for (int s = 0; s < 2; ++s) {
       if (!g.heads[s]) continue;
       a.x[s] = (const T *)g.x[s] + t0 * g.ldx[s];
       a.y[s] = (TO *)g.y[s] + t0 * g.ldy[s];
     }
     if (a.s.positions) a.s.positions += t0;
-    const unsigned grid = (unsigned)cdiv(a.units, kGroups);
-    if (at_once == 4) qk_fwd_kernel<T, TO, W, G, U, 4><<<grid, kThreads, 0, stream>>>(a);
-    else qk_fwd_kernel<T, TO, W, G, U, 1><<<grid, kThreads, 0, stream>>>(a);
+    const int64_t grid = cdiv(a.units, kGroups);
+    if (rounds) qk_fwd_kernel<T, TO, W, G, U, 2, true><<<(unsigned)std::min<int64_t>(grid, kFwdGrid), kThreads, 0, stream>>>(a);
+    else qk_fwd_kernel<T, TO, W, G, U, 1, false><<<(unsigned)grid, kThreads, 0, stream>>>(a);
   }
 }
 
