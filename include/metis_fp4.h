@@ -512,9 +512,9 @@ metis_status_t metis_qk_norm_rope_bwd(const void *dq, int64_t lddq, const void *
  *  y:  tokens x W->m of type ydt, rounded once from fp32.
  *  ws: metis_fp4_gemv_workspace_bytes() bytes, 256-byte aligned; NULL is fine
  *      where that is 0 (bf16 x and k == 0).
- * Any number of tokens is taken, 64 at a time: W is read once for each 64, so
- * that beyond a few hundred tokens quantizing x for spectral_fp4_linear_fwd is
- * faster. Values below 2^-126 may be taken as 0. A NaN or an infinity in x
+ * Any number of tokens is taken, 64 at a time (21 where x is fp32), and W is
+ * read once for each of these, so that beyond a few hundred tokens quantizing x
+ * for spectral_fp4_linear_fwd is faster. Values below 2^-126 may be taken as 0. A NaN or an infinity in x
  * spoils its own token. Bitwise reproducible. */
 size_t metis_fp4_gemv_workspace_bytes(int64_t tokens, metis_dtype_t dt, const metis_split_t *W);
 metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_t tokens, int64_t ldx, const metis_split_t *W,
