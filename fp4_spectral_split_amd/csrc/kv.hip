@@ -6,7 +6,7 @@
 // takes two DPP steps or one. The rotation is formed in fp64 (its products are
 // exact there) and rounded once to fp32, so that the codes do not depend on how
 // the sum was formed. The least it can do is read k and v and write the codes,
-// 15 us for 8152 tokens of 8 heads of 128 from fp32 (76 MB); it takes 30 us,
+// 15 us for 8149 tokens of 8 heads of 128 from fp32 (76 MB); it takes 30 us,
 // 24 us where the caches hold k and v: 240 vector instructions for eight elements
 // (13 us of it), and waits, of which more loads under way (33 us), one head of 16
 // tokens to a workgroup (29 us) or an eight-way search for the sequence (30 us)
@@ -31,12 +31,13 @@
 // The codes' registers are filled again, with the next 32 tokens', as soon as
 // both products' operands are decoded; the loads take the time of the softmax and
 // of the second product, and the table entries of the 32 after them are under way.
-// 64 sequences of 64 to 8192 tokens (285 MB of MXFP4 codes, 8 heads of 128, 4 query
-// heads to each): 70 us, 4.1 TB/s; only reading such bytes takes 48.7 us. Vector
-// instructions, most of them the decoding, are 45% of the time. Two sets of code
-// registers (q then has to lie in LDS) took 72 us, rows of v in LDS that no
-// two of a transposed read's lanes meet a bank with 70 us, 32 query rows to a pass
-// (5 sequences of 26000 tokens with 6 new ones) 38.6 against 35.0 us.
+// 64 sequences of 64 to 8192 tokens (281 MB of MXFP4 codes, 8 heads of 128, 4 query
+// heads to each): 70 us, 4.0 TB/s; 128 sequences of 2048 tokens, which need no
+// join, 5.5 TB/s. Only reading such pages takes 49 us (5.8 TB/s), so what is lost
+// is the end, where workgroups of unequal work leave CUs idle, and the start of
+// each. Two sets of code registers (q then has to lie in LDS) took 72 us, rows of v
+// in LDS that no two of a transposed read's lanes meet a bank with 70 us, 32 query
+// rows to a pass (5 sequences of 26000 tokens with 6 new ones) 38.6 against 35.0 us.
 #include <algorithm>
 
 #include "decode4.hpp"
@@ -423,16 +424,19 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
       uint32_t k[2][NC], ks[2][kKeyScales];
       uint32_t v[kV][4], vs[kV];
     };
-    auto row_at = [&](const Place<HALVES> &p, int token) -> uint32_t {  // token of the step
-      if (HALVES) return (token < 16 ? p.row[0] : p.row[1]) + (token & 15);
-      return __shfl(p.row[0], token, 64);
+    // where token `token` of the step has its row, `each` bytes a row. (In halves
+    // the wave's part of the address and the lane's are kept apart: the wave's
+    // is worked out once, and the lane's is the same in every step.)
+    auto row_at = [&](const uint8_t *p, const Place<HALVES> &at, int half, int token, int each) -> const uint8_t * {
+      if (!HALVES) return p + (uint64_t)__shfl(at.row[0], token, 64) * each;
+      const uint64_t row = half == 0 ? at.row[0] : half == 1 ? at.row[1] : token < 16 ? at.row[0] : at.row[1];
+      return p + row * each + (token & 15) * each;
     };
     auto load = [&](const Place<HALVES> &p, Tile &t) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint64_t kr = row_at(p, 16 * s + r);
-        load_words<NC>(g.kc + kr * (D / 2) + gq * (D / 8), t.k[s]);
-        const uint8_t *q = g.ks + kr * (D / kBlock4<NV>);
+        load_words<NC>(row_at(g.kc, p, s, 16 * s + r, D / 2) + gq * (D / 8), t.k[s]);
+        const uint8_t *q = row_at(g.ks, p, s, 16 * s + r, D / kBlock4<NV>);
 #pragma unroll
         for (int i = 0; i < kKeyScales; ++i)
           t.ks[s][i] = q[kKeyScales == NC ? (gq * NC + i) / kPerScale
@@ -441,9 +445,9 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
 #pragma unroll
       for (int x = 0; x < kV; ++x) {
         const int piece = min(lane + 64 * x, kTile * NC - 1), token = piece / NC, c = piece - token * NC;
-        const uint64_t vr = row_at(p, token);
-        load_words<4>(g.vc + vr * (D / 2) + 16 * c, t.v[x]);
-        const uint8_t *q = g.vs + vr * (D / kBlock4<NV>);
+        const int half = NC % 4 == 0 ? x / (NC / 4 + (NC < 4)) : -1;  // of all lanes, -1: not the same
+        load_words<4>(row_at(g.vc, p, half, token, D / 2) + 16 * c, t.v[x]);
+        const uint8_t *q = row_at(g.vs, p, half, token, D / kBlock4<NV>);
         t.vs[x] = NV ? (uint32_t)q[2 * c] | (uint32_t)q[2 * c + 1] << 8 : q[c];
       }
     };
@@ -739,9 +743,15 @@ void batch_in(Operands &o, const metis_kv_batch_t *b) {
 }
 
 // Tokens of a workgroup: as many as leave `kTarget` workgroups, had every
-// sequence the largest length, in whole steps of its waves (64 sequences of 64 to
-// 8192 tokens: 1024 workgroups 84, 2048 74, 4096 70, 8192 78, 16384 120 us).
-constexpr int kTarget = 4096;
+// sequence the largest length, in whole steps of its waves. 1024 of them are on
+// the GPU at once, and best where lengths are equal; 1.5 times as many leave
+// about that where they are not. Microseconds, heads of 128, 32 query heads on 8:
+//   workgroups                          1024  1536  2048  4096
+//   64 sequences of 64 to 8192 tokens     86    70    75    74
+//   64 of 4096                          65.7  62.3  65.8  68.8
+//   16 of 16000                         63.2  66.9  63.5  70.5
+//   1 of 32768                          18.8  18.8  22.8  22.8
+constexpr int kTarget = 1536;
 struct Splits {
   int splits, chunk;
 };
