@@ -19,7 +19,7 @@
 // tokens 5.4, 11.0 and 16.4 us. (Only reading the 31 MB of 4096 -> 14336 takes
 // 7.0 us.) What is lost is the start: a workgroup's first codes are on their way
 // for 2 to 3 us of the time. Beyond 16 columns of the products x has its share:
-// each workgroup reads all of it from the L2 (64 tokens 4096 -> 14336 42 us).
+// each workgroup reads all of it from the L2 (64 tokens 4096 -> 14336 30.5 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -39,8 +39,9 @@ constexpr int kMaxRank = 96;
 constexpr int kMaxWaves = 16, kHeldWaves = 12;
 constexpr int kSlices = 8;      // workgroups that share the columns of z's sums
 // From here on a workgroup takes 32 rows, which halves the reads of x and still
-// leaves a workgroup for each CU (32 tokens, rows by 16 and by
-// 32: 4096 rows 7.7 and 9.7, 8192 11.1 and 10.8, 14336 21.7 and 18.6 us).
+// leaves a workgroup for each CU (32 tokens, rows by 16 and by 32: 4096 rows 7.7
+// and 9.7, 8192 11.1 and 10.8, 14336 21.7 and 18.6 us; 64 tokens, 8192 rows 19.4 and
+// 15.7, 14336 37.8 and 30.5 us).
 constexpr int kManyRows = 8192;
 
 struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` columns
@@ -61,6 +62,7 @@ struct MainArgs {
   // tokens x rank_pad, their factors S not yet in
   Weight u;
   float *z;
+  const unsigned short *z_parts;  // joined, times S, as three bf16 parts, each tokens x rank_pad
   const float *s;
   int rank;
   int tiles;  // sixteens of rows (held): workgroup b has tiles b, b + gridDim.x, ...
@@ -184,18 +186,16 @@ template <bool NV> __device__ __forceinline__ ushortx8 low_rows(const MainArgs &
   const intx4 v = {(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
   return __builtin_bit_cast(ushortx8, v);
 }
-// z[k0 .. k0 + 7] of the token whose first part is column c of the products, its
-// slices joined in order, as three bf16 parts. The columns of its other parts
-// get none.
-__device__ __forceinline__ void load_z(const MainArgs &g, int c, int k0, ushortx8 (&part)[3]) {
-  const int pad = rank_pad(g.rank), token = c / g.parts;
-  const bool there = token * g.parts == c && token < g.tokens;
-  const float *p = g.z + (int64_t)min(token, g.tokens - 1) * pad + k0;
+// z[k0 .. k0 + 7] S of a token, its slices joined in order, as three bf16 parts.
+__device__ __forceinline__ void joined_z(const float *z, const float *s, int rank, int tokens, int token, int k0,
+                                         ushortx8 (&part)[3]) {
+  const int pad = rank_pad(rank);
+  const float *p = z + (int64_t)token * pad + k0;
   floatx4 a[kSlices], b[kSlices];
 #pragma unroll
   for (int i = 0; i < kSlices; ++i) {
-    a[i] = *(const floatx4 *)(p + (int64_t)i * g.tokens * pad);
-    b[i] = *(const floatx4 *)(p + (int64_t)i * g.tokens * pad + 4);
+    a[i] = *(const floatx4 *)(p + (int64_t)i * tokens * pad);
+    b[i] = *(const floatx4 *)(p + (int64_t)i * tokens * pad + 4);
   }
 #pragma unroll
   for (int i = 1; i < kSlices; ++i) {
@@ -204,8 +204,38 @@ __device__ __forceinline__ void load_z(const MainArgs &g, int c, int k0, ushortx
   }
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = there ? (i < 4 ? a[0][i % 4] : b[0][i % 4]) * g.s[min(k0 + i, g.rank - 1)] : 0.0f;
+  for (int i = 0; i < 8; ++i) v[i] = (i < 4 ? a[0][i % 4] : b[0][i % 4]) * s[min(k0 + i, rank - 1)];
   parts_bf16<3>(v, part);
+}
+// For the token whose first part is column c of the products; the columns of its
+// other parts get none. JOINED: by join_z_kernel.
+template <bool JOINED> __device__ __forceinline__ void load_z(const MainArgs &g, int c, int k0, ushortx8 (&part)[3]) {
+  const int first = c / g.parts, token = min(first, g.tokens - 1);
+  if (JOINED) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      part[i] = *(const ushortx8 *)(g.z_parts + ((int64_t)i * g.tokens + token) * rank_pad(g.rank) + k0);
+  } else {
+    joined_z(g.z, g.s, g.rank, g.tokens, token, k0, part);
+  }
+  if (first * g.parts != c || first >= g.tokens) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) part[i] = ushortx8{0, 0, 0, 0, 0, 0, 0, 0};
+  }
+}
+
+// Beyond 32 columns of the products z is joined once: 64 tokens read eight slices
+// of it, at rank 64 a quarter of x itself, in each of the workgroups (4096 -> 14336
+// 68.4 us, so 52.8).
+__global__ void __launch_bounds__(256) join_z_kernel(const float *z, const float *s, int rank, int tokens,
+                                                     unsigned short *out) {
+  const int pad = rank_pad(rank), at = (blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= tokens * pad) return;
+  const int token = at / pad, k0 = at - token * pad;
+  ushortx8 part[3];
+  joined_z(z, s, rank, tokens, token, k0, part);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *(ushortx8 *)(out + ((int64_t)i * tokens + token) * pad + k0) = part[i];
 }
 
 // Row of x that a lane loads for the sixteen columns of the products from c0 on
@@ -307,7 +337,7 @@ __global__ void __launch_bounds__(64 * kHeldWaves) gemv_held_kernel(MainArgs g) 
     Low low, next;
     load_low<NV>(g, row_of(blockIdx.x), k0, low);
     ushortx8 z[3];
-    load_z(g, r, k0, z);
+    load_z<false>(g, r, k0, z);
     const float whole = NV ? *g.u.whole : 1.0f;
     int buf = 0;
     for (int tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
@@ -399,8 +429,11 @@ __device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, i
   }
 }
 
+// Waves of a workgroup that have `tiles` sixteens by sixteens of sums each: these take a kilobyte of LDS each.
+constexpr int waves_at_most(int tiles) { return tiles > 4 ? 64 / tiles : kMaxWaves; }
+
 template <bool NV, int NT, int RT, bool Z>
-__global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
+__global__ void __launch_bounds__(64 * waves_at_most(NT * RT)) gemv_kernel(MainArgs g) {
   extern __shared__ float sums[];  // waves x RT x 16 NT columns x 16 rows
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all_waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -422,7 +455,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) gemv_kernel(MainArgs g) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       ushortx8 z[3];
-      load_z(g, 16 * n + r, k0, z);
+      load_z<(NT > 2)>(g, 16 * n + r, k0, z);
       floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int p = 2; p >= 0; --p) v = mfma16_bf16(a, z[p], v);
@@ -461,7 +494,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const float *x, int64_t ldx,
 template <bool NV, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, int waves, hipStream_t stream) {
   const dim3 grid((unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows * RT), Z ? kSlices : 1);
   const int low = Z ? 0 : (int)cdiv(g.rank, 32) * RT;
-  waves = std::min(waves, std::min(kMaxWaves, 64 / (NT * RT)) - low) + low;  // of LDS: 1 KB for a sixteen by sixteen
+  waves = std::min(waves, waves_at_most(NT * RT) - low) + low;
   gemv_kernel<NV, NT, RT, Z><<<grid, 64 * waves, (size_t)waves * RT * NT * 1024, stream>>>(g);
 }
 
@@ -487,7 +520,9 @@ template <bool NV> void launch(MainArgs g, hipStream_t stream) {
     if (many) launch_rows<NV, 2, 2, false>(g, waves, stream);
     else launch_rows<NV, 2, 1, false>(g, waves, stream);
   } else {
-    launch_rows<NV, 4, 1, false>(g, waves, stream);
+    // (the rank's terms of 32 rows take two waves each 32 of them, of the eight that LDS has room for)
+    if (many && low <= 1) launch_rows<NV, 4, 2, false>(g, waves, stream);
+    else launch_rows<NV, 4, 1, false>(g, waves, stream);
   }
 }
 template <bool NV> void launch_z(const MainArgs &g, hipStream_t stream) {
@@ -509,7 +544,7 @@ int64_t pass_tokens(bool f32) { return f32 ? 21 : 64; }
 
 struct Plan {
   float *z;
-  unsigned short *x;
+  unsigned short *z_parts, *x;
   size_t bytes;
 };
 Plan plan_of(void *ws, int64_t tokens, bool f32, int64_t cols, int rank) {
@@ -517,6 +552,7 @@ Plan plan_of(void *ws, int64_t tokens, bool f32, int64_t cols, int rank) {
   Carver c(ws);
   Plan p = {};
   if (rank) p.z = c.take<float>((size_t)(kSlices * n * rank_pad(rank)));
+  if (rank && n * (f32 ? 3 : 1) > 32) p.z_parts = c.take<unsigned short>((size_t)(3 * n * rank_pad(rank)));
   if (f32) p.x = c.take<unsigned short>((size_t)(3 * n * cols));
   p.bytes = c.bytes();
   return p;
@@ -578,6 +614,10 @@ extern "C" metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_
       z.w = weight_of(W->Vt_q);
       z.z = p.z;
       nv ? launch_z<true>(z, stream) : launch_z<false>(z, stream);
+      if (g.columns() > 32)
+        join_z_kernel<<<(unsigned)cdiv((int64_t)g.tokens * rank_pad(k), 256 * 8), 256, 0, stream>>>(p.z, W->S, k, g.tokens,
+                                                                                                   p.z_parts);
+      g.z_parts = p.z_parts;
       g.u = weight_of(W->Ut_q);
       g.z = p.z;
       g.s = W->S;

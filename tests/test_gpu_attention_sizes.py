@@ -113,3 +113,23 @@ def test_append_of_many_tokens_and_of_a_few_at_a_time(fmt):
     torch.cuda.synchronize()
     for a, b in ((one.k, many.k), (one.v, many.v)):
         assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("shape", [(64, 8224, 4128, 0), (40, 8192, 96, 32), (33, 8224, 544, 64), (57, 4128, 1376, 96),
+                                   (85, 8224, 160, 7), (64, 14336, 512, 33)])
+def test_products_with_many_rows_and_columns(shape, fmt):
+    """More than 32 columns of the products, where 32 rows share a workgroup and
+    the low-rank term's inner sums are joined ahead; fp32 x has three columns a
+    token, and its last pass fewer."""
+    T, m, n, k = shape
+    rec = L._record(m, n, k, fmt, 185)
+    for dtype, odt in (("bf16", "bf16"), ("f32", "f32")):
+        x = H.to_dev(H.rng(186).standard_normal((T, n)) * np.exp(H.rng(187).standard_normal((T, 1))), H.T[dtype], 3, 1)
+        out = H.Guard(T, m, H.T[odt], pad=5, shift=1)
+        print("case many columns", shape, fmt, dtype, flush=True)
+        y = M.metis_fp4_gemv(x, rec, dtype=H.T[odt], out=out.t)
+        torch.cuda.synchronize()
+        assert out.intact() and y is out.t
+        L._check(y, x, rec, H.T[odt])
+        assert torch.equal(M.metis_fp4_gemv(x, rec, dtype=H.T[odt]), y)
