@@ -1198,7 +1198,7 @@ def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=No
     ldq, heads = _heads(q, "q", cache.head_dim)
     dev, tokens, dt = q.device, q.shape[0], _code(q.dtype)
     b = _batch(batch, dev)
-    if heads % cache.heads:
+    if cache.heads < 1 or heads % cache.heads:
         raise MetisError("%d query heads over %d heads in the cache" % (heads, cache.heads))
     dtype = q.dtype if dtype is None else dtype
     odt = _code(dtype)

@@ -133,3 +133,13 @@ def test_products_with_many_rows_and_columns(shape, fmt):
         assert out.intact() and y is out.t
         L._check(y, x, rec, H.T[odt])
         assert torch.equal(M.metis_fp4_gemv(x, rec, dtype=H.T[odt]), y)
+
+
+def test_a_cache_without_heads_is_refused():
+    q = torch.zeros(1, 64, device="cuda")
+    rows = [(torch.zeros(0, dtype=torch.uint8, device="cuda"),) * 2 + (None,) for _ in range(2)]
+    cache = M.KvCache.from_codes("mxfp4", 3, 16, 0, 64, *rows)
+    batch = A.batch(np.zeros((1, 3), np.int32), [1])
+    for call in (lambda: M.metis_kv_attention(q, batch, cache), lambda: M.metis_kv_append(q, q, batch, cache)):
+        with pytest.raises(M.MetisError):
+            call()
