@@ -33,7 +33,7 @@
 // of the second product, and the table entries of the 32 after them are under way.
 // 64 sequences of 64 to 8192 tokens (281 MB of MXFP4 codes, 8 heads of 128, 4 query
 // heads to each): 70 us, 4.0 TB/s; 128 sequences of 2048 tokens, which need no
-// join, 5.5 TB/s. Only reading such pages takes 49 us (5.8 TB/s), so what is lost
+// join, 4.5 to 5.5 TB/s. Only reading such pages takes 49 us (5.8 TB/s), so what is lost
 // is the end, where workgroups of unequal work leave CUs idle, and the start of
 // each. Two sets of code registers (q then has to lie in LDS) took 72 us, rows of v
 // in LDS that no two of a transposed read's lanes meet a bank with 70 us, 32 query
@@ -751,13 +751,18 @@ void batch_in(Operands &o, const metis_kv_batch_t *b) {
 //   64 of 4096                          65.7  62.3  65.8  68.8
 //   16 of 16000                         63.2  66.9  63.5  70.5
 //   1 of 32768                          18.8  18.8  22.8  22.8
-constexpr int kTarget = 1536;
+// Where the heads of all sequences fill the GPU unsplit, up to 4096 tokens, they
+// stay so and need no join (128 of 2048 tokens 62 us, in two 77; 160 of 64 to 2048
+// 45.7 and 55.9; 128 of 64 to 4096 67 and 73). Longer ones, which may be more
+// unequal, are divided (128 of 64 to 8192 136 us, in two 130).
+constexpr int kTarget = 1536, kResident = 1024, kUnsplitSteps = 32;
 struct Splits {
   int splits, chunk;
 };
 Splits splits_of(int64_t work_rows, int64_t max_length) {
   const int64_t steps = std::max<int64_t>(1, cdiv(max_length, kStepTokens));
   int64_t per = cdiv(steps * work_rows, kTarget);          // steps of a workgroup
+  if (work_rows >= kResident && steps <= kUnsplitSteps) per = steps;
   per = std::max(per, cdiv(steps, kMaxSplits));
   per = std::max<int64_t>(1, std::min(per, steps));
   return {(int)cdiv(steps, per), (int)(per * kStepTokens)};

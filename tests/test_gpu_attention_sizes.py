@@ -10,6 +10,7 @@ import torch
 from tests import _attn as A
 from tests import _ffn as H
 from tests import test_gpu_gemv as L
+from tests import test_gpu_kv as V
 from tests import test_gpu_qk_rope as R
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +144,12 @@ def test_a_cache_without_heads_is_refused():
     for call in (lambda: M.metis_kv_attention(q, batch, cache), lambda: M.metis_kv_append(q, q, batch, cache)):
         with pytest.raises(M.MetisError):
             call()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("page,longest", [(16, 700), (12, 700), (64, 5000)])
+def test_attention_of_sequences_that_fill_the_gpu(page, longest, fmt):
+    """64 sequences of 16 heads of unequal lengths, one of them as long as the
+    hint says: unsplit up to 4096 tokens, divided beyond."""
+    lengths = [longest if i == 5 else (i * 37) % 300 for i in range(64)]
+    V.test_attention((16, 32, 32, page, None, lengths, 0), fmt, "bf16", "bf16")
