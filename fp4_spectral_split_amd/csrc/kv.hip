@@ -263,6 +263,11 @@ constexpr int kTile = 32;  // tokens of a wave's step
 constexpr int kStepTokens = kWaves * kTile;
 constexpr int kRowsQ = 16;
 constexpr int kMaxSplits = 256;  // a thread of the join for each
+// bf16 parts of a weight of the softmax: all 24 bits. Two parts hold 16 (2^-17), of
+// which a result that is small beside sum p |v| shows up to its leading bits; the
+// third takes 3 to 7% of the time (64 sequences of 64 to 8192 tokens 73.7 to 77.3 us,
+// 128 of 2048 54.5 to 57.3).
+constexpr int kWeightParts = 3;
 
 struct AttendArgs {
   const void *q;
@@ -332,8 +337,8 @@ template <bool HALVES> struct Place {
   bool bad[2];      // a page outside the cache
 };
 
-// NC: head size / 32. PQ, PP: bf16 parts of q and of the weights.
-template <bool NV, int NC, int PQ, int PP, typename TQ, bool HALVES>
+// NC: head size / 32. PQ: bf16 parts of q.
+template <bool NV, int NC, int PQ, typename TQ, bool HALVES>
 __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) attend_kernel(AttendArgs g) {
   constexpr int D = 32 * NC;
   constexpr int kPerScale = NV ? 2 : 4;  // units of eight elements under one scale
@@ -544,8 +549,8 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
         p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
         sum += p[i];
       }
-      ushortx8 pf[PP];
-      parts_bf16<PP>(p, pf);
+      ushortx8 pf[kWeightParts];
+      parts_bf16<kWeightParts>(p, pf);
       // the wave's own LDS rows: its writes are done before its reads
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
           a[4 + e] = (unsigned short)a1[e];
         }
 #pragma unroll
-        for (int part = PP - 1; part >= 0; --part) o[i] = mfma16_bf16(a, pf[part], o[i]);
+        for (int part = kWeightParts - 1; part >= 0; --part) o[i] = mfma16_bf16(a, pf[part], o[i]);
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -791,20 +796,20 @@ AttendPlan plan_of(void *ws, int64_t tokens, int32_t heads, int32_t max_new, int
   return p;
 }
 
-template <bool NV, int PQ, int PP, typename TQ, bool HALVES>
+template <bool NV, int PQ, typename TQ, bool HALVES>
 void attend_by_dim(const AttendArgs &g, int dim, unsigned grid, hipStream_t stream) {
 #define METIS_CASE(NC)                                                                             \
-  case NC: attend_kernel<NV, NC, PQ, PP, TQ, HALVES><<<grid, 64 * kWaves, 0, stream>>>(g); break;
+  case NC: attend_kernel<NV, NC, PQ, TQ, HALVES><<<grid, 64 * kWaves, 0, stream>>>(g); break;
   switch (dim / 32) {
     METIS_CASE(1) METIS_CASE(2) METIS_CASE(3) METIS_CASE(4) METIS_CASE(5) METIS_CASE(6) METIS_CASE(7) METIS_CASE(8)
   }
 #undef METIS_CASE
 }
-template <int PQ, int PP, typename TQ> void attend(const AttendArgs &g, bool nv, int dim, unsigned grid, hipStream_t stream) {
+template <int PQ, typename TQ> void attend(const AttendArgs &g, bool nv, int dim, unsigned grid, hipStream_t stream) {
   if (g.p.page_size % 16 == 0) {
-    nv ? attend_by_dim<true, PQ, PP, TQ, true>(g, dim, grid, stream) : attend_by_dim<false, PQ, PP, TQ, true>(g, dim, grid, stream);
+    nv ? attend_by_dim<true, PQ, TQ, true>(g, dim, grid, stream) : attend_by_dim<false, PQ, TQ, true>(g, dim, grid, stream);
   } else {
-    nv ? attend_by_dim<true, PQ, PP, TQ, false>(g, dim, grid, stream) : attend_by_dim<false, PQ, PP, TQ, false>(g, dim, grid, stream);
+    nv ? attend_by_dim<true, PQ, TQ, false>(g, dim, grid, stream) : attend_by_dim<false, PQ, TQ, false>(g, dim, grid, stream);
   }
 }
 
@@ -953,12 +958,9 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
   g.stat = p.stat;
   const unsigned grid = (unsigned)((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits);
   const int dim = (int)cache->k.cols;
-  // Parts of q and of the weights: q is bf16 and exact, or fp32 in three parts.
-  // A weight of one part would be off by 2^-9, as much as all of a bf16 result
-  // may be; two parts (2^-17) leave the result's own rounding, three fp32's.
-  if (dt == METIS_F32) attend<3, 3, float>(g, nv, dim, grid, stream);
-  else if (odt == METIS_F32) attend<1, 3, unsigned short>(g, nv, dim, grid, stream);
-  else attend<1, 2, unsigned short>(g, nv, dim, grid, stream);
+  // q is bf16 and exact, or fp32 in three parts
+  if (dt == METIS_F32) attend<3, float>(g, nv, dim, grid, stream);
+  else attend<1, unsigned short>(g, nv, dim, grid, stream);
   if (p.s.splits > 1) {
     JoinArgs jn = {};
     jn.b = g.b;

@@ -588,8 +588,8 @@ metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_
  *          best speed). The lengths themselves stay on the device.
  *  ws:     metis_kv_attention_workspace_bytes() bytes, 256-byte aligned.
  * Queries and keys enter the products as they are (fp32 queries as three bf16
- * parts), the weights exp(score - max) as two bf16 parts, three where q or o is
- * fp32; scores, sums and o in fp32. Bitwise reproducible. A NaN or an infinity
+ * parts), the weights exp(score - max) as three bf16 parts, all of their bits;
+ * scores, sums and o in fp32. Bitwise reproducible. A NaN or an infinity
  * in q spoils its own row; one in the cache every new token's of its sequence
  * and head, in the rows that the kernel works on with it. */
 size_t metis_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,

@@ -1,0 +1,61 @@
+"""Attention over the paged FP4 cache where its result is small beside the values
+it joins, against the fp64 oracle (oracle/attention.py)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as O
+from tests import _attn as A
+from tests import _ffn as H
+
+pytestmark = pytest.mark.gpu
+
+import fp4_spectral_split_amd as M
+
+U = H.U32
+
+
+def _cache_of(fmt, keys, values, page, heads=1):
+    """A cache of pages x page places of `heads` heads holding given rows, and the
+    oracle's view of it."""
+    rows, dim = keys.shape
+    pages = rows // (page * heads)
+    parts = []
+    for x in (keys, values):
+        whole = None if fmt == "mxfp4" else float(np.float32(8.0 / 2688))
+        parts.append(O.quantize_rows(x, fmt, whole) + (whole,))
+    t = M.KvCache.from_codes(fmt, pages, page, heads, dim, *[
+        (A.dev(c), A.dev(s), None if w is None else torch.tensor([w], device="cuda")) for c, s, w in parts])
+    return t, {"fmt": fmt, "pages": pages, "page_size": page, "heads": heads, "dim": dim, "k": parts[0], "v": parts[1]}
+
+
+@pytest.mark.parametrize("dtype,odt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("page", [16, 3])
+def test_values_that_nearly_cancel(page, fmt, dtype, odt):
+    """Two tokens with opposite values and nearly equal scores: o = v (1 - p) / (1 + p)
+    with p = 1 - d, d below 4e-4. u = 2^-24: a score is one exact product, its
+    scaling's roundings are u of a difference below 4e-4, so p is off by the
+    exponential's 2 u and the rest of one u; all bits of p enter the product,
+    where only two terms differ from zero, three steps of at most 2 u of the
+    magnitudes; the sum of the weights, its reciprocal and a tensor's scale add 3 u:
+    12 u of |v|, held to 16. (Weights cut to 16 bits would leave 2^-18 = 64 u.)"""
+    D, heads, T = 64, 32, 8
+    g = H.rng(201)
+    keys = np.zeros((2 * page, D))
+    keys[0, 0], keys[1, 0] = 1.0, -1.0
+    values = H.rng(202).choice([-1.0, 1.0], (2 * page, D)) * g.choice([0.5, 1.0, 1.5, 2.0, 3.0], (2 * page, D))
+    values[1] = -values[0]
+    cache, view = _cache_of(fmt, keys, values, page)
+    x = np.zeros((T, heads, D))
+    x[..., 0] = D ** 0.5 * np.exp(g.uniform(np.log(1e-5), np.log(2e-4), (T, heads))) * g.choice([-1, 1], (T, heads))
+    x[..., 1:] = g.standard_normal((T, heads, D - 1))  # meets zeros of the keys
+    q = H.to_dev(x.reshape(T, -1), H.T[dtype])
+    table, lengths = np.zeros((T, 1), np.int32), [2] * T
+    print("case cancel", page, fmt, dtype, odt, flush=True)
+    o, lse = M.metis_kv_attention(q, A.batch(table, lengths), cache, dtype=H.T[odt], need_lse=True)
+    torch.cuda.synchronize()
+    want, wl, spread, _ = O.attention(H.np64(q), heads, view, table, np.asarray(lengths), None, D ** -0.5, 0)
+    assert np.abs(want).max() < 4e-4 * spread.max()
+    A.close(H.np64(o).reshape(want.shape), want, 16 * U * spread + H.HALF[H.T[odt]] * 1.01 * np.abs(want), "o")
+    A.close(H.np64(lse), wl, 16 * U + 4 * U * np.abs(wl), "lse")
