@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
       v += *(const floatx4 *)((const float *)(lds + w * kVBytes) + rr * kOStride + d) * (mw[w] == -INFINITY ? 1.0f : by);
     }
     const int64_t orow = start + j2;
-    // a length that the table does not hold
-    if (beyond && length - new_tokens + j2 + 1 > 0) l = nan_f32();
+    // it sees tokens, but their number is beyond the table, or all their scores are -inf
+    if (length - new_tokens + j2 >= 0 && (beyond || (g.splits == 1 && l == 0.0f))) l = nan_f32();
     if (g.splits > 1) {
       const int64_t slot = ((int64_t)split * g.tokens + orow) * g.heads + h2;
       *(floatx4 *)(g.part + slot * D + d) = v;
@@ -685,6 +685,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs g) {
   l = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 64; ++w) l += wave_stat[w].y;
+  if (l == 0.0f && g.b.lengths[seq] >= stop - row) l = nan_f32();  // it sees tokens, but all their scores are -inf
   const int cols = g.dim / 4, groups = kJoinThreads / cols, grp = t / cols, d = (t - grp * cols) * 4;
   floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (grp < groups) {

@@ -589,9 +589,10 @@ metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_
  *  ws:     metis_kv_attention_workspace_bytes() bytes, 256-byte aligned.
  * Queries and keys enter the products as they are (fp32 queries as three bf16
  * parts), the weights exp(score - max) as three bf16 parts, all of their bits;
- * scores, sums and o in fp32. Bitwise reproducible. A NaN or an infinity
- * in q spoils its own row; one in the cache every new token's of its sequence
- * and head, in the rows that the kernel works on with it. */
+ * scores, sums and o in fp32. Bitwise reproducible. A NaN or an infinity in q
+ * makes its own row's o and lse NaN, as do scores that are all -inf by overflow;
+ * one in the cache spoils every new token's of its sequence and head, in the rows
+ * that the kernel works on with it. */
 size_t metis_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t max_new, int64_t max_length,
                                           const metis_kv_batch_t *batch, const metis_kv_cache_t *cache);
 metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, int64_t tokens, int64_t ldq, int32_t heads,

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import attention as O
+from oracle import formats as F
 from tests import _attn as A
 from tests import _ffn as H
 
@@ -23,7 +24,7 @@ def _cache_of(fmt, keys, values, page, heads=1):
     parts = []
     for x in (keys, values):
         whole = None if fmt == "mxfp4" else float(np.float32(8.0 / 2688))
-        parts.append(O.quantize_rows(x, fmt, whole) + (whole,))
+        parts.append(O.quantize_rows(F.f32(x), fmt, whole) + (whole,))
     t = M.KvCache.from_codes(fmt, pages, page, heads, dim, *[
         (A.dev(c), A.dev(s), None if w is None else torch.tensor([w], device="cuda")) for c, s, w in parts])
     return t, {"fmt": fmt, "pages": pages, "page_size": page, "heads": heads, "dim": dim, "k": parts[0], "v": parts[1]}
@@ -59,3 +60,35 @@ def test_values_that_nearly_cancel(page, fmt, dtype, odt):
     assert np.abs(want).max() < 4e-4 * spread.max()
     A.close(H.np64(o).reshape(want.shape), want, 16 * U * spread + H.HALF[H.T[odt]] * 1.01 * np.abs(want), "o")
     A.close(H.np64(lse), wl, 16 * U + 4 * U * np.abs(wl), "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("hint", [1 << 16, 1])
+def test_nan_and_infinity_in_q_stay_in_their_row(hint, fmt, dtype):
+    """A NaN or an infinity of either sign in one head of a query: that head's o and
+    lse are NaN, also where all of its scores are -inf, and for a sequence of a
+    single token or one whose finite query overflows; every other row keeps its bits."""
+    D, heads, page = 64, 4, 16
+    g = H.rng(211)
+    lengths = [1, 3, 40, 700, 700]
+    keys, values = g.standard_normal((96 * page, D)), g.standard_normal((96 * page, D))
+    keys[:, :2] = 2.0 + np.abs(keys[:, :2])  # of one sign
+    cache, _ = _cache_of(fmt, keys, values, page)
+    table, _ = A.table_for(g, lengths, page)
+    b = A.batch(table, lengths, max_length=hint)
+    x = g.standard_normal((len(lengths), heads, D))
+    call = lambda a: M.metis_kv_attention(H.to_dev(a.reshape(len(lengths), -1), H.T[dtype]), b, cache, need_lse=True)  # noqa: E731
+    want, wl = call(x)
+    for bad in (np.nan, np.inf, -np.inf, -3e38):
+        for row in range(len(lengths)):
+            y, head = x.copy(), row % heads
+            y[row, head, :2] = bad
+            print("case q", hint, fmt, dtype, bad, row, flush=True)
+            o, lse = call(y)
+            torch.cuda.synchronize()
+            o, lse = o.view(len(lengths), heads, D), lse.view(len(lengths), heads)
+            spoiled = torch.zeros(len(lengths), heads, dtype=torch.bool, device="cuda")
+            spoiled[row, head] = True
+            assert bool(torch.isnan(o[spoiled]).all()) and bool(torch.isnan(lse[spoiled]).all()), (bad, row)
+            assert torch.equal(o[~spoiled], want.view(o.shape)[~spoiled]) and torch.equal(lse[~spoiled], wl.view(lse.shape)[~spoiled])
