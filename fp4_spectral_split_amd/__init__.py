@@ -1122,8 +1122,8 @@ class KvBatch:
     """Sequences and their new tokens (see metis_kv_batch_t). table: int32,
     sequences x pages, each sequence's pages in order. lengths: int32, tokens
     of each sequence with its new ones (0: not in use). starts: int32, one more
-    than sequences: sequence s has the rows starts[s] .. starts[s + 1] - 1;
-    None: row s belongs to sequence s. max_new: at least the most new tokens of
+    than sequences, not decreasing: sequence s has the rows starts[s] ..
+    starts[s + 1] - 1; None: row s belongs to sequence s. max_new: at least the most new tokens of
     any sequence. max_length: about the largest length (default: what the table
     holds), which attention divides its work by."""
     table: torch.Tensor

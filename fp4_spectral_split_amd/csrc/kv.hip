@@ -91,6 +91,10 @@ __device__ __forceinline__ int sequence_of(const Batch &b, int64_t t) {
   return lo < b.seqs && b.starts[lo] <= t ? lo : -1;
 }
 
+// Whether row t, which sequence s claims, is its own: where starts decrease,
+// several claim a row, and one has it in every call.
+__device__ __forceinline__ bool belongs(const Batch &b, int64_t t, int s) { return !b.starts || sequence_of(b, t) == s; }
+
 template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
   Raw<T> r;
   load_all(p, r);
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
   constexpr int kOStride = D + 4;
   static_assert(kRowsQ * kOStride * 4 + kRowsQ * 8 <= kVBytes, "the join fits where v was");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kVBytes];
+  __shared__ int ours[kRowsQ];  // whether a query row belongs to this sequence
 
   const int lane = threadIdx.x & 63, r = lane & 15, gq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -391,11 +396,13 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
   const int chunk = max(g.chunk, (each + kStepTokens - 1) / kStepTokens * kStepTokens);
   const int64_t from64 = lo + split * (int64_t)chunk;
   if (g.splits > 1 && from64 >= hi) {  // nothing here; the join skips (-inf, 0)
-    if (threadIdx.x < kRowsQ && row_there)
+    if (threadIdx.x < kRowsQ && row_there && belongs(g.b, row, seq))
       g.stat[((int64_t)split * g.tokens + row) * g.heads + h] = make_float2(-INFINITY, beyond && end_row > 0 ? nan_f32() : 0.0f);
     return;
   }
   const int from = (int)from64, to = min(hi, (int)min((int64_t)INT32_MAX, from64 + chunk));
+  // the last wave looks it up: it has the fewest steps
+  if (wave == kWaves - 1 && lane < kRowsQ) ours[lane] = row_there && belongs(g.b, row, seq);
 
   floatx4 o[2 * NC];
 #pragma unroll
@@ -590,7 +597,7 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
     const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
     const int at2 = tile * kRowsQ + rr;
     const int j2 = (int)g.by_group.div((uint32_t)at2), h2 = kvh * g.group + at2 - j2 * g.group;
-    if (j2 >= count) continue;
+    if (!ours[rr]) continue;
     float m = -INFINITY, l = 0.0f;
     floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     float mw[kWaves];

@@ -543,6 +543,9 @@ typedef struct {
  *  starts:  int32[seqs + 1]: the new tokens of sequence s are the rows
  *           starts[s] .. starts[s + 1] - 1, its last ones in order; NULL: one
  *           new token each, row s of sequence s. Rows outside belong to none.
+ *           starts should not decrease. Where they do, a row that several
+ *           sequences claim is one and the same sequence's in all calls, or
+ *           none's: the s that a bisection finds for starts[s + 1] > row.
  * A new token i of n of a sequence of length L is at position L - n + i;
  * negative positions are no tokens. A sequence whose rows reach outside the
  * call's tokens is left out. max_pages * page_size <= 2^28. */

@@ -92,3 +92,49 @@ def test_nan_and_infinity_in_q_stay_in_their_row(hint, fmt, dtype):
             spoiled[row, head] = True
             assert bool(torch.isnan(o[spoiled]).all()) and bool(torch.isnan(lse[spoiled]).all()), (bad, row)
             assert torch.equal(o[~spoiled], want.view(o.shape)[~spoiled]) and torch.equal(lse[~spoiled], wl.view(lse.shape)[~spoiled])
+
+
+def _owner(starts, row):
+    """The sequence that a bisection for starts[s + 1] > row finds, -1 if none."""
+    lo, hi = 0, len(starts) - 1
+    while lo < hi:
+        mid = (lo + hi) // 2
+        if starts[mid + 1] > row:
+            hi = mid
+        else:
+            lo = mid + 1
+    return lo if lo < len(starts) - 1 and starts[lo] <= row else -1
+
+
+@pytest.mark.parametrize("hint", [1, 1 << 20])
+def test_rows_that_several_sequences_claim(hint):
+    """Decreasing starts: each row is worked on for one sequence, the one whose
+    place in the cache the append stores it at, whichever finishes last; rows of
+    none are left alone, and a second call gives the same bits."""
+    D, heads, page, T = 32, 4, 16, 24
+    g = H.rng(221)
+    S, width = 6, 130
+    cache, _ = _cache_of("mxfp4", g.standard_normal((S * width * page, D)), g.standard_normal((S * width * page, D)), page)
+    table = g.permutation(S * width).astype(np.int32).reshape(S, width)
+    q = A.dev(g.standard_normal((T, heads * D)), torch.float32)
+    for trial in range(8):
+        starts = [0, 3, 2, 4, 4, 9, 24] if trial == 0 else sorted(g.integers(0, T + 1, S + 1).tolist(), reverse=trial == 1)
+        if trial > 1:
+            g.shuffle(starts)
+        lengths = [2000 if s % 2 == trial % 2 else 30 for s in range(S)]  # unequal work
+        b = A.batch(table, lengths, starts, T, hint)
+        print("case claims", hint, starts, flush=True)
+        outs = []
+        for _ in range(2):
+            out, lse = torch.full((T, heads * D), 5.0, device="cuda"), None
+            _, lse = M.metis_kv_attention(q, b, cache, out=out, need_lse=True)
+            outs.append((out, lse))
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        for row in range(T):
+            s = _owner(starts, row)
+            if s < 0 or not starts[s] <= row < starts[s + 1]:
+                assert bool((outs[0][0][row] == 5.0).all()), (starts, row)
+                continue
+            one, l1 = M.metis_kv_attention(q[row:row + 1], A.batch(table[s:s + 1], [lengths[s] - (starts[s + 1] - row) + 1]), cache, need_lse=True)
+            assert torch.allclose(outs[0][0][row], one[0], rtol=1e-4, atol=1e-5) and torch.allclose(outs[0][1][row], l1[0], atol=1e-4), (starts, row)
