@@ -284,6 +284,7 @@ struct AttendArgs {
   int heads, group;  // query heads, and of them for each head of the cache
   FastDiv by_group;
   int tiles, splits, chunk;  // chunk: least tokens of a workgroup, a multiple of kStepTokens
+  int by_rows;               // workgroups are numbered by the call's rows, see number_of
   int max_new;
   float scale;               // times log2(e)
   int64_t window;
@@ -365,13 +366,28 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
   uint32_t id = blockIdx.x;
   const int kvh = id % g.p.heads;
   id /= g.p.heads;
-  const int seq = id % g.b.seqs;
-  id /= g.b.seqs;
-  const int tile = id % g.tiles, split = id / g.tiles;
-
+  int seq, tile, split = 0, lead = 0;
+  if (!g.by_rows) {
+    seq = id % g.b.seqs;
+    id /= g.b.seqs;
+    tile = id % g.tiles;
+    split = id / g.tiles;
+  } else {
+    lead = id % (uint32_t)g.tokens;
+    tile = id / (uint32_t)g.tokens;
+    seq = __builtin_amdgcn_readfirstlane(sequence_of(g.b, lead));
+    if (seq < 0) return;
+  }
   const int start = __builtin_amdgcn_readfirstlane(g.b.starts ? g.b.starts[seq] : seq);
   const int stop = __builtin_amdgcn_readfirstlane(g.b.starts ? g.b.starts[seq + 1] : seq + 1);
   if (start < 0 || stop > g.tokens || start >= stop) return;
+  if (g.by_rows) {  // the tile-th of those with query rows of this token, if no token before it has the tile
+    const int own = lead - start;
+    tile += own * g.group / kRowsQ;
+    if (tile * kRowsQ >= (own + 1) * g.group) return;
+    for (int k = (int)g.by_group.div((uint32_t)(tile * kRowsQ)); k < own; ++k)
+      if (belongs(g.b, start + k, seq)) return;
+  }
   const int new_tokens = stop - start, count = min(new_tokens, g.max_new);
   if (tile * kRowsQ >= count * (int64_t)g.group) return;
   const int length = max(__builtin_amdgcn_readfirstlane(g.b.lengths[seq]), 0);
@@ -774,11 +790,28 @@ struct Splits {
 };
 Splits splits_of(int64_t work_rows, int64_t max_length) {
   const int64_t steps = std::max<int64_t>(1, cdiv(max_length, kStepTokens));
-  int64_t per = cdiv(steps * work_rows, kTarget);          // steps of a workgroup
+  int64_t per = work_rows < kTarget ? cdiv(steps * work_rows, kTarget) : steps;  // steps of a workgroup
   if (work_rows >= kResident && steps <= kUnsplitSteps) per = steps;
   per = std::max(per, cdiv(steps, kMaxSplits));
   per = std::max<int64_t>(1, std::min(per, steps));
   return {(int)cdiv(steps, per), (int)(per * kStepTokens)};
+}
+
+// Workgroups of the attention. Each sequence has as many as the most new tokens
+// take, one after the other in memory (see attend_kernel), unless that is more
+// than a launch numbers: a prompt among thousands of sequences, or a batch with
+// room for millions. Then each row of the call has one for every tile that it is
+// in, which the tile's first row goes on with; those are never more than the
+// query rows. The lengths are not divided there (work_rows above kTarget).
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of 256 threads
+struct Number {
+  int64_t groups;
+  bool by_rows;
+};
+Number number_of(int64_t tokens, int32_t group, int64_t seqs, int64_t heads, int tiles, int splits) {
+  const int64_t groups = seqs * heads * tiles;
+  if (groups * splits < kMaxGroups) return {groups * splits, false};
+  return {heads * tokens * ((group + 14) / kRowsQ + 1), true};
 }
 
 struct AttendPlan {
@@ -926,7 +959,6 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
   const AttendPlan p = plan_of(ws, tokens, heads, max_new, max_length, batch, cache);
   if (p.bytes && (!ws || ws_bytes < p.bytes)) return METIS_ERR_WORKSPACE;
   if (p.bytes && ((uintptr_t)ws & 255)) return METIS_ERR_INVALID;
-  if ((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits >= (int64_t)1 << 24) return METIS_ERR_UNSUPPORTED;
   Operands all;
   all.out(o, tokens, n, ldo, elem_bytes(odt));
   all.out(lse, 1, tokens * heads, 0, 4);
@@ -964,7 +996,9 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
   g.lse = lse;
   g.part = p.part;
   g.stat = p.stat;
-  const unsigned grid = (unsigned)((int64_t)batch->seqs * cache->heads * p.tiles * p.s.splits);
+  const Number number = number_of(tokens, g.group, batch->seqs, cache->heads, p.tiles, p.s.splits);
+  g.by_rows = number.by_rows;
+  const unsigned grid = (unsigned)number.groups;
   const int dim = (int)cache->k.cols;
   // q is bf16 and exact, or fp32 in three parts
   if (dt == METIS_F32) attend<3, float>(g, nv, dim, grid, stream);

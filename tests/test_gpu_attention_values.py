@@ -138,3 +138,80 @@ def test_rows_that_several_sequences_claim(hint):
                 continue
             one, l1 = M.metis_kv_attention(q[row:row + 1], A.batch(table[s:s + 1], [lengths[s] - (starts[s + 1] - row) + 1]), cache, need_lse=True)
             assert torch.allclose(outs[0][0][row], one[0], rtol=1e-4, atol=1e-5) and torch.allclose(outs[0][1][row], l1[0], atol=1e-4), (starts, row)
+
+
+def _many(seqs, used, counts, lengths, g):
+    """A batch of `seqs` sequences, of which `used` have new tokens."""
+    starts = np.zeros(seqs + 1, np.int64)
+    for s, n in zip(used, counts):
+        starts[s + 1:] += n
+    every = np.zeros(seqs, np.int32)
+    every[used] = lengths
+    return starts, every
+
+
+@pytest.mark.parametrize("kvh,heads,dim,page", [(8, 8, 32, 160), (2, 10, 64, 40), (1, 20, 32, 160)])
+def test_a_prompt_among_very_many_sequences(kvh, heads, dim, page):
+    """More sequences times heads times tiles of the longest prompt than a launch
+    has workgroups for: what the used sequences alone get, and with decreasing
+    starts what the owner of each row gives it."""
+    g = H.rng(231)
+    counts, lengths = [128, 1, 20, 7], [150, 33, 20, 160]
+    group = heads // kvh
+    tiles = -(-128 * group // 16)
+    seqs = -(-(1 << 24) // (kvh * tiles)) + 3
+    used = [2, 3, seqs // 2, seqs - 1]
+    starts, every = _many(seqs, used, counts, lengths, g)
+    width = -(-160 // page)
+    cache, _ = _cache_of("mxfp4", g.standard_normal((4 * width * page * kvh, dim)), g.standard_normal((4 * width * page * kvh, dim)), page, kvh)
+    few = g.permutation(4 * width).astype(np.int32).reshape(4, width)
+    table = np.full((seqs, width), -1, np.int32)
+    table[used] = few
+    T = sum(counts) + 1
+    q = A.dev(g.standard_normal((T, heads * dim)), torch.bfloat16)
+    small = np.concatenate([[0], np.cumsum(counts)])
+    print("case many", kvh, heads, dim, seqs, flush=True)
+    for max_new in (128, 50):
+        outs = []
+        for b in (A.batch(few, lengths, small, max_new, 1 << 20), A.batch(table, every, starts, max_new, 1)):
+            out = torch.full((T, heads * dim), 5.0, device="cuda", dtype=torch.bfloat16)
+            outs.append((out, M.metis_kv_attention(q, b, cache, out=out, need_lse=True)[1]))
+        torch.cuda.synchronize()
+        tol = dict(rtol=2.0 ** -7, atol=2.0 ** -9)  # the few may be split
+        assert torch.allclose(outs[0][0].float(), outs[1][0].float(), **tol) and torch.allclose(outs[0][1], outs[1][1], atol=1e-4)
+        assert bool((outs[1][0][-1] == 5.0).all())
+    mid = seqs // 2  # a sequence that claims rows of others, and one that reaches back
+    starts[mid - 7], starts[mid + 9], starts[seqs // 4] = 140, 30, 77
+    every[mid - 8], every[mid + 9], every[seqs // 4], every[seqs // 4 - 1] = 140, 160, 155, 99
+    table[[mid - 8, mid + 9, seqs // 4, seqs // 4 - 1]] = few
+    out = torch.full((T, heads * dim), 5.0, device="cuda", dtype=torch.bfloat16)
+    M.metis_kv_attention(q, A.batch(table, every, starts, 128, 1), cache, out=out)
+    claimed = set()
+    for row in range(T):
+        s = _owner(starts, row)
+        position = int(every[s] - (starts[s + 1] - row)) if s >= 0 else -1
+        if s < 0 or row - starts[s] >= 128:
+            assert bool((out[row] == 5.0).all()), row
+        elif position < 0:
+            assert not out[row].any(), row
+        else:
+            claimed.add(s)
+            one, _ = M.metis_kv_attention(q[row:row + 1], A.batch(table[s:s + 1], [position + 1]), cache)
+            assert torch.allclose(out[row].float(), one[0].float(), **tol), row
+    assert len(claimed) > 1
+
+
+def test_room_for_millions_of_sequences():
+    """A batch of one new token each whose table has 2^21 + 1 sequences for three
+    tokens: the same as a batch of three."""
+    kvh, dim, page, seqs = 8, 32, 16, (1 << 21) + 1
+    g = H.rng(241)
+    cache, _ = _cache_of("nvfp4", g.standard_normal((3 * page * kvh, dim)), g.standard_normal((3 * page * kvh, dim)), page, kvh)
+    q = A.dev(g.standard_normal((3, kvh * dim)), torch.float32)
+    table, lengths = np.full((seqs, 1), -1, np.int32), np.zeros(seqs, np.int32)
+    table[:3, 0], lengths[:3] = [2, 0, 1], [16, 3, 9]
+    print("case room", flush=True)
+    got = M.metis_kv_attention(q, A.batch(table, lengths), cache, need_lse=True)
+    want = M.metis_kv_attention(q, A.batch(table[:3], lengths[:3]), cache, need_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
