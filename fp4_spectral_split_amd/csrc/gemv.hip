@@ -429,11 +429,14 @@ __device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, i
   }
 }
 
-// Waves of a workgroup that have `tiles` sixteens by sixteens of sums each: these take a kilobyte of LDS each.
-constexpr int waves_at_most(int tiles) { return tiles > 4 ? 64 / tiles : kMaxWaves; }
+// Waves of a workgroup at most: the sums of each take NT RT kilobytes of LDS, and
+// from four on a thread needs more than the 128 registers that sixteen waves leave
+// it (24 tokens 4096 -> 14336: NVFP4 spilled 39 registers and took 34.2 us, twelve
+// waves 21.9; MXFP4 18.3 and 17.9).
+constexpr int waves_at_most(int nt, int rt) { return nt * rt > 4 ? 64 / (nt * rt) : nt * rt == 4 ? 12 : kMaxWaves; }
 
 template <bool NV, int NT, int RT, bool Z>
-__global__ void __launch_bounds__(64 * waves_at_most(NT * RT)) gemv_kernel(MainArgs g) {
+__global__ void __launch_bounds__(64 * waves_at_most(NT, RT)) gemv_kernel(MainArgs g) {
   extern __shared__ float sums[];  // waves x RT x 16 NT columns x 16 rows
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all_waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const float *x, int64_t ldx,
 template <bool NV, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, int waves, hipStream_t stream) {
   const dim3 grid((unsigned)cdiv(Z ? rank_pad(g.w.rows) : g.w.rows, kRows * RT), Z ? kSlices : 1);
   const int low = Z ? 0 : (int)cdiv(g.rank, 32) * RT;
-  waves = std::min(waves, waves_at_most(NT * RT) - low) + low;
+  waves = std::min(waves, waves_at_most(NT, RT) - low) + low;
   gemv_kernel<NV, NT, RT, Z><<<grid, 64 * waves, (size_t)waves * RT * NT * 1024, stream>>>(g);
 }
 
