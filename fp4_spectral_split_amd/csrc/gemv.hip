@@ -39,9 +39,14 @@ constexpr int kMaxRank = 96;
 constexpr int kMaxWaves = 16, kHeldWaves = 12;
 constexpr int kSlices = 8;      // workgroups that share the columns of z's sums
 // From here on a workgroup takes 32 rows, which halves the reads of x and still
-// leaves a workgroup for each CU (32 tokens, rows by 16 and by 32: 4096 rows 7.7
-// and 9.7, 8192 11.1 and 10.8, 14336 21.7 and 18.6 us; 64 tokens, 8192 rows 19.4 and
-// 15.7, 14336 37.8 and 30.5 us).
+// leaves a workgroup for each CU (4096 columns, microseconds with rows by 16 and by 32:
+//                      MXFP4         NVFP4
+//   32 tokens,  4096   8.4   8.5     8.0   8.6 rows
+//               8192  11.9  10.3    11.1   9.3
+//              14336  22.1  19.5    22.7  20.4
+//   64 tokens,  4096  10.8  12.8    11.0  13.6
+//               8192  19.0  13.7    19.7  14.5
+//              14336  38.8  27.3    41.2  29.0).
 constexpr int kManyRows = 8192;
 
 struct Weight {  // an FP4 matrix of `rows` rows, blocks along its `cols` columns
@@ -116,12 +121,21 @@ __device__ __forceinline__ void load_codes(const Weight &w, int row0, int c, int
   }
 }
 
+// Lanes of a wave exchange through LDS: what they wrote comes before what any of
+// them reads from here on, and what they read before what is written. The LDS
+// keeps a wave's order; this holds the compiler to it. (It orders the loads
+// otherwise: 16 tokens 4096 -> 4096 5.4 to 5.6 us, 64 tokens 4096 -> 14336 30.1 to 27.4.)
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
 // Sixteen bytes from lane 4 r + q to lane 16 q + r, through a kilobyte of LDS
 // that is the wave's own (its accesses take place in order). The sixteen-byte
 // pieces of a row change places with r / 4, so that neither side meets a bank twice.
 __device__ __forceinline__ u32x4_a1 spread(const u32x4_a1 &v, uint8_t *mine, int lane) {
   const int r = lane & 15, q = lane >> 4;
+  wave_fence();
   *(intx4 *)(mine + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) * 16)) = __builtin_bit_cast(intx4, v);
+  wave_fence();
   return __builtin_bit_cast(u32x4_a1, *(const intx4 *)(mine + r * 64 + ((q ^ (r >> 2)) * 16)));
 }
 
@@ -432,7 +446,7 @@ __device__ __forceinline__ void columns(const MainArgs &g, int row0, int wave, i
 // Waves of a workgroup at most: the sums of each take NT RT kilobytes of LDS, and
 // from four on a thread needs more than the 128 registers that sixteen waves leave
 // it (24 tokens 4096 -> 14336: NVFP4 spilled 39 registers and took 34.2 us, twelve
-// waves 21.9; MXFP4 18.3 and 17.9).
+// waves 18.6; MXFP4, 64 tokens with rank 64, 53.6 and 48).
 constexpr int waves_at_most(int nt, int rt) { return nt * rt > 4 ? 64 / (nt * rt) : nt * rt == 4 ? 12 : kMaxWaves; }
 
 template <bool NV, int NT, int RT, bool Z>
