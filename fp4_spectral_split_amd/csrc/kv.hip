@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(64 * kWaves, NC <= 4 && PQ == 1 ? 4 : 2) atten
   const int j0 = (int)g.by_group.div((uint32_t)(tile * kRowsQ));
   const int j1 = min(count - 1, (int)g.by_group.div((uint32_t)(tile * kRowsQ + kRowsQ - 1)));
   const int hi = beyond ? 0 : max(0, length - new_tokens + j1 + 1);
-  const int first = (int)(g.window > 0 ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0);
+  const int first = (int)(g.window > 0 && !beyond ? max((int64_t)0, length - new_tokens + j0 + 1 - g.window) : 0);
   const int lo = first / kTile * kTile;
   // all of it, whatever the length that the launch was made for
   const int each = (max(hi - lo, 0) + g.splits - 1) / g.splits;

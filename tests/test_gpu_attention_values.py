@@ -215,3 +215,31 @@ def test_room_for_millions_of_sequences():
     want = M.metis_kv_attention(q, A.batch(table[:3], lengths[:3]), cache, need_lse=True)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("hint", [1, 1 << 20])
+def test_lengths_far_beyond_the_table_with_a_window(hint, page):
+    """Lengths up to 2^31 - 1 in a table of 40 places: NaN, with any window; the
+    sequences beside them keep their results."""
+    D, heads = 64, 4
+    g = H.rng(261)
+    lengths = np.array([2 ** 31 - 1, 40, 2 ** 31 - 33, 41, 2 ** 31 - 97, 2 ** 28 + 1], np.int32)
+    width = -(-40 // page)
+    cache, _ = _cache_of("mxfp4", g.standard_normal((width * page, D)), g.standard_normal((width * page, D)), page)
+    table = np.tile(g.permutation(width).astype(np.int32), (len(lengths), 1))
+    capacity = width * page
+    starts = [0, 3, 5, 6, 8, 9, 12]
+    q = A.dev(g.standard_normal((12, heads * D)), torch.float32)
+    for window in (0, 1, 16, 2 ** 31 - 1, 2 ** 40):
+        print("case beyond", page, hint, window, flush=True)
+        o, lse = M.metis_kv_attention(q, A.batch(table, lengths, starts, 3, hint), cache, window=window, need_lse=True)
+        torch.cuda.synchronize()
+        for s, length in enumerate(lengths):
+            rows = slice(starts[s], starts[s + 1])
+            if length > capacity:
+                assert bool(torch.isnan(o[rows]).all()) and bool(torch.isnan(lse[rows]).all()), (window, s)
+            else:
+                one = M.metis_kv_attention(q[rows], A.batch(table[s:s + 1], lengths[s:s + 1], [0, starts[s + 1] - starts[s]], 3, hint),
+                                           cache, window=window, need_lse=True)
+                assert torch.allclose(o[rows], one[0], rtol=1e-5, atol=1e-6) and torch.allclose(lse[rows], one[1], atol=1e-5)
