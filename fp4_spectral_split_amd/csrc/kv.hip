@@ -989,7 +989,7 @@ extern "C" metis_status_t metis_kv_attention(const void *q, metis_dtype_t dt, in
   g.chunk = p.s.chunk;
   g.max_new = max_new;
   g.scale = scale * 1.44269504f;
-  g.window = window;
+  g.window = std::min(window, kMaxTokens);  // no sequence has more; a position less a window stays in range
   g.o = o;
   g.ldo = ldo;
   g.o_bf16 = odt == METIS_BF16;

@@ -243,3 +243,24 @@ def test_lengths_far_beyond_the_table_with_a_window(hint, page):
                 one = M.metis_kv_attention(q[rows], A.batch(table[s:s + 1], lengths[s:s + 1], [0, starts[s + 1] - starts[s]], 3, hint),
                                            cache, window=window, need_lse=True)
                 assert torch.allclose(o[rows], one[0], rtol=1e-5, atol=1e-6) and torch.allclose(lse[rows], one[1], atol=1e-5)
+
+
+def test_windows_up_to_the_largest_number():
+    """Windows no shorter than any sequence are none, up to 2^63 - 1, also for
+    sequences with more new tokens than their length, whose first ones have
+    negative positions: the same bits."""
+    D, heads, page = 64, 4, 16
+    g = H.rng(271)
+    cache, _ = _cache_of("nvfp4", g.standard_normal((8 * page, D)), g.standard_normal((8 * page, D)), page)
+    table = g.permutation(8).astype(np.int32).reshape(2, 4)
+    starts, lengths = [0, 50, 60], [7, 64]
+    q = A.dev(g.standard_normal((60, heads * D)), torch.float32)
+    for hint in (1, None):
+        b = A.batch(table, lengths, starts, 50, hint)
+        want = M.metis_kv_attention(q, b, cache, need_lse=True)
+        for window in (64, 2 ** 28, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
+            print("case window", hint, window, flush=True)
+            got = M.metis_kv_attention(q, b, cache, window=window, need_lse=True)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert not got[0][:43].any() and bool(torch.isneginf(got[1][:43]).all()) and bool(got[0][43:].any(dim=1).all())
