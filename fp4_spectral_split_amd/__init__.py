@@ -1198,6 +1198,11 @@ def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=No
     ldq, heads = _heads(q, "q", cache.head_dim)
     dev, tokens, dt = q.device, q.shape[0], _code(q.dtype)
     b = _batch(batch, dev)
+    max_new = batch.max_new
+    if max_new < 1:
+        raise MetisError("max_new must be at least 1, got %r" % (max_new,))
+    if batch.starts is not None:  # a bound beyond the call's tokens says no more than these
+        max_new = min(max_new, max(tokens, 1))
     if cache.heads < 1 or heads % cache.heads:
         raise MetisError("%d query heads over %d heads in the cache" % (heads, cache.heads))
     dtype = q.dtype if dtype is None else dtype
@@ -1212,10 +1217,10 @@ def metis_kv_attention(q, batch, cache, scale=None, window=0, dtype=None, out=No
         if not every:
             lse.fill_(float("-inf"))
     longest = max(1, int(batch.max_length) if batch.max_length is not None else b.max_pages * cache.page_size)
-    nws = _attention_workspace(tokens, heads, batch.max_new, longest, b.seqs, b.max_pages, batch.starts is not None,
+    nws = _attention_workspace(tokens, heads, max_new, longest, b.seqs, b.max_pages, batch.starts is not None,
                                cache.pages, cache.page_size, cache.heads, c.k.fmt, cache.head_dim)
     ws = q.new_empty(nws, dtype=torch.uint8) if nws else None  # of its own per call, as in metis_norm_bwd
-    _run(dev, load().metis_kv_attention, q.data_ptr(), dt, tokens, ldq, heads, b, c, batch.max_new, longest,
+    _run(dev, load().metis_kv_attention, q.data_ptr(), dt, tokens, ldq, heads, b, c, max_new, longest,
          cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), odt, ldo,
          None if lse is None else lse.data_ptr(), ws.data_ptr() if nws else None, nws)
     return out, lse

@@ -264,3 +264,21 @@ def test_windows_up_to_the_largest_number():
             torch.cuda.synchronize()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert not got[0][:43].any() and bool(torch.isneginf(got[1][:43]).all()) and bool(got[0][43:].any(dim=1).all())
+
+
+def test_a_bound_of_new_tokens_beyond_32_bits():
+    """max_new is an upper bound: any number of at least the most new tokens."""
+    D, heads, page = 64, 4, 16
+    g = H.rng(281)
+    cache, _ = _cache_of("mxfp4", g.standard_normal((8 * page, D)), g.standard_normal((8 * page, D)), page)
+    table = g.permutation(8).astype(np.int32).reshape(2, 4)
+    q = A.dev(g.standard_normal((12, heads * D)), torch.bfloat16)
+    call = lambda n: M.metis_kv_attention(q, A.batch(table, [40, 64], [0, 9, 12], n), cache)[0]  # noqa: E731
+    want = call(9)
+    for bound in (12, 2 ** 31, 2 ** 32 + 1, 2 ** 63 - 1):
+        got = call(bound)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), bound
+    for bound in (0, -1, 1 - 2 ** 32):
+        with pytest.raises(M.MetisError):
+            call(bound)
