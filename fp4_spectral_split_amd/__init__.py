@@ -1084,6 +1084,8 @@ class KvCache:
             raise MetisError("FP4 format must be mxfp4 or nvfp4, got %r" % (fmt,))
         if (f == NVFP4) != (k_scale is not None) or (f == NVFP4) != (v_scale is not None):
             raise MetisError("k_scale and v_scale belong to nvfp4, and to it alone")
+        if f == NVFP4 and not all(2.0 ** -126 <= float(s) < 2.0 ** 128 for s in (k_scale, v_scale)):
+            raise MetisError("k_scale and v_scale must be positive normal numbers, got %r and %r" % (k_scale, v_scale))
         if min(pages, page_size, heads, head_dim) < 1 or head_dim % 32:
             raise MetisError("a cache needs pages of at least one place and heads of a multiple of 32")
         rows = pages * heads * page_size

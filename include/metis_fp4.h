@@ -527,8 +527,8 @@ metis_status_t metis_fp4_gemv(const void *x, metis_dtype_t dt, int64_t tokens, i
  *  head_dim: a multiple of 32, at most 256 (beyond: METIS_ERR_UNSUPPORTED), in
  *      both formats; at most 2^31 - 1 rows. page_size may be any number >= 1.
  *  NVFP4: the tensor scales are the caller's and are read only: tensor_scale
- *      of k and v has to be set before anything is stored (largest magnitude
- *      expected / 2688); larger values saturate. */
+ *      of k and v has to be set to a positive normal number before anything is
+ *      stored (largest magnitude expected / 2688); larger values saturate. */
 typedef struct {
   int64_t pages;
   int32_t page_size, heads;
