@@ -1115,9 +1115,6 @@ class KvCache:
     def head_dim(self):
         return self.k.cols
 
-    def c(self):
-        return _KvCache(self.pages, self.page_size, self.heads, self.k.c(), self.v.c())
-
 
 @dataclass
 class KvBatch:
