@@ -1171,7 +1171,7 @@ def metis_kv_append(k, v, batch, cache, rope=None, pairs="halves"):
     is given, see metis_qk_norm_rope_fwd) and values in the cache, quantized as
     fp4_block_quant does; returns the cache. k, v: tokens x (heads * head_dim)
     fp32/bf16 CUDA tensors of one type. Tokens outside the batch, its table or
-    the rope are not stored; pages written to belong to one sequence each."""
+    the rope are not stored; a page written to stands once in the table."""
     ldk = _matrix(k, "k")
     dev, dt = k.device, _code(k.dtype)
     c, b = _cache(cache, k.get_device()), _batch(batch, dev)

@@ -488,7 +488,9 @@ metis_status_t metis_qk_norm_rope_fwd(const void *q, int64_t ldq, int32_t q_head
  *          tokens they are zero (stored) or kept (added).
  *  ws:     metis_qk_norm_rope_bwd_workspace_bytes() bytes, 256-byte aligned;
  *          may be NULL without dwq and dwk.
- * Sums run in a fixed order: bitwise reproducible. */
+ *  tokens times half the heads of q or k, rounded up, has to be below 2^29
+ *  (beyond: METIS_ERR_UNSUPPORTED; parts of the tokens can be added up with
+ *  accumulate). Sums run in a fixed order: bitwise reproducible. */
 size_t metis_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim);
 metis_status_t metis_qk_norm_rope_bwd(const void *dq, int64_t lddq, const void *dk, int64_t lddk, metis_dtype_t dydt,
                                       const void *q, int64_t ldq, int32_t q_heads, const void *k, int64_t ldk,
@@ -564,8 +566,9 @@ typedef struct {
  * Each row of a head is then quantized as fp4_block_quant does with the
  * cache's tensor scale. A row that belongs to no sequence, and a token whose
  * position is outside the table or the rope, or whose page is outside
- * [0, pages), is not stored; nothing else in the cache changes. Pages that a
- * call writes to have to belong to one sequence each. */
+ * [0, pages), is not stored; nothing else in the cache changes. A page that a
+ * call writes to may stand only once in the tables: in one sequence's, in one
+ * place of it. */
 metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, metis_dtype_t dt,
                                int64_t tokens, const metis_kv_batch_t *batch, const float *rope, int64_t rope_rows,
                                int32_t rot_dim, metis_rope_t pairs, const metis_kv_cache_t *cache, hipStream_t stream);
