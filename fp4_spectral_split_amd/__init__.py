@@ -1122,9 +1122,10 @@ class KvBatch:
     sequences x pages, each sequence's pages in order. lengths: int32, tokens
     of each sequence with its new ones (0: not in use). starts: int32, one more
     than sequences, not decreasing: sequence s has the rows starts[s] ..
-    starts[s + 1] - 1; None: row s belongs to sequence s. max_new: at least the most new tokens of
-    any sequence. max_length: about the largest length (default: what the table
-    holds), which attention divides its work by."""
+    starts[s + 1] - 1; None: row s belongs to sequence s. max_new: at least the
+    most new tokens of any sequence. max_length: about the most tokens that a
+    query sees, the largest length or a window (default: what the table holds),
+    which attention divides its work by: the nearer, the faster."""
     table: torch.Tensor
     lengths: torch.Tensor
     starts: Optional[torch.Tensor] = None

@@ -15,11 +15,12 @@
 // fp32 x enters as three bf16 parts (exact), each a column of the products of
 // its own, z likewise; these and z come from launches of their own ahead of the
 // main one. Without those, MXFP4, codes not in any cache: 1 token 4096 -> 4096
-// 5.1 us, 4096 -> 14336 11.3 us (2.8 TB/s), 4096 -> 28672 17.8 us (3.5 TB/s); 16
-// tokens 5.4, 11.0 and 16.4 us. (Only reading the 31 MB of 4096 -> 14336 takes
-// 7.0 us.) What is lost is the start: a workgroup's first codes are on their way
-// for 2 to 3 us of the time. Beyond 16 columns of the products x has its share:
-// each workgroup reads all of it from the L2 (64 tokens 4096 -> 14336 30.5 us).
+// 5.1 us, 4096 -> 14336 11.4 us (2.7 TB/s), 4096 -> 28672 16.9 us (3.7 TB/s); 16
+// tokens 5.7, 11.7 and 16.1 us; NVFP4 5.5, 12.3, 17.8 and 5.8, 13.2, 18.7. (Only
+// reading the 31 MB of 4096 -> 14336 takes 7.0 us.) What is lost is the start: a
+// workgroup's first codes are on their way for 2 to 3 us of the time. Beyond a few
+// columns of the products x has its share: each workgroup reads all of it from the
+// L2 (64 tokens 4096 -> 14336, 235 MB: 27.3 us; five of fp32, 14336 -> 4096, 110 MB).
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +34,7 @@ namespace {
 constexpr int kRows = 16;       // rows of W in a workgroup
 constexpr int kStep = 128;      // columns of a wave's step
 // Workgroups that take several tiles of rows, one for each CU (16 tokens
-// 4096 -> 14336: 128 workgroups 16.1, 256 11.8, 512 13.8, one for each tile 18.4 us).
+// 4096 -> 14336: 128 workgroups 16.2, 256 11.7, 512 13.5, one for each tile 18.1 us).
 constexpr int kHeldGrid = 256;
 constexpr int kMaxRank = 96;
 constexpr int kMaxWaves = 16, kHeldWaves = 12;
@@ -240,7 +241,7 @@ template <bool JOINED> __device__ __forceinline__ void load_z(const MainArgs &g,
 
 // Beyond 32 columns of the products z is joined once: 64 tokens read eight slices
 // of it, at rank 64 a quarter of x itself, in each of the workgroups (4096 -> 14336
-// 68.4 us, so 52.8).
+// 51.2 us, so 48.3; with the few workgroups of 4096 -> 4096 18.1, so 19.7).
 __global__ void __launch_bounds__(256) join_z_kernel(const float *z, const float *s, int rank, int tokens,
                                                      unsigned short *out) {
   const int pad = rank_pad(rank), at = (blockIdx.x * 256 + threadIdx.x) * 8;
@@ -518,7 +519,7 @@ template <bool NV, int NT, int RT, bool Z> void launch_rows(const MainArgs &g, i
 template <bool NV> void launch(MainArgs g, hipStream_t stream) {
   const int n = g.columns(), cols = g.w.cols, steps = (int)cdiv(cols, kStep), low = (int)cdiv(g.rank, 32);
   // x held in registers pays where a workgroup has several tiles (16 tokens
-  // 4096 -> 14336 11.0 us, else 14.3; 4096 -> 4096 6.1, else 5.4)
+  // 4096 -> 14336 11.7 us, else 12.8; 4096 -> 4096 6.2, else 5.8)
   if (n <= 16 && steps <= 32 && g.w.rows > kHeldGrid * kRows) {
     const int s = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, waves = std::max(1, (int)cdiv(steps, s));
     g.tiles = (int)cdiv(g.w.rows, kRows);

@@ -32,12 +32,15 @@
 // both products' operands are decoded; the loads take the time of the softmax and
 // of the second product, and the table entries of the 32 after them are under way.
 // 64 sequences of 64 to 8192 tokens (281 MB of MXFP4 codes, 8 heads of 128, 4 query
-// heads to each): 70 us, 4.0 TB/s; 128 sequences of 2048 tokens, which need no
-// join, 4.5 to 5.5 TB/s. Only reading such pages takes 49 us (5.8 TB/s), so what is lost
-// is the end, where workgroups of unequal work leave CUs idle, and the start of
-// each. Two sets of code registers (q then has to lie in LDS) took 72 us, rows of v
-// in LDS that no two of a transposed read's lanes meet a bank with 70 us, 32 query
-// rows to a pass (5 sequences of 26000 tokens with 6 new ones) 38.6 against 35.0 us.
+// heads to each): 72.5 us, 3.9 TB/s (NVFP4, 298 MB: 89 us with the join); 128 sequences of 2048
+// tokens, which need no join, 58 us (4.9 TB/s). Only reading such pages takes 49 us
+// (5.8 TB/s), so what is lost is the end, where workgroups of unequal work leave CUs
+// idle, the start of each, and instructions: the weights' third part alone is 4 us.
+// With weights of two parts, 70 us then, two sets of code registers (q then has to
+// lie in LDS) took 72 us, rows of v in LDS that no two of a transposed read's lanes
+// meet a bank with 70 us, 32 query rows to a pass (5 sequences of 26000 tokens with
+// 6 new ones) 38.6 against 35.0 us. Sixteen query rows decode all codes that they
+// see: a prompt of 2048 tokens takes 108 us (NVFP4 140), its operations 28.
 #include <algorithm>
 
 #include "decode4.hpp"
@@ -269,7 +272,7 @@ constexpr int kRowsQ = 16;
 constexpr int kMaxSplits = 256;  // a thread of the join for each
 // bf16 parts of a weight of the softmax: all 24 bits. Two parts hold 16 (2^-17), of
 // which a result that is small beside sum p |v| shows up to its leading bits; the
-// third takes 3 to 7% of the time (64 sequences of 64 to 8192 tokens 73.7 to 77.3 us,
+// third takes 3 to 7% of the time (64 sequences of 64 to 8192 tokens 68.9 to 72.5 us,
 // 128 of 2048 54.5 to 57.3).
 constexpr int kWeightParts = 3;
 
@@ -774,7 +777,8 @@ void batch_in(Operands &o, const metis_kv_batch_t *b) {
 // Tokens of a workgroup: as many as leave `kTarget` workgroups, had every
 // sequence the largest length, in whole steps of its waves. 1024 of them are on
 // the GPU at once, and best where lengths are equal; 1.5 times as many leave
-// about that where they are not. Microseconds, heads of 128, 32 query heads on 8:
+// about that where they are not. Microseconds, heads of 128, 32 query heads on 8
+// (with weights of two parts; all a few percent less than with three):
 //   workgroups                          1024  1536  2048  4096
 //   64 sequences of 64 to 8192 tokens     86    70    75    74
 //   64 of 4096                          65.7  62.3  65.8  68.8

@@ -589,9 +589,10 @@ metis_status_t metis_kv_append(const void *k, int64_t ldk, const void *v, int64_
  *          where nothing is seen (to join with attention over other tokens).
  *  max_new: an upper bound of the new tokens of any sequence (1 without
  *          starts); those beyond it are left as they were.
- *  max_length: about the largest length, which the work is divided by (any
- *          value >= 1 gives the same result but for rounding; the true one the
- *          best speed). The lengths themselves stay on the device.
+ *  max_length: about the most tokens that a query sees, the largest length or
+ *          with a window the window, which the work is divided by (any value
+ *          >= 1 gives the same result but for rounding; the true one the best
+ *          speed). The lengths themselves stay on the device.
  *  ws:     metis_kv_attention_workspace_bytes() bytes, 256-byte aligned.
  * Queries and keys enter the products as they are (fp32 queries as three bf16
  * parts), the weights exp(score - max) as three bf16 parts, all of their bits;
