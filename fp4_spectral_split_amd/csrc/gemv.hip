@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(64 * waves_at_most(NT, RT)) gemv_kernel(MainAr
     }
   } else {
     columns<NV, NT, RT, Z>(g, row0, wave, waves, lane, (uint8_t *)(sums + wave * RT * NT * 256), acc);
+    wave_fence();  // the sums take the place of the pieces
   }
 #pragma unroll
   for (int t = 0; t < RT; ++t)
